@@ -485,8 +485,6 @@ def _own_state(s):
         o["kept"] = torch.empty(B, hkv, s["budget"], dtype=torch.int32, device="cuda")
         o["lens"] = torch.empty(B, dtype=torch.int32, device="cuda")
         o["kb"], o["vb"] = values(s["budget"]), values(s["budget"])
-        n = capi.dflash_kvq_evict_workspace(B, hkv, s["max_keys"], s["budget"])
-        o["ws"] = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
     s["own"] = o
     return o
 
@@ -511,7 +509,7 @@ def _run_own(s):
                               s["score_in"], o["out"])
         return o["out"]
     capi.dflash_kvq_evict(cache, B, s["src"], s["dst"], s["kv_lens"], s["max_keys"], s["budget"],
-                          s["window"], s["score"], o["kept"], o["lens"], o["ws"])
+                          s["window"], s["score"], o["kept"], o["lens"])
     capi.dflash_kvq_read(cache, B, s["budget"], s["dst"], None, o["lens"], o["kb"], o["vb"])
     return o["kept"], o["lens"], s["score"][B:], o["kb"], o["vb"]
 
