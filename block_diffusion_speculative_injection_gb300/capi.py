@@ -55,8 +55,18 @@ class DTree(ctypes.Structure):
     ]
 
 
+class _KvqCacheStruct(ctypes.Structure):
+    _fields_ = [
+        ("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+        ("v_exp", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _SIGS = {
     "dflash_create": ([ctypes.POINTER(Config), ctypes.POINTER(_P)], _I),
     "dflash_set_weight": ([_P, ctypes.c_char_p, _P, _I, ctypes.POINTER(ctypes.c_int64), _I], _I),
@@ -95,6 +105,15 @@ _SIGS = {
     "dflash_spec_accept_workspace": ([_I, _I, _I], ctypes.c_int64),
     "dflash_spec_accept_sampled": ([_I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P],
                                    _I),
+    "dflash_kvq_append": ([_P, _I, _I, _P, _P, _P, _P, _P, _L, _L, _P], _I),
+    "dflash_kvq_read": ([_P, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "dflash_kvq_attention": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _L, _P, _P, _P, _L,
+                              _P], _I),
+    "dflash_kvq_attention_workspace": ([_I, _I, _I, _I, _I], _L),
+    "dflash_kvq_score": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _L, _P, ctypes.c_float, _P,
+                          _P, _P], _I),
+    "dflash_kvq_evict": ([_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P], _I),
+    "dflash_kvq_check": ([_P, _P], _I),
     "dflash_plan_gemm": ([_I, _I, _I, _I, _I, _I, _P], _I),
     "dflash_plan_attention": ([_I, _I, _I, _I, _I, ctypes.c_int64, _I, _P], _I),
     "dflash_profile": ([_P, _I], _I),
@@ -420,6 +439,156 @@ def dflash_spec_accept_sampled(batch, block, vocab, draft_logits, target_logits,
                                            _stream(stream))
     if st != 0:
         raise DFlashError(st, "dflash_spec_accept_sampled")
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit KV cache (dflash_kvq_*)
+# ---------------------------------------------------------------------------
+MASK_NONE, MASK_CAUSAL, MASK_TREE = 0, 1, 2
+
+
+def _kvq_need(ok: bool, what: str) -> None:
+    if not ok:
+        raise DFlashError(1, what)
+
+
+def _kvq_dense(t, name: str, dtype: str, shape) -> None:
+    """A contiguous tensor of one of these dtypes and this shape (None passes)."""
+    if t is None:
+        return
+    _kvq_need(str(t.dtype)[6:] in dtype.split("|") and tuple(t.shape) == tuple(shape)
+              and t.is_contiguous(),
+              f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _kvq_rows(t, name: str, batch: int, rows: int, heads: int) -> int:
+    """Elements between the rows of a bf16 [batch][rows][heads][128] tensor
+    whose rows may be slices of wider ones."""
+    _kvq_need(str(t.dtype) == "torch.bfloat16" and tuple(t.shape) == (batch, rows, heads, 128),
+              f"{name}: need bfloat16 of shape {(batch, rows, heads, 128)}")
+    sb, sr, sh, sd = t.stride()
+    if rows == 1:
+        sr = sb if batch > 1 else heads * 128
+    _kvq_need(sd == 1 and (sh == 128 or heads == 1) and (sb == rows * sr or batch == 1),
+              f"{name}: rows of {heads} * 128 elements, equally spaced, are needed")
+    return sr
+
+
+class KvqCache:
+    """An 8-bit KV cache over tensors the caller owns (and this keeps alive):
+    k8, v8 [n_pages][n_kv_heads][128][128] uint8 or float8_e4m3fn, k_exp, v_exp
+    [n_pages][n_kv_heads][8] int8, page_table [n_seqs][pages_per_seq] int32,
+    status [1] int32 (zero at the start)."""
+
+    def __init__(self, k8, v8, k_exp, v_exp, page_table, status):
+        n_pages, heads = k8.shape[0], k8.shape[1]
+        for t, name in ((k8, "k8"), (v8, "v8")):
+            _kvq_dense(t, name, "uint8|float8_e4m3fn", (n_pages, heads, PAGE_SLOTS, 128))
+        for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            _kvq_dense(t, name, "int8", (n_pages, heads, PAGE_SLOTS // 16))
+        _kvq_need(page_table.dim() == 2, "page_table: need [n_seqs][pages_per_seq]")
+        _kvq_dense(page_table, "page_table", "int32", page_table.shape)
+        _kvq_dense(status, "status", "int32", (1,))
+        self.tensors = (k8, v8, k_exp, v_exp, page_table, status)
+        self.n_kv_heads = heads
+        self.n_seqs, self.pages_per_seq = page_table.shape
+        self.slots = self.pages_per_seq * PAGE_SLOTS
+        self._struct = _KvqCacheStruct(*[_ptr(t) for t in self.tensors], n_pages, heads,
+                                       self.n_seqs, self.pages_per_seq)
+        self.ref = ctypes.addressof(self._struct)
+
+
+def _kvq_check(status: int, name: str) -> None:
+    if status != 0:
+        raise DFlashError(status, name)
+
+
+def dflash_kvq_append(cache: KvqCache, batch, rows, seq_ids, start, counts, k, v,
+                      stream=None) -> None:
+    """Writes bf16 rows k, v [batch][rows][n_kv_heads][128] (rows may be slices
+    of wider ones) to slots start[b] .. start[b] + counts[b] - 1."""
+    for t, name in ((seq_ids, "seq_ids"), (start, "start"), (counts, "counts")):
+        _kvq_dense(t, name, "int32", (batch,))
+    ks = _kvq_rows(k, "k", batch, rows, cache.n_kv_heads)
+    vs = _kvq_rows(v, "v", batch, rows, cache.n_kv_heads)
+    _kvq_check(load().dflash_kvq_append(cache.ref, batch, rows, _ptr(seq_ids), _ptr(start),
+                                        _ptr(counts), _ptr(k), _ptr(v), ks, vs, _stream(stream)),
+               "dflash_kvq_append")
+
+
+def dflash_kvq_read(cache: KvqCache, batch, rows, seq_ids, start, counts, k_out, v_out,
+                    stream=None) -> None:
+    """Values of slots start[b] + j, j < counts[b], as bf16 [batch][rows][n_kv_heads][128]."""
+    for t, name in ((seq_ids, "seq_ids"), (start, "start"), (counts, "counts")):
+        _kvq_dense(t, name, "int32", (batch,))
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _kvq_dense(t, name, "bfloat16", (batch, rows, cache.n_kv_heads, 128))
+    _kvq_check(load().dflash_kvq_read(cache.ref, batch, rows, _ptr(seq_ids), _ptr(start),
+                                      _ptr(counts), _ptr(k_out), _ptr(v_out), _stream(stream)),
+               "dflash_kvq_read")
+
+
+def _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q):
+    for t, name in ((seq_ids, "seq_ids"), (kv_lens, "kv_lens"), (q_lens, "q_lens")):
+        _kvq_dense(t, name, "int32", (batch,))
+    words = 0
+    if mask == MASK_TREE:
+        _kvq_need(anc is not None and anc.dim() == 3, "anc: need [batch][block][words]")
+        words = anc.shape[2]
+        _kvq_dense(anc, "anc", "int64|uint64", (batch, block, words))
+    return words, _kvq_rows(q, "q", batch, block, n_heads)
+
+
+def dflash_kvq_attention_workspace(batch, n_heads, n_kv_heads, block, max_keys) -> int:
+    return int(load().dflash_kvq_attention_workspace(batch, n_heads, n_kv_heads, block, max_keys))
+
+
+def dflash_kvq_attention(cache: KvqCache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens,
+                         anc, max_keys, q, out, lse=None, workspace=None, stream=None) -> None:
+    """Attention of q [batch][block][n_heads][128] (rows may be slices of wider
+    ones) over the cache: out of that shape, lse [batch][block][n_heads]."""
+    words, qs = _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q)
+    _kvq_dense(out, "out", "bfloat16", (batch, block, n_heads, 128))
+    _kvq_dense(lse, "lse", "float32", (batch, block, n_heads))
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _kvq_check(load().dflash_kvq_attention(cache.ref, batch, n_heads, block, mask, _ptr(seq_ids),
+                                           _ptr(kv_lens), _ptr(q_lens), _ptr(anc), words, max_keys,
+                                           _ptr(q), qs, _ptr(out), _ptr(lse), _ptr(workspace),
+                                           nbytes, _stream(stream)), "dflash_kvq_attention")
+
+
+def dflash_kvq_score(cache: KvqCache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc,
+                     max_keys, q, lse, decay, score_in, score_out, stream=None) -> None:
+    """score_out = decay * score_in + the weights each slot received; scores
+    [n_seqs][n_kv_heads][pages_per_seq * 128] (score_in None: zero)."""
+    words, qs = _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q)
+    _kvq_dense(lse, "lse", "float32", (batch, block, n_heads))
+    for t, name in ((score_in, "score_in"), (score_out, "score_out")):
+        _kvq_dense(t, name, "float32", (cache.n_seqs, cache.n_kv_heads, cache.slots))
+    _kvq_check(load().dflash_kvq_score(cache.ref, batch, n_heads, block, mask, _ptr(seq_ids),
+                                       _ptr(kv_lens), _ptr(q_lens), _ptr(anc), words, max_keys,
+                                       _ptr(q), qs, _ptr(lse), decay, _ptr(score_in),
+                                       _ptr(score_out), _stream(stream)), "dflash_kvq_score")
+
+
+def dflash_kvq_evict(cache: KvqCache, batch, src_ids, dst_ids, kv_lens, max_keys, budget, window,
+                     score, kept, new_lens, stream=None) -> None:
+    """Keeps the last `window` slots and the best-scored others of sequences
+    src_ids, `budget` in all, in the pages of sequences dst_ids."""
+    for t, name in ((src_ids, "src_ids"), (dst_ids, "dst_ids"), (kv_lens, "kv_lens"),
+                    (new_lens, "new_lens")):
+        _kvq_dense(t, name, "int32", (batch,))
+    _kvq_dense(score, "score", "float32", (cache.n_seqs, cache.n_kv_heads, cache.slots))
+    _kvq_dense(kept, "kept", "int32", (batch, cache.n_kv_heads, budget))
+    _kvq_check(load().dflash_kvq_evict(cache.ref, batch, _ptr(src_ids), _ptr(dst_ids),
+                                       _ptr(kv_lens), max_keys, budget, window, _ptr(score),
+                                       _ptr(kept), _ptr(new_lens), _stream(stream)),
+               "dflash_kvq_evict")
+
+
+def dflash_kvq_check(cache: KvqCache, stream=None) -> None:
+    """Waits for the stream, clears the cache's status word and raises if it was set."""
+    _kvq_check(load().dflash_kvq_check(cache.ref, _stream(stream)), "dflash_kvq_check")
 
 
 def dflash_debug_trace(ctx, dst=None) -> None:

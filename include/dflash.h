@@ -439,6 +439,156 @@ DFLASH_API dflash_status dflash_block_attention_noalloc(int32_t batch, int32_t n
                                                         const void *v_dev, void *out_dev,
                                                         dflash_stream_t stream);
 
+/* ---- KV cache held in 8 bits (no context) ---------------------------------
+ * A paged cache at half the bytes of the bf16 one, for serving many or long
+ * sequences: the caller owns its memory, and maps pages with the allocator
+ * dflash_kv_pool_* (or any other).  The pages give no quantised cache; the
+ * format is the library's own.  head_dim is 128.
+ *   k8, v8        [n_pages][n_kv_heads][DFLASH_PAGE_SLOTS][128] e4m3 codes
+ *   k_exp, v_exp  [n_pages][n_kv_heads][DFLASH_PAGE_SLOTS / 16] int8: one
+ *                 exponent for each 16 slots of a head; value = code * 2^exp
+ *   page_table    [n_seqs][pages_per_seq] int32 page ids (-1: unmapped): slot s
+ *                 of sequence q is row s % DFLASH_PAGE_SLOTS of page
+ *                 page_table[q][s / DFLASH_PAGE_SLOTS]
+ *   status        one int32, zero at the start: the first failure a kernel met
+ *                 (dflash_kvq_check reads and clears it)
+ * All pointers are device memory of the device that is current at the call
+ * (any other pointer: DFLASH_E_INVALID_ARG): k8 and v8 16-byte aligned, k_exp
+ * and v_exp 8-byte aligned, n_pages * n_kv_heads * 128 < 2^31.
+ * The exponent of a block of 16 slots is the smallest e in [-40, 40] with
+ * max |x| <= 448 * 2^e over its rows, codes are rounded to nearest even.  A
+ * power of two makes scaling exact: a code is off by at most 2^-4 of its value
+ * (half a step), or 2^(e - 10) where that is more.  Magnitudes above 448 * 2^40
+ * saturate.  A non-finite element is stored as the code of NaN.
+ * Calls only enqueue work on `stream` and keep nothing between calls, so they
+ * may be captured and run on several streams; calls that write the same slots,
+ * scores or outputs must be ordered by the caller, and one call must not name a
+ * sequence twice where it writes.
+ * batch entry b is sequence seq_ids[b] (seq_ids NULL: b); an id outside
+ * [0, n_seqs), a negative length or a count outside [0, rows] (q_lens: [0,
+ * block]) skips that entry and sets the status DFLASH_E_DEVICE_CHECK; a slot whose page is not mapped (or past
+ * pages_per_seq) sets DFLASH_E_CAPACITY. */
+typedef struct {
+  void *k8_dev, *v8_dev;
+  int8_t *k_exp_dev, *v_exp_dev;
+  const int32_t *page_table_dev;
+  int32_t *status_dev;
+  int32_t n_pages, n_kv_heads, n_seqs, pages_per_seq;
+} dflash_kvq_cache;
+
+/* Which of the cache's slots a query row sees (dflash_kvq_attention / _score).
+ * A sequence has n = kv_lens[b] slots; its r = q_lens[b] rows are its last r
+ * slots, so row j sits at slot n - r + j. */
+enum {
+  DFLASH_MASK_NONE = 0,   /* every slot < n */
+  DFLASH_MASK_CAUSAL = 1, /* slots <= n - r + j */
+  DFLASH_MASK_TREE = 2    /* slots < n - r, and n - r + i where bit i of anc[b][j] is set */
+};
+
+/* Writes rows j < counts[b] (NULL: rows) of K and V to slots start[b] + j.  The
+ * slots before start[b] are the committed ones: where they share a block of 16
+ * with new rows, the block's exponent covers both and they are recoded (exact
+ * but for values below the smallest normal code of the new exponent).  Slots
+ * from start[b] on count as empty, so a rejected draft is rolled back by
+ * length, as in the bf16 cache.  Rows of slots without a mapped page are
+ * dropped (status DFLASH_E_CAPACITY).
+ *   k_dev, v_dev  [batch][rows] rows of n_kv_heads * 128 bf16, row_stride
+ *                 elements apart (>= n_kv_heads * 128, a multiple of 8: a slice
+ *                 of a fused projection's output), 16-byte aligned
+ *   start_dev [batch], counts_dev [batch] or NULL */
+DFLASH_API dflash_status dflash_kvq_append(const dflash_kvq_cache *cache, int32_t batch,
+                                           int32_t rows, const int32_t *seq_ids_dev,
+                                           const int32_t *start_dev, const int32_t *counts_dev,
+                                           const void *k_dev, const void *v_dev,
+                                           int64_t k_row_stride, int64_t v_row_stride,
+                                           dflash_stream_t stream);
+
+/* The values of slots start[b] + j, j < counts[b] (start NULL: 0, counts NULL:
+ * rows), as bf16 (exact) to k_out / v_out [batch][rows][n_kv_heads][128]; either
+ * may be NULL.  Rows past counts[b] are left as they were; slots without a
+ * mapped page read as zero (status DFLASH_E_CAPACITY). */
+DFLASH_API dflash_status dflash_kvq_read(const dflash_kvq_cache *cache, int32_t batch, int32_t rows,
+                                         const int32_t *seq_ids_dev, const int32_t *start_dev,
+                                         const int32_t *counts_dev, void *k_out_dev,
+                                         void *v_out_dev, dflash_stream_t stream);
+
+/* Attention over the 8-bit cache: row j < q_lens[b] (NULL: block) of sequence b,
+ * query head h (KV head h / (n_heads / n_kv_heads)) gets
+ *   out = sum_s p_s v_s,  p = softmax over the slots it sees of q . k_s / sqrt(128).
+ * The rows' own K/V are in the cache already (dflash_kvq_append).  A row that
+ * sees no slot gets zeros (lse -inf).  Slots on unmapped pages count as not seen
+ * (status DFLASH_E_CAPACITY).  Rows past q_lens[b] are left as they were.  What
+ * a row does not see (other rows' slots, whatever lies behind slot n) does not
+ * enter its result, NaN included.
+ *   q_dev    [batch][block] rows of n_heads * 128 bf16, q_row_stride elements
+ *            apart (>= n_heads * 128, a multiple of 8), 16-byte aligned
+ *   out_dev  [batch][block][n_heads][128] bf16, 16-byte aligned
+ *   lse_dev  [batch][block][n_heads] float or NULL: natural log of the sum of
+ *            exp(q . k_s / sqrt(128))
+ *   anc_dev  [batch][block][anc_words] uint64 (mask TREE; else ignored)
+ *   max_keys host bound on the lengths, for planning only (any value >= 1 gives
+ *            right results; 1..2^29)
+ *   workspace_dev  split-KV partials, 16-byte aligned: at least
+ *            dflash_kvq_attention_workspace(...) bytes, or NULL / 0 to run
+ *            without splitting; two calls that overlap need one each
+ * n_heads / n_kv_heads 1..64. */
+DFLASH_API dflash_status dflash_kvq_attention(
+    const dflash_kvq_cache *cache, int32_t batch, int32_t n_heads, int32_t block, int32_t mask,
+    const int32_t *seq_ids_dev, const int32_t *kv_lens_dev, const int32_t *q_lens_dev,
+    const uint64_t *anc_dev, int32_t anc_words, int32_t max_keys, const void *q_dev,
+    int64_t q_row_stride, void *out_dev, float *lse_dev, void *workspace_dev,
+    int64_t workspace_bytes, dflash_stream_t stream);
+
+/* Bytes of workspace dflash_kvq_attention uses for these sizes on the current
+ * device (0: no split needed; -1: unsupported sizes). */
+DFLASH_API int64_t dflash_kvq_attention_workspace(int32_t batch, int32_t n_heads,
+                                                  int32_t n_kv_heads, int32_t block,
+                                                  int32_t max_keys);
+
+/* Accumulates the attention weight that every cache slot received:
+ *   score_out[q][g][s] = decay * score_in[q][g][s]
+ *                        + sum over rows j and query heads h of KV head g of
+ *                          exp(q_jh . k_s / sqrt(128) - lse_jh)   (s seen by j)
+ * for the slots s < n of the batch's sequences q; the rest is left as it was.
+ * Arguments as in dflash_kvq_attention, whose lse is read (a row with lse -inf
+ * adds nothing).  For a drafted block call it after acceptance, with the
+ * committed length and q_lens = the rows kept.
+ *   score_in_dev, score_out_dev [n_seqs][n_kv_heads][pages_per_seq * 128] float;
+ *   may be the same array; score_in NULL reads as zero.  4-byte aligned. */
+DFLASH_API dflash_status dflash_kvq_score(
+    const dflash_kvq_cache *cache, int32_t batch, int32_t n_heads, int32_t block, int32_t mask,
+    const int32_t *seq_ids_dev, const int32_t *kv_lens_dev, const int32_t *q_lens_dev,
+    const uint64_t *anc_dev, int32_t anc_words, int32_t max_keys, const void *q_dev,
+    int64_t q_row_stride, const float *lse_dev, float decay, const float *score_in_dev,
+    float *score_out_dev, dflash_stream_t stream);
+
+/* Eviction by accumulated weight.  Of the n = kv_lens[b] slots of sequence
+ * src_ids[b], KV head by KV head, the last `window` and the best-scored of the
+ * others are kept, `budget` in all (all of them where n <= budget; ties go to the
+ * lowest slot, NaN ranks below everything), and written in slot order to slots
+ * 0 .. min(n, budget) - 1 of sequence dst_ids[b], whose pages the caller has
+ * mapped (dflash_kv_pool_reserve of another slot; the source's pages can be
+ * released after).  Blocks take their exponents anew.  Sources are only read.  An
+ * entry with dst_ids[b] == src_ids[b] is refused on the device
+ * (DFLASH_E_DEVICE_CHECK, entry skipped); rows for unmapped destination pages are
+ * dropped, source slots on unmapped pages read as zero (DFLASH_E_CAPACITY).
+ *   score_dev    [n_seqs][n_kv_heads][pages_per_seq * 128]: row src_ids[b] is read,
+ *                row dst_ids[b] gets the kept slots' scores, then zeros
+ *   kept_dev     [batch][n_kv_heads][budget] int32 out: source slot of each kept
+ *                row, -1 past min(n, budget)
+ *   new_lens_dev [batch] int32 out: min(n, budget)
+ *   max_keys     host bound on the lengths, for planning only (1..2^29)
+ * budget 1..pages_per_seq * 128, window 0..budget. */
+DFLASH_API dflash_status dflash_kvq_evict(const dflash_kvq_cache *cache, int32_t batch,
+                                          const int32_t *src_ids_dev, const int32_t *dst_ids_dev,
+                                          const int32_t *kv_lens_dev, int32_t max_keys,
+                                          int32_t budget, int32_t window, float *score_dev,
+                                          int32_t *kept_dev, int32_t *new_lens_dev,
+                                          dflash_stream_t stream);
+
+/* Waits for `stream`, then returns and clears the cache's status word. */
+DFLASH_API dflash_status dflash_kvq_check(const dflash_kvq_cache *cache, dflash_stream_t stream);
+
 /* ---- temperature-1 drafting and acceptance ------------------------------------
  * The pages run DFlash at temperature 1 ("DFlash benchmark results" report: an
  * average 4.03x); at that temperature the drafter fills the block with
