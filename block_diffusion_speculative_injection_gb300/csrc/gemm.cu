@@ -748,6 +748,17 @@ bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t*
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_rows128(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  memset(m, 0, sizeof(*m));
+  const cuuint64_t gdim[2] = {128u, rows}, gstride[1] = {128u};
+  const cuuint32_t box[2] = {128u, box_rows}, estride[2] = {1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 dflash_status tmap_2d(dflash_ctx* ctx, const void* ptr, int64_t rows, int64_t cols, int box_rows,
                       const CUtensorMap** out) {
   return get_tmap(ctx, ptr, rows, cols, box_rows, out);

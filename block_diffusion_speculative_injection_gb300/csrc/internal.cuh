@@ -320,6 +320,8 @@ dflash_status tmap_2d(dflash_ctx* ctx, const void* ptr, int64_t rows, int64_t co
                       const CUtensorMap** out);
 bool encode_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box);
+// rows of 128 bytes [rows][128], box [box_rows][128], 128-byte swizzle
+bool encode_tmap_rows128(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows);
 
 int64_t block_attention_workspace(int batch, int H, int Hkv, int hd, int ctx_len, int block);
 dflash_status plan_attention(int sm_count, int batch, int H, int Hkv, int q_per_seq,
@@ -631,6 +633,16 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, ui
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same product of 8-bit operands (kind::f8f6f4, fp32 accumulate).
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Arrive on an mbarrier once all previously issued tcgen05.mma of this thread complete.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
@@ -760,6 +772,10 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr, uint32_t m
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
+}
+// kind::f8f6f4, D f32, A/B e4m3, both K-major, M x N
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 // bit 16 of the instruction descriptor: the B operand is MN-major
 constexpr uint32_t kIdescBMajorMN = 1u << 16;

@@ -25,6 +25,8 @@ struct KvqAttnK {
   const float* score_in;
   float* score_out;
   float decay;
+  int n_splits;
+  float *part_o, *part_ml;  // [split][row][head][128], [split][row][head] (m, l)
 };
 
 constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
@@ -76,58 +78,693 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
   return d;
 }
 
-// one warp per (row, query head), slots in order, lane l holding dims 4l..4l+3
-__global__ void __launch_bounds__(128) kvq_attn_kernel(const KvqAttnK p) {
+// ---------------------------------------------------------------------------
+// Attention on the 5th-generation tensor cores, both products in 8 bits.
+//
+// One CTA: 64 query rows (64 / G block positions x the G query heads of a KV
+// head) against one split of the sequence's slots, a page (128 slots) a tile.
+// K and V go from the pages to the tensor cores as they are (e4m3, TMA): no
+// conversion, so a tile costs half of the bytes and of the shared memory of a
+// bf16 one.  What is not 8-bit is split into e4m3 parts:
+//
+//   q = 2^a (q1 + q2): q1 = e4m3(q 2^-a), q2 = e4m3 of what q1 leaves.  The parts'
+//   4 + 4 significand bits hold a bf16 (8 bits) exactly where the element is above
+//   2^-10 of the row's largest, and to 2^-18 of that below.  S = Q1 K^T + Q2 K^T,
+//   two MMAs (M = 64) into one accumulator.
+//
+//   The weights carry V's exponents: with u_k = log2(e) s_k + eV_k (eV_k the exponent of
+//   slot k's block of V) and m >= max u - 1, y_k = 2^(u_k - m - 1) <= 1 is the weight
+//   of the CODES of V, and the softmax sum is sum y_k 2^-eV_k.  So neither K's
+//   exponents (a factor of S) nor V's (an addend of the exponent) cost a
+//   multiplication an element.  y = p1 + p2 / 16: p1 has the leading 4 bits, p2 (on a
+//   16 times finer scale) the residual, of either sign, rounded with a fixed dither
+//   over the 16 slots of a block: an error below 2^-8 y, without bias, and for
+//   weights down to 2^-24 of the largest (values below the smallest codes, 2^-13
+//   of y for p2, are dithered, not dropped).  P1 and P2 are the halves of one
+//   M = 128 operand, so both products cost one full-rate MMA; row r of P1 is
+//   operand row 32 (r / 16) + r % 16 and of P2 the one 16 further, which puts the
+//   two halves of an output row into lanes t and t + 16 of one warp.
+//
+// Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle):
+//   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB; two stages of K and two of
+//   V [128 slots][128], 16 KB each.  96 KB, so two CTAs share an SM: one's softmax
+//   runs beside the other's MMAs and loads.
+// Tensor memory: 256 columns, S [64 rows][128] and O [128 operand rows][128].  An
+// M = 64 accumulator keeps row m in lane (m / 16) * 32 + m % 16.
+//
+// Warps 0-3 (softmax): two threads per row (lanes t, t + 16), 64 slots each, held
+// in registers.  O and the sum are rescaled when the maximum grows by more
+// than a factor 2.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S of
+// the next tile before P V of this one.
+// A warp none of whose rows is in use only takes part in the barriers.
+// ---------------------------------------------------------------------------
+constexpr int kTile = kPageSlots;
+constexpr uint32_t kTileBytes = kTile * kKvqHd;  // one K or V tile, and P
+constexpr uint32_t kQPart = 64 * kKvqHd;
+constexpr uint32_t kAOffP = 2 * kQPart;
+constexpr uint32_t kAOffK = kAOffP + kTileBytes;
+constexpr int kAStages = 2;
+constexpr uint32_t kAOffV = kAOffK + kAStages * kTileBytes;
+constexpr uint32_t kAOffNan = kAOffV + kAStages * kTileBytes;  // [128 slots][4] bits of NaN dims
+constexpr uint32_t kAOffBar = kAOffNan + kTile * 16;
+constexpr int kAttnQSmem = (int)kAOffBar + 256 + 1024;  // barriers, alignment slack
+constexpr int kAttnQThreads = 192;
+constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
+constexpr float kLazyLog2 = 1.f;  // growth of the maximum that is not yet rescaled
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// bits below n set (n clamped to 0..32)
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
+}
+
+// Slots of a split, and whose rows of a q tile they are.  A sequence's slots are
+// shared out over the launch's splits in whole pages; `used` splits are not empty.
+// Weights y0, y1 <= 1 of slots `at`, `at + 1` of a block as e4m3 codes times 2^8 (an
+// fp16 below 2 is e4m3 but for 2^8 and three more significand bits, so code
+// and rounding are integer operations on its bits): codes of p1 and of p2 in the
+// high byte of each half of `hi` and `lo`, y = (p1 + p2 / 16) / 2^8.
+__device__ __forceinline__ void split_weights(float y0, float y1, int at, uint32_t& hi,
+                                              uint32_t& lo) {
+  const __half2 y = __floats2half2_rn(y0, y1);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;  // to nearest
+  const uint32_t d = u & 0xff80ff80u;
+  hi = u << 1;
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&d), __float2half2_rn(-16.f),
+                            __hmul2(y, __float2half2_rn(16.f)));  // exact, either sign
+  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);
+  // dither of slot k: 4 + 8 * (bits of k reversed), of the 128 below a code's step
+  const uint32_t rev0 = ((at & 1) << 3) | ((at & 2) << 1) | ((at & 4) >> 1) | ((at & 8) >> 3);
+  const uint32_t dither = (4 + 8 * rev0) | ((4 + 8 * (rev0 | 8)) << 16);
+  const uint32_t w = (rb + dither) << 1;
+  lo = (w & 0x7fff7fffu) | (rb & 0x80008000u);
+}
+
+struct KvqSpan {
+  int key_end, per_split, used;
+};
+__device__ __forceinline__ KvqSpan kvq_span(const KvqAttnK& p, int n, int r, int key_end, int j1) {
+  KvqSpan s;
+  // rows j < j1 of a causal pass see slots below n - r + j1
+  s.key_end = p.mask == DFLASH_MASK_CAUSAL ? min(key_end, n - r + j1) : key_end;
+  s.key_end = max(s.key_end, 0);
+  const int tiles = (s.key_end + kTile - 1) / kTile;
+  const int per = max(1, (tiles + p.n_splits - 1) / p.n_splits);
+  s.per_split = per * kTile;
+  s.used = (tiles + per - 1) / per;
+  return s;
+}
+
+// visibility of slots kb .. kb + 31 (all below `stop`) for row j
+__device__ __forceinline__ uint32_t visible32(const KvqAttnK& p, int kb, int stop, int ctx, int j,
+                                              const uint64_t* anc) {
+  const uint32_t m = bits_below(stop - kb);
+  if (p.mask == DFLASH_MASK_NONE) return m;
+  if (p.mask == DFLASH_MASK_CAUSAL) return m & bits_below(ctx + j + 1 - kb);
+  uint32_t t = 0;
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {  // the one or two words that 32 ancestor bits span
+    const int i0 = kb - ctx;     // block index of bit 0
+    const int word = (i0 >> 6) + w;
+    if (word < 0 || word >= p.anc_words) continue;
+    const int sh = word * 64 - i0;  // where the word's bit 0 lands
+    if (sh >= 32 || sh <= -64) continue;
+    t |= (uint32_t)(sh >= 0 ? anc[word] << sh : anc[word] >> -sh);
+  }
+  return m & (bits_below(ctx - kb) | t);
+}
+
+struct KvqMaps {
+  CUtensorMap k, v;
+};
+
+__global__ void __launch_bounds__(kAttnQThreads, 2)
+    kvq_attn_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int POS = 64 / p.G;
+  const int b = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
+  const int kvh = blockIdx.y, j0 = blockIdx.x * POS;
+  int32_t* const status = p.c.status;
+  int seq, n, r, key_end;
+  if (!kvq_entry(p, b, seq, n, r, key_end) || j0 >= r) return;
+  const int j1 = min(j0 + POS, r), ctx = n - r;
+  const KvqSpan span = kvq_span(p, n, r, key_end, j1);
+  const int k_begin = split * span.per_split;
+  const int k_stop = min(span.key_end, k_begin + span.per_split);
+  const int n_tiles = k_stop > k_begin ? (k_stop - k_begin + kTile - 1) / kTile : 0;
+
+  // the row of a softmax thread
+  const int t16 = lane & 15, h = lane >> 4;
+  const int row = warp * 16 + t16;
+  const int jr = j0 + row / p.G, hr = kvh * p.G + row % p.G;
+  const bool live = warp < 4 && row < POS * p.G && jr < j1;
+  const long long grow = (long long)b * p.block + jr;
+
+  if (n_tiles == 0) {
+    // no slot at all: rows without anything seen (an unused split of a longer
+    // sequence has nothing to do: the merge knows the used ones)
+    if (split == 0 && live) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + (grow * p.H + hr) * kKvqHd + 64 * h);
+      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse && h == 0) p.lse[grow * p.H + hr] = -INFINITY;
+    }
+    return;
+  }
+
+  uint8_t* const ps = sm + kAOffP;
+  uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(sm + kAOffNan);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kAOffBar);
+  uint64_t* const q_full = bars;
+  uint64_t* const s_full = bars + 1;
+  uint64_t* const s_free = bars + 2;
+  uint64_t* const p_full = bars + 3;
+  uint64_t* const pv_done = bars + 4;
+  uint64_t* const k_full = bars + 5;
+  uint64_t* const k_empty = k_full + kAStages;
+  uint64_t* const v_full = k_empty + kAStages;
+  uint64_t* const v_empty = v_full + kAStages;
+  uint64_t* const meet = v_empty + kAStages;  // the softmax warps among themselves
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(meet + 1);
+  volatile int* const nan_any = reinterpret_cast<volatile int*>(tslot + 1);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(pv_done, 1);
+    mbar_init(meet, 4);
+    for (int i = 0; i < kAStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    *nan_any = 0;
+    mbar_fence_init();
+  }
+  if (warp < 4) *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
+  if (warp == 4) {
+    tmem_alloc(tslot, kAttnQTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // dependents start once every CTA holds its tensor memory: one that allocates
+  // earlier could keep this kernel waiting for columns while it waits for us
+  pdl_trigger();
+  const uint32_t tmem = *tslot;
+  const int first_page = k_begin / kPageSlots;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
+      // softmax does not see its slots)
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.v);
+      int k_issued = 0, v_issued = 0;
+      auto load = [&](int t, bool is_v, int pg) -> bool {
+        const int st = t % kAStages, ph = (t / kAStages) & 1;
+        uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st];
+        uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+        if (t >= kAStages && !mbar_wait(empty, ph ^ 1, status)) return false;
+        mbar_arrive_expect_tx(full, kTileBytes);
+        tma_load_2d(sm + (is_v ? kAOffV : kAOffK) + st * kTileBytes, is_v ? &maps.v : &maps.k, 0,
+                    (max(pg, 0) * p.c.Hkv + kvh) * kPageSlots, full);
+        return true;
+      };
+      int pg_k = kvq_page(p.c, seq, first_page), pg_v = 0;
+      for (int t = 0; t <= n_tiles; ++t) {
+        const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, first_page + t + 1) : 0;
+        if (t < n_tiles) {
+          if (pg_k < 0) set_dev_status(status, kDevCapacity);
+          if (!load(t, false, pg_k)) break;
+          k_issued = t + 1;
+        }
+        if (t >= 1) {
+          if (!load(t - 1, true, pg_v)) break;
+          v_issued = t;
+        }
+        pg_v = pg_k;
+        pg_k = pg_next;
+      }
+      // every issued copy has landed before this thread leaves
+      for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
+        mbar_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
+      for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
+        mbar_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      // ---- MMA issuer: S(t), then P V(t - 1)
+      constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
+      constexpr uint32_t id_o = idesc_e4m3_f32(128, kKvqHd) | kIdescBMajorMN;
+      const uint32_t qa = smem_u32(sm), pa = smem_u32(ps);
+      bool ok = mbar_wait(q_full, 0, status);
+      for (int t = 0; ok && t <= n_tiles; ++t) {
+        if (t < n_tiles) {
+          const int st = t % kAStages;
+          if (!mbar_wait(&k_full[st], (t / kAStages) & 1, status)) break;
+          if (t >= 1 && !mbar_wait(s_free, (t - 1) & 1, status)) break;
+          tc_fence_after();
+          const uint32_t ka = smem_u32(sm + kAOffK + st * kTileBytes);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f8(tmem, sw128_desc(qa + part * kQPart + kk * 32), sw128_desc(ka + kk * 32), id_s,
+                        part + kk > 0 ? 1u : 0u);
+          tc_commit(s_full);
+          tc_commit(&k_empty[st]);
+        }
+        if (t >= 1) {
+          const int u = t - 1, st = u % kAStages;
+          if (!mbar_wait(p_full, u & 1, status)) break;
+          if (!mbar_wait(&v_full[st], (u / kAStages) & 1, status)) break;
+          tc_fence_after();
+          const uint32_t va = smem_u32(sm + kAOffV + st * kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f8(tmem + kTmemOCol, sw128_desc(pa + kk * 32),
+                      sw128_desc_mn(va + kk * 32 * kKvqHd, kTileBytes), id_o, u + kk > 0 ? 1u : 0u);
+          tc_commit(pv_done);
+          tc_commit(&v_empty[st]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax warps: half h of row t16's thread pair holds slots
+    // 64 h .. 64 h + 63 of every tile (blocks 4 h .. 4 h + 3)
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const uint64_t* const anc =
+        p.mask == DFLASH_MASK_TREE ? p.anc + (live ? grow : (long long)b * p.block + j0) * p.anc_words
+                                   : nullptr;
+    // the query row in two e4m3 parts
+    int qe = 0;
+    {
+      float x[64];
+      const uint4* src =
+          reinterpret_cast<const uint4*>(p.q + grow * p.q_stride + (long long)hr * kKvqHd + 64 * h);
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bf16x8_to_f(live ? src[i] : make_uint4(0u, 0u, 0u, 0u), x + 8 * i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float m = fabsf(x[8 * i + k]);
+          a = m < INFINITY ? fmaxf(a, m) : a;
+        }
+      }
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+      const int bits = __float_as_int(a);
+      qe = (bits >> 23) - 127 - ((bits & 0x7fffff) > 0x600000 ? 7 : 8);
+      qe = min(80, max(-80, qe));
+      const float s = pow2i(-qe);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w1[4], w2[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float* const y = x + 16 * i + 8 * k;
+          float d[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = fabsf(y[e]) < INFINITY ? y[e] * s : __int_as_float(0x7fffffff);
+          const uint2 c1 = kvq_encode8(y);
+          kvq_decode8(c1, d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = y[e] - d[e];
+          const uint2 c2 = kvq_encode8(d);
+          w1[2 * k] = c1.x;
+          w1[2 * k + 1] = c1.y;
+          w2[2 * k] = c2.x;
+          w2[2 * k + 1] = c2.y;
+        }
+        const uint32_t off = (uint32_t)row * 128 + ((uint32_t)((4 * h + i) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(sm + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        *reinterpret_cast<uint4*>(sm + kQPart + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    const float q_scale = pow2i(qe) * kScaleLog2;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    // slots from here on are not seen by every row of the CTA
+    const int mask_from = p.mask == DFLASH_MASK_NONE     ? k_stop
+                          : p.mask == DFLASH_MASK_CAUSAL ? min(k_stop, ctx + j0 + 1)
+                                                         : min(k_stop, ctx);
+    const int partial_from = p.mask == DFLASH_MASK_NONE ? k_stop : mask_from;
+    float m_used = -INFINITY, l = 0.f;
+    uint32_t bad[4] = {0u, 0u, 0u, 0u};  // dims in which the row saw a NaN of V
+    bool ok = true;
+    // page and exponents of tile t, read a tile ahead
+    auto exps_of = [&](int pg) -> uint2 {
+      if (pg < 0) return make_uint2(0u, 0u);
+      const int64_t at = kvq_ph(p.c, pg, kvh) * kKvqSubs + 4 * h;
+      return make_uint2(*reinterpret_cast<const uint32_t*>(p.c.ex[0] + at),
+                        *reinterpret_cast<const uint32_t*>(p.c.ex[1] + at));
+    };
+    // a barrier of the four warps whose wait is bounded like every other
+    uint32_t met = 0;
+    auto warps_meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(meet);
+        ok = mbar_wait(meet, met & 1, status);
+      }
+      ++met;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      __syncwarp();
+      return ok;
+    };
+    int pg = kvq_page(p.c, seq, first_page);
+    int pg_next = n_tiles > 1 ? kvq_page(p.c, seq, first_page + 1) : -1;
+    uint2 ex = exps_of(pg);
+    for (int t = 0; t < n_tiles; ++t) {
+      const int tile0 = k_begin + t * kTile;
+      const int pg_now = pg;
+      const uint2 ex_now = ex;
+      pg = pg_next;
+      pg_next = t + 2 < n_tiles ? kvq_page(p.c, seq, first_page + t + 2) : -1;
+      ex = t + 1 < n_tiles ? exps_of(pg) : make_uint2(0u, 0u);
+      const int stop = pg_now < 0 ? tile0 : k_stop;  // slots from here on are not seen
+      const bool masked = tile0 + kTile > min(stop, mask_from);
+      if (lane == 0) ok = mbar_wait(s_full, t & 1, status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      float s[64];
+      if (warp_live) {
+        tc_fence_after();
+        tmem_ld_half32_nowait<64>(lane_base, reinterpret_cast<uint32_t*>(s));
+        tmem_ld_half32_nowait<64>(lane_base + 32, reinterpret_cast<uint32_t*>(s) + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free);
+      float ck[4], ev[4], mx = -INFINITY;
+      if (warp_live) {
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t vis = visible32(p, tile0 + 64 * h + 32 * c, stop, ctx, jr, anc);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[32 * c + i] = (vis >> i) & 1u ? s[32 * c + i] : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ck[i] = q_scale * pow2i((int)(int8_t)(ex_now.x >> (8 * i)));
+          ev[i] = (float)(int)(int8_t)(ex_now.y >> (8 * i));
+          float bm = s[16 * i];
+#pragma unroll
+          for (int k = 1; k < 16; ++k) bm = fmaxf(bm, s[16 * i + k]);
+          mx = fmaxf(mx, fmaf(bm, ck[i], ev[i]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      }
+      // P V(t - 1) done: P is free, and O holds tiles 0 .. t - 1 (a warp without
+      // rows waits too: its arrival below must not count for an earlier tile)
+      if (t > 0) {
+        if (lane == 0) ok = mbar_wait(pv_done, (t - 1) & 1, status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+      }
+      if (warp_live) {
+        const bool grow_m = mx > m_used + kLazyLog2;
+        if (__any_sync(0xffffffffu, grow_m)) {
+          const float alpha = grow_m ? ex2(m_used - mx) : 1.f;
+          if (t > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(lane_base + kTmemOCol + 32 * c, o);
+            }
+            tmem_wait_st();
+          }
+          if (grow_m) {
+            l *= alpha;
+            m_used = mx;
+          }
+        }
+        const float base = m_used == -INFINITY ? 0.f : -m_used - kLazyLog2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float add = ev[i] + base;
+          float sum = 0.f;
+          uint32_t c1[4], c2[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int at = 4 * w + 2 * k;  // slots `at`, `at + 1` of the block
+              const float e0 = ex2(fmaf(s[16 * i + at], ck[i], add));
+              const float e1 = ex2(fmaf(s[16 * i + at + 1], ck[i], add));
+              sum += e0;
+              sum += e1;
+              split_weights(e0, e1, at, hi[k], lo[k]);
+            }
+            c1[w] = __byte_perm(hi[0], hi[1], 0x7531);
+            c2[w] = __byte_perm(lo[0], lo[1], 0x7531);
+          }
+          l = fmaf(sum, pow2i(-(int)ev[i]), l);
+          const uint32_t off = (uint32_t)(32 * warp + t16) * 128 +
+                               ((uint32_t)((4 * h + i) ^ (t16 & 7)) << 4);
+          *reinterpret_cast<uint4*>(ps + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+          *reinterpret_cast<uint4*>(ps + off + 16 * 128) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+        }
+      }
+      // V rows that are not seen must not hold NaN codes (0 * NaN): those behind
+      // the split's slots, or on no page, are zeroed; in rows that some query
+      // rows see and others do not, NaN codes are zeroed and noted for the rows
+      // that see them
+      if (tile0 + kTile > min(stop, partial_from)) {
+        const int st = t % kAStages;
+        if (lane == 0) ok = mbar_wait(&v_full[st], (t / kAStages) & 1, status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        uint8_t* const vs = sm + kAOffV + st * kTileBytes;
+        const int v_end = max(stop - tile0, 0), v_from = max(0, min(v_end, partial_from - tile0));
+        for (int i = v_from * 8 + (int)threadIdx.x; i < kTile * 8; i += 128) {
+          const int vr = i >> 3, ch = i & 7;
+          uint4* const at = reinterpret_cast<uint4*>(vs + vr * 128 + ((ch ^ (vr & 7)) << 4));
+          if (vr >= v_end) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
+          const uint4 v4 = *at;
+          uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+          uint32_t found = 0;  // bit per byte
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t m = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            w[k] &= ~(m | (m - (m >> 7)));
+            found |= ((m >> 7) * 0x10204080u >> 28) << (4 * k);
+          }
+          if (found) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            atomicOr(&nan_bits[vr * 4 + (ch >> 1)], found << (16 * (ch & 1)));
+            *nan_any = 1;
+          }
+        }
+        if (!warps_meet()) break;
+        if (*nan_any) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t vis = visible32(p, tile0 + 64 * h + 32 * c, stop, ctx, jr, anc);
+            while (vis) {
+              const int at = 64 * h + 32 * c + __ffs(vis) - 1;
+              vis &= vis - 1;
+              for (int k = 0; k < 4; ++k) bad[k] |= nan_bits[at * 4 + k];
+            }
+          }
+          if (!warps_meet()) break;
+          *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
+          if (threadIdx.x == 0) *nan_any = 0;
+          if (!warps_meet()) break;
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    // ---- epilogue: lanes t and t + 16 hold the P1 and the P2 part of row t's O
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bad[k] |= __shfl_xor_sync(0xffffffffu, bad[k], 16);
+    if (ok) {
+      const int u = n_tiles - 1;
+      if (lane == 0) ok = mbar_wait(pv_done, u & 1, status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (ok && warp_live) {
+      tc_fence_after();
+      const bool none = l == 0.f;
+      const long long rh = grow * p.H + hr;
+      const bool whole = span.used == 1;
+      // the codes of p1 are 2^8 times their values, those of p2 2^12 times
+      const float part_scale = h ? 1.f / 4096 : 1.f / 256;
+      const float scale = whole ? (none ? 0.f : 1.f / l) : 1.f;
+      const long long pbase = ((long long)split * p.batch * p.block * p.H + rh);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        // columns 32 c .. of both halves of the dims; the thread keeps the half h
+        uint32_t o0[32], o1[32];
+        tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o0);
+        tmem_ld32_nowait(lane_base + kTmemOCol + 64 + 32 * c, o1);
+        tmem_wait_ld();
+        float o[32];
+        const uint32_t nan = bad[2 * h + c];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float mine = __uint_as_float(h ? o1[i] : o0[i]) * part_scale;
+          const float give = __uint_as_float(h ? o0[i] : o1[i]) * part_scale;
+          const float other = __shfl_xor_sync(0xffffffffu, give, 16);
+          o[i] = none ? 0.f : (mine + other) * scale;
+          if ((nan >> i) & 1u) o[i] = __int_as_float(0x7fffffff);
+        }
+        if (!live) continue;
+        const int d0 = 64 * h + 32 * c;
+        if (whole) {
+          uint4* og = reinterpret_cast<uint4*>(p.out + rh * kKvqHd + d0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) og[i] = f_to_bf16x8(o + 8 * i);
+        } else {
+          float4* po = reinterpret_cast<float4*>(p.part_o + pbase * kKvqHd + d0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            po[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (live && h == 0) {
+        // l is in units of 2^(m + 1)
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + pbase * 2) = make_float2(m_used, l);
+        else if (p.lse)
+          p.lse[rh] = none ? -INFINITY : (m_used + kLazyLog2 + log2f(l)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tmem_dealloc(tmem, kAttnQTmem);
+}
+
+// Merge of the splits of a row: one warp per (row, head), lane l holding dims
+// 4 l .. 4 l + 3; the used splits' (m, l) and outputs are loaded kB at a time,
+// all before any is used, and summed in split order.
+constexpr int kMergeWarps = 4;
+template <int kB>
+__global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAttnK p) {
   pdl_trigger();
   pdl_wait();
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int h = (int)(w % p.H);
-  const long long row = w / p.H;
+  const long long rh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const long long rows = (long long)p.batch * p.block;
+  if (rh >= rows * p.H) return;
+  const long long row = rh / p.H;
   const int b = (int)(row / p.block), j = (int)(row % p.block);
-  if (b >= p.batch) return;
   int seq, n, r, key_end;
   if (!kvq_entry(p, b, seq, n, r, key_end) || j >= r) return;
-  const int kvh = h / p.G;
-  const uint64_t* anc = p.mask == DFLASH_MASK_TREE ? p.anc + row * p.anc_words : nullptr;
-  const float4 q = load_q4(p.q + row * p.q_stride + h * kKvqHd + lane * 4);
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < key_end; k0 += kPageSlots) {
-    const int page = kvq_page(p.c, seq, k0 / kPageSlots);
-    if (page < 0) {
-      set_dev_status(p.c.status, kDevCapacity);
-      continue;
-    }
-    const int64_t ph = kvq_ph(p.c, page, kvh);
-    for (int i = 0; i < min(kPageSlots, key_end - k0); ++i) {
-      if (!kvq_sees(p, k0 + i, n, r, j, anc)) continue;
-      const int64_t at = ph * kKvqPageBytes + i * kKvqHd + lane * 4;
-      const int64_t sub = ph * kKvqSubs + i / kKvqSub;
-      const float4 k = decode4(*reinterpret_cast<const uint32_t*>(p.c.c8[0] + at));
-      const float s = dot4(q, k) * (pow2i(p.c.ex[0][sub]) * kScaleLog2);
-      const float mn = fmaxf(m, s);
-      const float corr = exp2f(m - mn), pk = exp2f(s - mn);
-      const float4 v = decode4(*reinterpret_cast<const uint32_t*>(p.c.c8[1] + at));
-      const float pv = pk * pow2i(p.c.ex[1][sub]);
-      l = l * corr + pk;
-      o.x = o.x * corr + pv * v.x;
-      o.y = o.y * corr + pv * v.y;
-      o.z = o.z * corr + pv * v.z;
-      o.w = o.w * corr + pv * v.w;
-      m = mn;
+  const int POS = 64 / p.G;
+  const KvqSpan span = kvq_span(p, n, r, key_end, min(j / POS * POS + POS, r));
+  if (span.used <= 1) return;  // written whole
+  const long long stride = rows * p.H;
+  const float2* const ml = reinterpret_cast<const float2*>(p.part_ml) + rh;
+  const float4* const po = reinterpret_cast<const float4*>(p.part_o + rh * kKvqHd) + lane;
+  float m = -INFINITY;
+  for (int s = lane; s < span.used; s += 32) {
+    const float2 x = ml[s * stride];
+    if (x.y != 0.f) m = fmaxf(m, x.x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (m == -INFINITY) m = 0.f;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < span.used; s0 += kB) {
+    float4 o[kB];
+    const float2 x = lane < kB && s0 + lane < span.used ? ml[(s0 + lane) * stride]
+                                                        : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+      if (s0 + i < span.used) o[i] = po[(s0 + i) * (stride * (kKvqHd / 4))];
+    // a split whose sum is zero saw nothing (its m is -inf)
+    const float w = x.y != 0.f ? ex2(x.x - m) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      if (s0 + i >= span.used) break;
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      l += wi * __shfl_sync(0xffffffffu, x.y, i);
+      acc.x += wi * o[i].x;
+      acc.y += wi * o[i].y;
+      acc.z += wi * o[i].z;
+      acc.w += wi * o[i].w;
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-  const __nv_bfloat162 c = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 pk;
   pk.x = *reinterpret_cast<const uint32_t*>(&a);
   pk.y = *reinterpret_cast<const uint32_t*>(&c);
-  *reinterpret_cast<uint2*>(p.out + (row * p.H + h) * kKvqHd + lane * 4) = pk;
-  if (p.lse && lane == 0)
-    p.lse[row * p.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(p.out + rh * kKvqHd + lane * 4) = pk;
+  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + kLazyLog2 + log2f(l)) * kLn2;
 }
+
+// Splits of a launch of `ctas` CTAs over max_keys slots: the count that minimises
+// waves of resident CTAs (two per SM) x (tiles per split + two tiles' worth of
+// fixed cost), as many as the workspace holds.
+constexpr int kKvqMaxSplits = 256;
+static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t max_splits) {
+  const int64_t tiles = (max_keys + kTile - 1) / kTile;
+  const int64_t slots = 2 * (int64_t)sm_count;
+  const int64_t top = std::min(std::min<int64_t>(kKvqMaxSplits, tiles), max_splits);
+  int64_t best = 1, best_cost = INT64_MAX;
+  for (int64_t sp = 1; sp <= top; ++sp) {
+    const int64_t per = (tiles + sp - 1) / sp;
+    if (sp > 1 && (tiles + per - 1) / per < sp) continue;  // some would be empty
+    const int64_t cost = ((ctas * sp + slots - 1) / slots) * (per + 2) + (sp > 1 ? 1 : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = sp;
+    }
+  }
+  return (int)best;
+}
+
+static int kvq_sms() {
+  static std::atomic<int> sms[kMaxDevices];
+  const int dev = current_device_slot();
+  if (dev < 0) return 1;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 1;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64 / G); }
 
 // one warp per (sequence, KV head, slot): the rows in order
 __global__ void __launch_bounds__(128) kvq_score_kernel(const KvqAttnK p) {
@@ -176,6 +813,11 @@ static bool kvq_attn_shape_ok(int batch, int H, int Hkv, int block, int max_keys
          (int64_t)batch * block * H < ((int64_t)1 << 31);
 }
 
+// fp32 partial outputs and (m, l) of one split
+static int64_t kvq_part_bytes(int batch, int block, int H) {
+  return (int64_t)batch * block * H * (kKvqHd + 2) * (int64_t)sizeof(float);
+}
+
 // what the attention and the score take alike
 static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, int batch, int H,
                                    int block, int mask, const int32_t* seq_ids,
@@ -218,7 +860,9 @@ extern "C" {
 int64_t dflash_kvq_attention_workspace(int32_t batch, int32_t n_heads, int32_t n_kv_heads,
                                        int32_t block, int32_t max_keys) {
   if (!kvq_attn_shape_ok(batch, n_heads, n_kv_heads, block, max_keys)) return -1;
-  return 0;
+  const int64_t ctas = kvq_q_tiles(block, n_heads / n_kv_heads) * n_kv_heads * batch;
+  const int splits = kvq_plan_splits(kvq_sms(), ctas, max_keys, 65535 / batch);
+  return splits == 1 ? 0 : splits * kvq_part_bytes(batch, block, n_heads);
 }
 
 dflash_status dflash_kvq_attention(const dflash_kvq_cache* cache, int32_t batch, int32_t n_heads,
@@ -238,10 +882,30 @@ dflash_status dflash_kvq_attention(const dflash_kvq_cache* cache, int32_t batch,
   DF_TRY(kvq_ptrs_ok(ptrs, 3));
   p.out = static_cast<bf16*>(out);
   p.lse = lse;
-  const int64_t warps = (int64_t)batch * block * n_heads;
-  if (launch_k(true, kvq_attn_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0,
-               (cudaStream_t)stream, p) != cudaSuccess)
+  const int64_t q_tiles = kvq_q_tiles(block, p.G), rh = (int64_t)batch * block * n_heads;
+  const int64_t room = workspace ? workspace_bytes / kvq_part_bytes(batch, block, n_heads) : 0;
+  p.n_splits = kvq_plan_splits(kvq_sms(), q_tiles * cache->n_kv_heads * batch, max_keys,
+                               std::max<int64_t>(1, std::min<int64_t>(room, 65535 / batch)));
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = p.part_o + p.n_splits * rh * kKvqHd;
+  KvqMaps maps;
+  const uint64_t kv_rows = (uint64_t)cache->n_pages * cache->n_kv_heads * kPageSlots;
+  if (!encode_tmap_rows128(&maps.k, cache->k8_dev, kv_rows, kTile) ||
+      !encode_tmap_rows128(&maps.v, cache->v8_dev, kv_rows, kTile))
     return DFLASH_E_CUDA;
+  static std::atomic<bool> smem_done[kMaxDevices];
+  if (ensure_smem_attr(smem_done, kvq_attn_kernel, kAttnQSmem) != cudaSuccess) return DFLASH_E_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  const dim3 grid((unsigned)q_tiles, cache->n_kv_heads, batch * p.n_splits);
+  if (launch_k(true, kvq_attn_kernel, grid, dim3(kAttnQThreads), kAttnQSmem, st, maps, p) !=
+      cudaSuccess)
+    return DFLASH_E_CUDA;
+  if (p.n_splits > 1) {
+    const dim3 mg((unsigned)((rh + kMergeWarps - 1) / kMergeWarps));
+    if (launch_k(true, p.n_splits <= 8 ? kvq_merge_kernel<8> : kvq_merge_kernel<32>, mg,
+                 dim3(32 * kMergeWarps), 0, st, p) != cudaSuccess)
+      return DFLASH_E_CUDA;
+  }
   return DFLASH_OK;
 }
 
