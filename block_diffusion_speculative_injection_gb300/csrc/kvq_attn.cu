@@ -93,17 +93,18 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 //   two MMAs (M = 64) into one accumulator.
 //
 //   The weights carry V's exponents: with u_k = log2(e) s_k + eV_k (eV_k the exponent of
-//   slot k's block of V) and m >= max u - 1, y_k = 2^(u_k - m - 1) <= 1 is the weight
-//   of the CODES of V, and the softmax sum is sum y_k 2^-eV_k.  So neither K's
+//   slot k's block of V) and m >= max u - 4, z_k = 2^(u_k - m) <= 16 is the weight
+//   of the CODES of V, and the softmax sum is sum z_k 2^-eV_k.  So neither K's
 //   exponents (a factor of S) nor V's (an addend of the exponent) cost a
-//   multiplication an element.  y = p1 + p2 / 16: p1 has the leading 4 bits, p2 (on a
+//   multiplication an element, and errors in z are relative to the largest
+//   contribution to the output.  16 z = p1 + p2 / 16: p1 has the leading 4 bits, p2 (on a
 //   16 times finer scale) the residual, of either sign, rounded with a fixed dither
-//   over the 16 slots of a block: an error below 2^-8 y, without bias, and for
-//   weights down to 2^-24 of the largest (values below the smallest codes, 2^-13
-//   of y for p2, are dithered, not dropped).  P1 and P2 are the halves of one
-//   M = 128 operand, so both products cost one full-rate MMA; row r of P1 is
-//   operand row 32 (r / 16) + r % 16 and of P2 the one 16 further, which puts the
-//   two halves of an output row into lanes t and t + 16 of one warp.
+//   over the 16 slots of a block: an error below 2^-8 z, without bias, down to z = 2^-10;
+//   smaller weights are held to 2^-17 (dithered down to 2^-22: many small ones add
+//   up).  P1 and P2 are the halves of one M = 128 operand, so both products cost one
+//   full-rate MMA; row r of P1 is operand row 32 (r / 16) + r % 16 and of P2 the one
+//   16 further, which puts the two halves of an output row into lanes t and t + 16
+//   of one warp.
 //
 // Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle):
 //   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB; two stages of K and two of
@@ -114,7 +115,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 //
 // Warps 0-3 (softmax): two threads per row (lanes t, t + 16), 64 slots each, held
 // in registers.  O and the sum are rescaled when the maximum grows by more
-// than a factor 2.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S of
+// than a factor 16.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S of
 // the next tile before P V of this one.
 // A warp none of whose rows is in use only takes part in the barriers.
 // ---------------------------------------------------------------------------
@@ -130,7 +131,10 @@ constexpr uint32_t kAOffBar = kAOffNan + kTile * 16;
 constexpr int kAttnQSmem = (int)kAOffBar + 256 + 1024;  // barriers, alignment slack
 constexpr int kAttnQThreads = 192;
 constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
-constexpr float kLazyLog2 = 1.f;  // growth of the maximum that is not yet rescaled
+// Growth of the maximum that is not yet rescaled: z <= 2^4.  (At a factor of 2, 58 %
+// of the warps' tiles rescaled O on 33-page splits, at 16 one in ten does; the headroom costs
+// p2 that many binades at the bottom.)
+constexpr float kLazyLog2 = 4.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -144,24 +148,51 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 
 // Slots of a split, and whose rows of a q tile they are.  A sequence's slots are
 // shared out over the launch's splits in whole pages; `used` splits are not empty.
-// Weights y0, y1 <= 1 of slots `at`, `at + 1` of a block as e4m3 codes times 2^8 (an
-// fp16 below 2 is e4m3 but for 2^8 and three more significand bits, so code
-// and rounding are integer operations on its bits): codes of p1 and of p2 in the
-// high byte of each half of `hi` and `lo`, y = (p1 + p2 / 16) / 2^8.
-__device__ __forceinline__ void split_weights(float y0, float y1, int at, uint32_t& hi,
-                                              uint32_t& lo) {
-  const __half2 y = __floats2half2_rn(y0, y1);
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;  // to nearest
-  const uint32_t d = u & 0xff80ff80u;
-  hi = u << 1;
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&d), __float2half2_rn(-16.f),
-                            __hmul2(y, __float2half2_rn(16.f)));  // exact, either sign
-  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);
-  // dither of slot k: 4 + 8 * (bits of k reversed), of the 128 below a code's step
-  const uint32_t rev0 = ((at & 1) << 3) | ((at & 2) << 1) | ((at & 4) >> 1) | ((at & 8) >> 3);
-  const uint32_t dither = (4 + 8 * rev0) | ((4 + 8 * (rev0 | 8)) << 16);
-  const uint32_t w = (rb + dither) << 1;
-  lo = (w & 0x7fff7fffu) | (rb & 0x80008000u);
+// Four weights z <= 16 of consecutive slots, the first a multiple of 4 in its block,
+// as four codes of p1 and four of p2, z = (p1 + p2 / 16) / 16.  z in fp16 carries 11
+// significand bits; an fp16 below 2 is an e4m3 code (times 2^8) with three more
+// of them, so codes and roundings are integer operations on its bits:
+//   p1 / 2^8 = y rounded to 4 bits, y = z / 16 (exponent bits - 4; zero for y < 2^-14,
+//   which p2 holds alone), p2 / 2^8 = z - 16 y rounded to 4 bits with a dither.
+__device__ __forceinline__ void split_weights(const float* z, int at, uint32_t& c1, uint32_t& c2) {
+  uint32_t d[2], w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {  // slots at + k and at + k + 2
+    const __half2 zh = __floats2half2_rn(z[k], z[k + 2]);
+    const uint32_t u = __viaddmax_s16x2_relu(*reinterpret_cast<const uint32_t*>(&zh),
+                                             0xf040f040u /* 0x40 - 0x1000 */, 0u);
+    d[k] = u & 0xff80ff80u;
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&d[k]), __float2half2_rn(-16.f), zh);
+    const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);  // exact, either sign
+    // slot i's dither, of the 128 units below a step of the code: 4 + 8 (i's four
+    // bits reversed)
+    const int i = at + k;
+    const uint32_t rev = ((i & 1) << 3) | ((i & 2) << 1) | ((i & 4) >> 1) | ((i & 8) >> 3);
+    const uint32_t dither = (4 + 8 * rev) | ((4 + 8 * (rev | 4)) << 16);  // i + 2: bit 1 set
+    w[k] = ((rb + rb + 2 * dither) & 0x7fff7fffu) | (rb & 0x80008000u);
+  }
+  c1 = (d[0] >> 7) + (d[1] << 1);  // codes in bits 14..7 of each half
+  c2 = __byte_perm(w[0], w[1], 0x7351);  // codes in the high bytes
+}
+
+// (a0, a1) * b + c and (a0, a1) + (b0, b1) in one instruction each
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 struct KvqSpan {
@@ -490,7 +521,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           ev[i] = (float)(int)(int8_t)(ex_now.y >> (8 * i));
           float bm = s[16 * i];
 #pragma unroll
-          for (int k = 1; k < 16; ++k) bm = fmaxf(bm, s[16 * i + k]);
+          for (int k = 1; k < 15; k += 2) bm = fmaxf(fmaxf(bm, s[16 * i + k]), s[16 * i + k + 1]);
+          bm = fmaxf(bm, s[16 * i + 15]);
           mx = fmaxf(mx, fmaf(bm, ck[i], ev[i]));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -524,28 +556,26 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
             m_used = mx;
           }
         }
-        const float base = m_used == -INFINITY ? 0.f : -m_used - kLazyLog2;
+        const float base = m_used == -INFINITY ? 0.f : -m_used;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float add = ev[i] + base;
-          float sum = 0.f;
+          float2 sum = make_float2(0.f, 0.f);
           uint32_t c1[4], c2[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t hi[2], lo[2];
+            float z[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int at = 4 * w + 2 * k;  // slots `at`, `at + 1` of the block
-              const float e0 = ex2(fmaf(s[16 * i + at], ck[i], add));
-              const float e1 = ex2(fmaf(s[16 * i + at + 1], ck[i], add));
-              sum += e0;
-              sum += e1;
-              split_weights(e0, e1, at, hi[k], lo[k]);
+            for (int k = 0; k < 4; k += 2) {
+              const float2 x = fma2(make_float2(s[16 * i + 4 * w + k], s[16 * i + 4 * w + k + 1]),
+                                    ck[i], add);
+              z[k] = ex2(x.x);
+              z[k + 1] = ex2(x.y);
+              sum = add2(sum, make_float2(z[k], z[k + 1]));
             }
-            c1[w] = __byte_perm(hi[0], hi[1], 0x7531);
-            c2[w] = __byte_perm(lo[0], lo[1], 0x7531);
+            split_weights(z, 4 * w, c1[w], c2[w]);
           }
-          l = fmaf(sum, pow2i(-(int)ev[i]), l);
+          l = fmaf(sum.x + sum.y, pow2i(-(int)ev[i]), l);
           const uint32_t off = (uint32_t)(32 * warp + t16) * 128 +
                                ((uint32_t)((4 * h + i) ^ (t16 & 7)) << 4);
           *reinterpret_cast<uint4*>(ps + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
@@ -620,8 +650,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       const bool none = l == 0.f;
       const long long rh = grow * p.H + hr;
       const bool whole = span.used == 1;
-      // the codes of p1 are 2^8 times their values, those of p2 2^12 times
-      const float part_scale = h ? 1.f / 4096 : 1.f / 256;
+      const float part_scale = h ? 1.f / 256 : 1.f / 16;
       const float scale = whole ? (none ? 0.f : 1.f / l) : 1.f;
       const long long pbase = ((long long)split * p.batch * p.block * p.H + rh);
 #pragma unroll 1
@@ -655,11 +684,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         }
       }
       if (live && h == 0) {
-        // l is in units of 2^(m + 1)
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + pbase * 2) = make_float2(m_used, l);
         else if (p.lse)
-          p.lse[rh] = none ? -INFINITY : (m_used + kLazyLog2 + log2f(l)) * kLn2;
+          p.lse[rh] = none ? -INFINITY : (m_used + log2f(l)) * kLn2;
       }
     }
   }
@@ -727,7 +755,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   pk.x = *reinterpret_cast<const uint32_t*>(&a);
   pk.y = *reinterpret_cast<const uint32_t*>(&c);
   *reinterpret_cast<uint2*>(p.out + rh * kKvqHd + lane * 4) = pk;
-  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + kLazyLog2 + log2f(l)) * kLn2;
+  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Splits of a launch of `ctas` CTAs over max_keys slots: the count that minimises
