@@ -25,6 +25,7 @@ struct KvqAttnK {
   const float* score_in;
   float* score_out;
   float decay;
+  int pos, g_inv;  // block positions of a CTA's 64 rows; row / G = row * g_inv >> 16 (row < 64)
   int n_splits;
   float *part_o, *part_ml;  // [split][row][head][128], [split][row][head] (m, l)
 };
@@ -33,20 +34,35 @@ constexpr float kScaleLog2 = 0.12751743f;  // log2(e) / sqrt(128)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Entry b: sequence, slots n, rows r, and the first slot the cache cannot hold
-// or the sequence does not have (key_end); false: skip it.
-__device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, int& n, int& r,
-                                          int& key_end) {
-  seq = kvq_seq(p.c, p.seq_ids, b);
-  n = p.kv_lens[b];
-  r = p.q_lens ? p.q_lens[b] : p.block;
-  if (seq < 0) return false;
-  if (n < 0 || r < 0 || r > p.block) {
+// or the sequence does not have (key_end); false: skip it.  In two steps, so that
+// the loads can be under way while something else is done.
+struct KvqEntry {
+  int seq, n, r;
+};
+__device__ __forceinline__ KvqEntry kvq_entry_load(const KvqAttnK& p, int b) {
+  KvqEntry e;
+  e.seq = p.seq_ids ? p.seq_ids[b] : b;
+  e.n = p.kv_lens[b];
+  e.r = p.q_lens ? p.q_lens[b] : p.block;
+  return e;
+}
+__device__ __forceinline__ bool kvq_entry_check(const KvqAttnK& p, const KvqEntry& e, int& key_end) {
+  key_end = 0;
+  if (e.seq < 0 || e.seq >= p.c.n_seqs || e.n < 0 || e.r < 0 || e.r > p.block) {
     set_dev_status(p.c.status, kDevCheck);
     return false;
   }
-  key_end = min(n, p.c.pps * kPageSlots);
-  if (key_end < n) set_dev_status(p.c.status, kDevCapacity);
+  key_end = min(e.n, p.c.pps * kPageSlots);
+  if (key_end < e.n) set_dev_status(p.c.status, kDevCapacity);
   return true;
+}
+__device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, int& n, int& r,
+                                          int& key_end) {
+  const KvqEntry e = kvq_entry_load(p, b);
+  seq = e.seq;
+  n = e.n;
+  r = e.r;
+  return kvq_entry_check(p, e, key_end);
 }
 
 // does row j of a sequence (n slots, r rows) see slot k < n?
@@ -127,7 +143,10 @@ constexpr uint32_t kAOffK = kAOffP + kTileBytes;
 constexpr int kAStages = 2;
 constexpr uint32_t kAOffV = kAOffK + kAStages * kTileBytes;
 constexpr uint32_t kAOffNan = kAOffV + kAStages * kTileBytes;  // [128 slots][4] bits of NaN dims
-constexpr uint32_t kAOffBar = kAOffNan + kTile * 16;
+constexpr uint32_t kAOffQs = kAOffNan + kTile * 16;  // scale of each query row
+constexpr uint32_t kAOffBar = kAOffQs + 64 * 4;
+constexpr uint32_t kORow = kKvqHd * 4 + 16;  // an accumulator row staged over the tiles, padded
+static_assert(128 * kORow <= kAOffNan, "accumulator rows fit");
 constexpr int kAttnQSmem = (int)kAOffBar + 256 + 1024;  // barriers, alignment slack
 constexpr int kAttnQThreads = 192;
 constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
@@ -195,6 +214,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// block position (within the CTA's) of one of its 64 rows
+__device__ __forceinline__ int row_pos(const KvqAttnK& p, int row) { return row * p.g_inv >> 16; }
+
 struct KvqSpan {
   int key_end, per_split, used;
 };
@@ -240,34 +262,22 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   uint8_t* sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int POS = 64 / p.G;
+  const int POS = p.pos;
   const int b = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
   const int kvh = blockIdx.y, j0 = blockIdx.x * POS;
   int32_t* const status = p.c.status;
-  int seq, n, r, key_end;
-  if (!kvq_entry(p, b, seq, n, r, key_end) || j0 >= r) return;
-  const int j1 = min(j0 + POS, r), ctx = n - r;
-  const KvqSpan span = kvq_span(p, n, r, key_end, j1);
-  const int k_begin = split * span.per_split;
-  const int k_stop = min(span.key_end, k_begin + span.per_split);
-  const int n_tiles = k_stop > k_begin ? (k_stop - k_begin + kTile - 1) / kTile : 0;
-
-  // the row of a softmax thread
+  const KvqEntry entry = kvq_entry_load(p, b);
+  // the query rows of a softmax warp, two a load (eight dims a lane); rows past the
+  // sequence's are in bounds (j < block) and dropped later
   const int t16 = lane & 15, h = lane >> 4;
-  const int row = warp * 16 + t16;
-  const int jr = j0 + row / p.G, hr = kvh * p.G + row % p.G;
-  const bool live = warp < 4 && row < POS * p.G && jr < j1;
-  const long long grow = (long long)b * p.block + jr;
-
-  if (n_tiles == 0) {
-    // no slot at all: rows without anything seen (an unused split of a longer
-    // sequence has nothing to do: the merge knows the used ones)
-    if (split == 0 && live) {
-      uint4* o = reinterpret_cast<uint4*>(p.out + (grow * p.H + hr) * kKvqHd + 64 * h);
-      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse && h == 0) p.lse[grow * p.H + hr] = -INFINITY;
-    }
-    return;
+  uint4 q_raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int qr = warp * 16 + 2 * i + h, qg = row_pos(p, qr), qj = j0 + qg;
+    q_raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (warp < 4 && qr < POS * p.G && qj < p.block)
+      q_raw[i] = *reinterpret_cast<const uint4*>(p.q + ((long long)b * p.block + qj) * p.q_stride +
+                                                 (kvh * p.G + qr - qg * p.G) * kKvqHd + 8 * t16);
   }
 
   uint8_t* const ps = sm + kAOffP;
@@ -307,6 +317,21 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     tmem_alloc(tslot, kAttnQTmem);
     tmem_relinquish();
   }
+  int key_end;
+  const bool work = kvq_entry_check(p, entry, key_end) && j0 < entry.r;
+  const int seq = entry.seq, n = entry.n, r = entry.r;
+  const int j1 = min(j0 + POS, r), ctx = n - r;
+  const KvqSpan span = kvq_span(p, n, r, key_end, j1);
+  const int k_begin = split * span.per_split;
+  const int k_stop = min(span.key_end, k_begin + span.per_split);
+  const int n_tiles = work && k_stop > k_begin ? (k_stop - k_begin + kTile - 1) / kTile : 0;
+
+  // the row of a softmax thread
+  const int row = warp * 16 + t16;
+  const int jg = row_pos(p, row);
+  const int jr = j0 + jg, hr = kvh * p.G + row - jg * p.G;
+  const bool live = work && warp < 4 && row < POS * p.G && jr < j1;
+  const long long grow = (long long)b * p.block + jr;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -316,7 +341,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   const uint32_t tmem = *tslot;
   const int first_page = k_begin / kPageSlots;
 
-  if (warp == 4) {
+  if (n_tiles == 0) {
+    // no slot at all: rows without anything seen get zeros (an unused split of a
+    // longer sequence has nothing to do: the merge knows the used ones)
+    if (split == 0 && live) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + (grow * p.H + hr) * kKvqHd + 64 * h);
+      for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse && h == 0) p.lse[grow * p.H + hr] = -INFINITY;
+    }
+  } else if (warp == 4) {
     if (lane == 0) {
       // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
       // softmax does not see its slots)
@@ -401,56 +434,67 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     const uint64_t* const anc =
         p.mask == DFLASH_MASK_TREE ? p.anc + (live ? grow : (long long)b * p.block + j0) * p.anc_words
                                    : nullptr;
-    // the query row in two e4m3 parts
-    int qe = 0;
-    {
-      float x[64];
-      const uint4* src =
-          reinterpret_cast<const uint4*>(p.q + grow * p.q_stride + (long long)hr * kKvqHd + 64 * h);
-      float a = 0.f;
+    // The warp's 16 query rows in two e4m3 parts.  y = q 2^-(a + 8) in fp16 is exact but
+    // for elements below 2^-15 of the largest; an fp16 below 2 is an e4m3 code
+    // times 2^8 with three more significand bits, so the parts come out of
+    // integer operations on its bits.
+    float* const q_scales = reinterpret_cast<float*>(sm + kAOffQs) + warp * 16;
+    if (warp_live) {
+      // largest magnitude of each row, on bf16 pairs (as integers, NaN above all)
+      uint32_t top[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        bf16x8_to_f(live ? src[i] : make_uint4(0u, 0u, 0u, 0u), x + 8 * i);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float m = fabsf(x[8 * i + k]);
-          a = m < INFINITY ? fmaxf(a, m) : a;
-        }
+        constexpr uint32_t abs2 = 0x7fff7fffu;
+        top[i] = __vimax3_u16x2(q_raw[i].x & abs2, q_raw[i].y & abs2, q_raw[i].z & abs2);
+        top[i] = __vmaxu2(top[i], q_raw[i].w & abs2);
       }
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-      const int bits = __float_as_int(a);
-      qe = (bits >> 23) - 127 - ((bits & 0x7fffff) > 0x600000 ? 7 : 8);
-      qe = min(80, max(-80, qe));
-      const float s = pow2i(-qe);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const uint4 now = q_raw[0];
+        const uint32_t bits = max(top[0] & 0xffffu, top[0] >> 16) << 16;
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {  // keeps the loop rolled
+          q_raw[k] = q_raw[k + 1];
+          top[k] = top[k + 1];
+        }
+        const int qr = warp * 16 + 2 * i + h;
+        // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
+        // magnitude above 448 * 2^118 becomes NaN
+        const int e = max(-80, (int)(bits >> 23) - 127 - ((bits & 0x7fffff) > 0x600000 ? 7 : 8));
+        const bool row_bad = e > 118;
+        const float sc = pow2i(-min(e, 118) - 8);
+        float x[8];
+        bf16x8_to_f(now, x);
         uint32_t w1[4], w2[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float* const y = x + 16 * i + 8 * k;
-          float d[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            y[e] = fabsf(y[e]) < INFINITY ? y[e] * s : __int_as_float(0x7fffffff);
-          const uint2 c1 = kvq_encode8(y);
-          kvq_decode8(c1, d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = y[e] - d[e];
-          const uint2 c2 = kvq_encode8(d);
-          w1[2 * k] = c1.x;
-          w1[2 * k + 1] = c1.y;
-          w2[2 * k] = c2.x;
-          w2[2 * k + 1] = c2.y;
+        for (int k = 0; k < 4; ++k) {
+          const __half2 y = __floats2half2_rn(x[2 * k] * sc, x[2 * k + 1] * sc);
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
+          const uint32_t d = u & 0xff80ff80u;
+          const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
+          w1[k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
+          w2[k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
         }
-        const uint32_t off = (uint32_t)row * 128 + ((uint32_t)((4 * h + i) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(sm + off) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-        *reinterpret_cast<uint4*>(sm + kQPart + off) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        const uint32_t off = (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
+        *reinterpret_cast<uint2*>(sm + off) =
+            make_uint2(__byte_perm(w1[0], w1[1], 0x7531), __byte_perm(w1[2], w1[3], 0x7531));
+        *reinterpret_cast<uint2*>(sm + kQPart + off) =
+            make_uint2(__byte_perm(w2[0], w2[1], 0x7531), __byte_perm(w2[2], w2[3], 0x7531));
+        // a bad row: minus its scale
+        if (t16 == 0) q_scales[2 * i + h] = row_bad ? -kScaleLog2 : pow2i(e) * kScaleLog2;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
     }
-    const float q_scale = pow2i(qe) * kScaleLog2;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    const float q_signed = warp_live ? q_scales[t16] : 0.f;
+    const float q_scale = fabsf(q_signed);
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     // slots from here on are not seen by every row of the CTA
     const int mask_from = p.mask == DFLASH_MASK_NONE     ? k_stop
@@ -648,46 +692,64 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     if (ok && warp_live) {
       tc_fence_after();
       const bool none = l == 0.f;
-      const long long rh = grow * p.H + hr;
+      if (q_signed < 0.f && !none) l = __int_as_float(0x7fffffff);
       const bool whole = span.used == 1;
-      const float part_scale = h ? 1.f / 256 : 1.f / 16;
-      const float scale = whole ? (none ? 0.f : 1.f / l) : 1.f;
-      const long long pbase = ((long long)split * p.batch * p.block * p.H + rh);
+      // Through shared memory (Q, P, K and V are done with), so that the stores are
+      // whole rows: lane i's 128 columns (row i % 16, part i / 16) as a padded row
+      uint8_t* const stage = sm + warp * 32 * kORow;
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        // columns 32 c .. of both halves of the dims; the thread keeps the half h
-        uint32_t o0[32], o1[32];
-        tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o0);
-        tmem_ld32_nowait(lane_base + kTmemOCol + 64 + 32 * c, o1);
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o);
         tmem_wait_ld();
-        float o[32];
-        const uint32_t nan = bad[2 * h + c];
+        uint4* const at = reinterpret_cast<uint4*>(stage + lane * kORow + 128 * c);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float mine = __uint_as_float(h ? o1[i] : o0[i]) * part_scale;
-          const float give = __uint_as_float(h ? o0[i] : o1[i]) * part_scale;
-          const float other = __shfl_xor_sync(0xffffffffu, give, 16);
-          o[i] = none ? 0.f : (mine + other) * scale;
-          if ((nan >> i) & 1u) o[i] = __int_as_float(0x7fffffff);
-        }
-        if (!live) continue;
-        const int d0 = 64 * h + 32 * c;
-        if (whole) {
-          uint4* og = reinterpret_cast<uint4*>(p.out + rh * kKvqHd + d0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) og[i] = f_to_bf16x8(o + 8 * i);
-        } else {
-          float4* po = reinterpret_cast<float4*>(p.part_o + pbase * kKvqHd + d0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            po[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+        for (int i = 0; i < 8; ++i) at[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
+      const long long rh = grow * p.H + hr;
       if (live && h == 0) {
         if (!whole)
-          *reinterpret_cast<float2*>(p.part_ml + pbase * 2) = make_float2(m_used, l);
+          *reinterpret_cast<float2*>(p.part_ml + ((long long)split * p.batch * p.block * p.H + rh) * 2) =
+              make_float2(m_used, l);
         else if (p.lse)
           p.lse[rh] = none ? -INFINITY : (m_used + log2f(l)) * kLn2;
+      }
+      const float scale = none ? 0.f : (whole ? 1.f / l : 1.f);
+      const bool any_bad = __any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u);
+      const int n_live = __popc(__ballot_sync(0xffffffffu, live) & 0xffffu);  // rows 0 .. n_live - 1
+      __syncwarp();
+#pragma unroll 2
+      for (int i = 0; i < n_live; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(stage + i * kORow + 16 * lane);
+        const float4 y = *reinterpret_cast<const float4*>(stage + (16 + i) * kORow + 16 * lane);
+        const float sc = __shfl_sync(0xffffffffu, scale, i);
+        const long long at = __shfl_sync(0xffffffffu, rh, i) * kKvqHd + 4 * lane;
+        const float s1 = sc * (1.f / 16), s2 = sc * (1.f / 256);
+        // (a row that saw nothing has sc = 0, and no NaN: its weights were zero)
+        float4 v = make_float4(x.x * s1 + y.x * s2, x.y * s1 + y.y * s2, x.z * s1 + y.z * s2,
+                               x.w * s1 + y.w * s2);
+        if (sc == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (any_bad) {
+          uint32_t nan = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x4 = __shfl_sync(0xffffffffu, bad[k], i);
+            if (k == lane >> 3) nan = x4 >> (4 * (lane & 7));
+          }
+          if (nan & 1u) v.x = __int_as_float(0x7fffffff);
+          if (nan & 2u) v.y = __int_as_float(0x7fffffff);
+          if (nan & 4u) v.z = __int_as_float(0x7fffffff);
+          if (nan & 8u) v.w = __int_as_float(0x7fffffff);
+        }
+        if (whole) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+          uint2 w;
+          w.x = *reinterpret_cast<const uint32_t*>(&lo);
+          w.y = *reinterpret_cast<const uint32_t*>(&hi);
+          *reinterpret_cast<uint2*>(p.out + at) = w;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + (long long)split * p.batch * p.block * p.H * kKvqHd + at) = v;
+        }
       }
     }
   }
@@ -697,31 +759,38 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
 }
 
 // Merge of the splits of a row: one warp per (row, head), lane l holding dims
-// 4 l .. 4 l + 3; the used splits' (m, l) and outputs are loaded kB at a time,
-// all before any is used, and summed in split order.
+// 4 l .. 4 l + 3.  The used splits' (m, l) sit one a lane, their outputs are loaded eight
+// at a time; sums run in split order.
 constexpr int kMergeWarps = 4;
-template <int kB>
 __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAttnK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const long long rh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const long long rows = (long long)p.batch * p.block;
-  if (rh >= rows * p.H) return;
+  const long long rows = (long long)p.batch * p.block, stride = rows * p.H;
+  if (rh >= stride) return;
   const long long row = rh / p.H;
   const int b = (int)(row / p.block), j = (int)(row % p.block);
-  int seq, n, r, key_end;
-  if (!kvq_entry(p, b, seq, n, r, key_end) || j >= r) return;
-  const int POS = 64 / p.G;
-  const KvqSpan span = kvq_span(p, n, r, key_end, min(j / POS * POS + POS, r));
-  if (span.used <= 1) return;  // written whole
-  const long long stride = rows * p.H;
   const float2* const ml = reinterpret_cast<const float2*>(p.part_ml) + rh;
   const float4* const po = reinterpret_cast<const float4*>(p.part_o + rh * kKvqHd) + lane;
-  float m = -INFINITY;
-  for (int s = lane; s < span.used; s += 32) {
-    const float2 x = ml[s * stride];
-    if (x.y != 0.f) m = fmaxf(m, x.x);
+  // the first splits are read before it is known how many are used (the
+  // partials of all of them are in bounds)
+  constexpr int kB = 8;
+  float4 o[kB];
+#pragma unroll
+  for (int i = 0; i < kB; ++i)
+    if (i < p.n_splits) o[i] = po[i * (stride * (kKvqHd / 4))];
+  float2 x = lane < p.n_splits ? ml[lane * stride] : make_float2(-INFINITY, 0.f);
+  int seq, n, r, key_end;
+  if (!kvq_entry(p, b, seq, n, r, key_end) || j >= r) return;
+  const int POS = p.pos;
+  const KvqSpan span = kvq_span(p, n, r, key_end, min(j / POS * POS + POS, r));
+  if (span.used <= 1) return;  // written whole
+  // a split whose sum is zero saw nothing (its m is -inf)
+  float m = lane < span.used && x.y != 0.f ? x.x : -INFINITY;
+  for (int s = lane + 32; s < span.used; s += 32) {
+    const float2 y = ml[s * stride];
+    if (y.y != 0.f) m = fmaxf(m, y.x);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -729,19 +798,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < span.used; s0 += kB) {
-    float4 o[kB];
-    const float2 x = lane < kB && s0 + lane < span.used ? ml[(s0 + lane) * stride]
-                                                        : make_float2(-INFINITY, 0.f);
+    if (s0 > 0) {
+      if ((s0 & 31) == 0)
+        x = s0 + lane < span.used ? ml[(s0 + lane) * stride] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int i = 0; i < kB; ++i)
-      if (s0 + i < span.used) o[i] = po[(s0 + i) * (stride * (kKvqHd / 4))];
-    // a split whose sum is zero saw nothing (its m is -inf)
+      for (int i = 0; i < kB; ++i)
+        if (s0 + i < span.used) o[i] = po[(s0 + i) * (stride * (kKvqHd / 4))];
+    }
     const float w = x.y != 0.f ? ex2(x.x - m) : 0.f;
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
       if (s0 + i >= span.used) break;
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      l += wi * __shfl_sync(0xffffffffu, x.y, i);
+      const float wi = __shfl_sync(0xffffffffu, w, (s0 + i) & 31);
+      l += wi * __shfl_sync(0xffffffffu, x.y, (s0 + i) & 31);
       acc.x += wi * o[i].x;
       acc.y += wi * o[i].y;
       acc.z += wi * o[i].z;
@@ -874,6 +943,8 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   p->block = block;
   p->H = H;
   p->G = H / cache->n_kv_heads;
+  p->pos = 64 / p->G;
+  p->g_inv = (65536 + p->G - 1) / p->G;
   p->q = static_cast<const bf16*>(q);
   p->q_stride = q_row_stride;
   return DFLASH_OK;
@@ -930,8 +1001,7 @@ dflash_status dflash_kvq_attention(const dflash_kvq_cache* cache, int32_t batch,
     return DFLASH_E_CUDA;
   if (p.n_splits > 1) {
     const dim3 mg((unsigned)((rh + kMergeWarps - 1) / kMergeWarps));
-    if (launch_k(true, p.n_splits <= 8 ? kvq_merge_kernel<8> : kvq_merge_kernel<32>, mg,
-                 dim3(32 * kMergeWarps), 0, st, p) != cudaSuccess)
+    if (launch_k(true, kvq_merge_kernel, mg, dim3(32 * kMergeWarps), 0, st, p) != cudaSuccess)
       return DFLASH_E_CUDA;
   }
   return DFLASH_OK;
