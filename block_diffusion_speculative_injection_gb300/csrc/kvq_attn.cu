@@ -255,6 +255,32 @@ struct KvqMaps {
   CUtensorMap k, v;
 };
 
+// Bounded wait of a whole warp (every lane polls, so every lane has the
+// barrier's ordering): gives up after about 2 s, like mbar_wait, but looks at the
+// clock only once 4096 polls have failed (reading it costs more than most waits
+// here last).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 4095u) == 0) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 2000000000ull) break;
+    }
+  }
+  set_dev_status(status, kDevTimeout);
+  return false;
+}
+// one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __global__ void __launch_bounds__(kAttnQThreads, 2)
     kvq_attn_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
   pdl_wait();
@@ -350,80 +376,97 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       if (p.lse && h == 0) p.lse[grow * p.H + hr] = -INFINITY;
     }
   } else if (warp == 4) {
-    if (lane == 0) {
-      // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
-      // softmax does not see its slots)
+    // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
+    // softmax does not see its slots).  Whole warps wait, one lane issues: the
+    // addresses and descriptors stay in uniform registers.
+    const bool leader = elect_one();
+    if (leader) {
       tma_prefetch_desc(&maps.k);
       tma_prefetch_desc(&maps.v);
-      int k_issued = 0, v_issued = 0;
-      auto load = [&](int t, bool is_v, int pg) -> bool {
-        const int st = t % kAStages, ph = (t / kAStages) & 1;
-        uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st];
-        uint64_t* full = is_v ? &v_full[st] : &k_full[st];
-        if (t >= kAStages && !mbar_wait(empty, ph ^ 1, status)) return false;
+    }
+    int k_issued = 0, v_issued = 0;
+    auto load = [&](int t, bool is_v, int pg) -> bool {
+      const int st = t % kAStages, ph = (t / kAStages) & 1;
+      uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st];
+      uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+      if (t >= kAStages && !__all_sync(0xffffffffu, warp_wait(empty, ph ^ 1, status))) return false;
+      if (leader) {
         mbar_arrive_expect_tx(full, kTileBytes);
         tma_load_2d(sm + (is_v ? kAOffV : kAOffK) + st * kTileBytes, is_v ? &maps.v : &maps.k, 0,
                     (max(pg, 0) * p.c.Hkv + kvh) * kPageSlots, full);
-        return true;
-      };
-      int pg_k = kvq_page(p.c, seq, first_page), pg_v = 0;
-      for (int t = 0; t <= n_tiles; ++t) {
-        const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, first_page + t + 1) : 0;
-        if (t < n_tiles) {
-          if (pg_k < 0) set_dev_status(status, kDevCapacity);
-          if (!load(t, false, pg_k)) break;
-          k_issued = t + 1;
-        }
-        if (t >= 1) {
-          if (!load(t - 1, true, pg_v)) break;
-          v_issued = t;
-        }
-        pg_v = pg_k;
-        pg_k = pg_next;
       }
-      // every issued copy has landed before this thread leaves
-      for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
-        mbar_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
-      for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
-        mbar_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
+      __syncwarp();
+      return true;
+    };
+    int pg_k = kvq_page(p.c, seq, first_page), pg_v = 0;
+    for (int t = 0; t <= n_tiles; ++t) {
+      const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, first_page + t + 1) : 0;
+      if (t < n_tiles) {
+        if (pg_k < 0) set_dev_status(status, kDevCapacity);
+        if (!load(t, false, pg_k)) break;
+        k_issued = t + 1;
+      }
+      if (t >= 1) {
+        if (!load(t - 1, true, pg_v)) break;
+        v_issued = t;
+      }
+      pg_v = pg_k;
+      pg_k = pg_next;
     }
+    // every issued copy has landed before this warp leaves
+    for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
+      warp_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
+    for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
+      warp_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
     __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0) {
-      // ---- MMA issuer: S(t), then P V(t - 1)
-      constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
-      constexpr uint32_t id_o = idesc_e4m3_f32(128, kKvqHd) | kIdescBMajorMN;
-      const uint32_t qa = smem_u32(sm), pa = smem_u32(ps);
-      bool ok = mbar_wait(q_full, 0, status);
-      for (int t = 0; ok && t <= n_tiles; ++t) {
-        if (t < n_tiles) {
-          const int st = t % kAStages;
-          if (!mbar_wait(&k_full[st], (t / kAStages) & 1, status)) break;
-          if (t >= 1 && !mbar_wait(s_free, (t - 1) & 1, status)) break;
-          tc_fence_after();
-          const uint32_t ka = smem_u32(sm + kAOffK + st * kTileBytes);
+    // ---- MMA issuer: S(t), then P V(t - 1)
+    constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
+    constexpr uint32_t id_o = idesc_e4m3_f32(128, kKvqHd) | kIdescBMajorMN;
+    const uint64_t q_desc = sw128_desc(smem_u32(sm)), p_desc = sw128_desc(smem_u32(ps));
+    const uint64_t k_desc = sw128_desc(smem_u32(sm + kAOffK));
+    const uint64_t v_desc = sw128_desc_mn(smem_u32(sm + kAOffV), kTileBytes);
+    // (a descriptor's address field counts 16 bytes)
+    const bool leader = elect_one();
+    bool ok = __all_sync(0xffffffffu, warp_wait(q_full, 0, status));
+    for (int t = 0; ok && t <= n_tiles; ++t) {
+      if (t < n_tiles) {
+        const int st = t % kAStages;
+        ok = warp_wait(&k_full[st], (t / kAStages) & 1, status);
+        if (ok && t >= 1) ok = warp_wait(s_free, (t - 1) & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t kd = k_desc + st * (kTileBytes >> 4);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f8(tmem, sw128_desc(qa + part * kQPart + kk * 32), sw128_desc(ka + kk * 32), id_s,
+              tc_mma_f8(tmem, q_desc + part * (kQPart >> 4) + kk * 2, kd + kk * 2, id_s,
                         part + kk > 0 ? 1u : 0u);
           tc_commit(s_full);
           tc_commit(&k_empty[st]);
         }
-        if (t >= 1) {
-          const int u = t - 1, st = u % kAStages;
-          if (!mbar_wait(p_full, u & 1, status)) break;
-          if (!mbar_wait(&v_full[st], (u / kAStages) & 1, status)) break;
-          tc_fence_after();
-          const uint32_t va = smem_u32(sm + kAOffV + st * kTileBytes);
+        __syncwarp();
+      }
+      if (t >= 1) {
+        const int u = t - 1, st = u % kAStages;
+        ok = warp_wait(&v_full[st], (u / kAStages) & 1, status);
+        if (ok) ok = warp_wait(p_full, u & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t vd = v_desc + st * (kTileBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f8(tmem + kTmemOCol, sw128_desc(pa + kk * 32),
-                      sw128_desc_mn(va + kk * 32 * kKvqHd, kTileBytes), id_o, u + kk > 0 ? 1u : 0u);
+            tc_mma_f8(tmem + kTmemOCol, p_desc + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
+                      u + kk > 0 ? 1u : 0u);
           tc_commit(pv_done);
           tc_commit(&v_empty[st]);
         }
+        __syncwarp();
       }
     }
     __syncwarp();
@@ -511,17 +554,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       return make_uint2(*reinterpret_cast<const uint32_t*>(p.c.ex[0] + at),
                         *reinterpret_cast<const uint32_t*>(p.c.ex[1] + at));
     };
+    auto wait_for = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, warp_wait(bar, parity, status));
+    };
     // a barrier of the four warps whose wait is bounded like every other
     uint32_t met = 0;
     auto warps_meet = [&]() -> bool {
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(meet);
-        ok = mbar_wait(meet, met & 1, status);
-      }
-      ++met;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      ok = wait_for(meet, met++ & 1);
       return ok;
     };
     int pg = kvq_page(p.c, seq, first_page);
@@ -536,9 +577,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       ex = t + 1 < n_tiles ? exps_of(pg) : make_uint2(0u, 0u);
       const int stop = pg_now < 0 ? tile0 : k_stop;  // slots from here on are not seen
       const bool masked = tile0 + kTile > min(stop, mask_from);
-      if (lane == 0) ok = mbar_wait(s_full, t & 1, status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      if (!(ok = wait_for(s_full, t & 1))) break;
       float s[64];
       if (warp_live) {
         tc_fence_after();
@@ -573,11 +612,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       }
       // P V(t - 1) done: P is free, and O holds tiles 0 .. t - 1 (a warp without
       // rows waits too: its arrival below must not count for an earlier tile)
-      if (t > 0) {
-        if (lane == 0) ok = mbar_wait(pv_done, (t - 1) & 1, status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-      }
+      if (t > 0 && !(ok = wait_for(pv_done, (t - 1) & 1))) break;
       if (warp_live) {
         const bool grow_m = mx > m_used + kLazyLog2;
         if (__any_sync(0xffffffffu, grow_m)) {
@@ -632,9 +667,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       // that see them
       if (tile0 + kTile > min(stop, partial_from)) {
         const int st = t % kAStages;
-        if (lane == 0) ok = mbar_wait(&v_full[st], (t / kAStages) & 1, status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+        if (!(ok = wait_for(&v_full[st], (t / kAStages) & 1))) break;
         uint8_t* const vs = sm + kAOffV + st * kTileBytes;
         const int v_end = max(stop - tile0, 0), v_from = max(0, min(v_end, partial_from - tile0));
         for (int i = v_from * 8 + (int)threadIdx.x; i < kTile * 8; i += 128) {
@@ -684,11 +717,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k) bad[k] |= __shfl_xor_sync(0xffffffffu, bad[k], 16);
-    if (ok) {
-      const int u = n_tiles - 1;
-      if (lane == 0) ok = mbar_wait(pv_done, u & 1, status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
+    if (ok) ok = wait_for(pv_done, (n_tiles - 1) & 1);
     if (ok && warp_live) {
       tc_fence_after();
       const bool none = l == 0.f;
