@@ -126,13 +126,14 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 //   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB; two stages of K and two of
 //   V [128 slots][128], 16 KB each.  96 KB, so two CTAs share an SM: one's softmax
 //   runs beside the other's MMAs and loads.
-// Tensor memory: 256 columns, S [64 rows][128] and O [128 operand rows][128].  An
-// M = 64 accumulator keeps row m in lane (m / 16) * 32 + m % 16.
+// Tensor memory: 256 columns, S [64 rows][128] twice and O [128 operand rows][128].  An
+// M = 64 accumulator keeps row m in lane (m / 16) * 32 + m % 16, so a second one fits
+// into the other 16 lanes of each quarter: S of odd tiles starts at lane 16.
 //
 // Warps 0-3 (softmax): two threads per row (lanes t, t + 16), 64 slots each, held
 // in registers.  O and the sum are rescaled when the maximum grows by more
-// than a factor 16.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S of
-// the next tile before P V of this one.
+// than a factor 16.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S two
+// tiles ahead of P V.
 // A warp none of whose rows is in use only takes part in the barriers.
 // ---------------------------------------------------------------------------
 constexpr int kTile = kPageSlots;
@@ -150,6 +151,7 @@ static_assert(128 * kORow <= kAOffNan, "accumulator rows fit");
 constexpr int kAttnQSmem = (int)kAOffBar + 256 + 1024;  // barriers, alignment slack
 constexpr int kAttnQThreads = 192;
 constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
+constexpr uint32_t kSOdd = 16u << 16;  // lane offset of the S buffer of odd tiles
 // Growth of the maximum that is not yet rescaled: z <= 2^4.  (At a factor of 2, 58 %
 // of the warps' tiles rescaled O on 33-page splits, at 16 one in ten does; the headroom costs
 // p2 that many binades at the bottom.)
@@ -310,11 +312,11 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(sm + kAOffNan);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kAOffBar);
   uint64_t* const q_full = bars;
-  uint64_t* const s_full = bars + 1;
-  uint64_t* const s_free = bars + 2;
-  uint64_t* const p_full = bars + 3;
-  uint64_t* const pv_done = bars + 4;
-  uint64_t* const k_full = bars + 5;
+  uint64_t* const s_full = bars + 1;  // two S buffers
+  uint64_t* const s_free = bars + 3;
+  uint64_t* const p_full = bars + 5;
+  uint64_t* const pv_done = bars + 6;
+  uint64_t* const k_full = bars + 7;
   uint64_t* const k_empty = k_full + kAStages;
   uint64_t* const v_full = k_empty + kAStages;
   uint64_t* const v_empty = v_full + kAStages;
@@ -324,8 +326,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 4);
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+    }
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     mbar_init(meet, 4);
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       warp_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
     __syncwarp();
   } else if (warp == 5) {
-    // ---- MMA issuer: S(t), then P V(t - 1)
+    // ---- MMA issuer: S two tiles ahead of P V
     constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
     constexpr uint32_t id_o = idesc_e4m3_f32(128, kKvqHd) | kIdescBMajorMN;
     const uint64_t q_desc = sw128_desc(smem_u32(sm)), p_desc = sw128_desc(smem_u32(ps));
@@ -429,45 +433,46 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     // (a descriptor's address field counts 16 bytes)
     const bool leader = elect_one();
     bool ok = __all_sync(0xffffffffu, warp_wait(q_full, 0, status));
-    for (int t = 0; ok && t <= n_tiles; ++t) {
-      if (t < n_tiles) {
-        const int st = t % kAStages;
-        ok = warp_wait(&k_full[st], (t / kAStages) & 1, status);
-        if (ok && t >= 1) ok = warp_wait(s_free, (t - 1) & 1, status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t kd = k_desc + st * (kTileBytes >> 4);
+    auto scores = [&](int t) {
+      const int st = t % kAStages;
+      ok = warp_wait(&k_full[st], (t / kAStages) & 1, status);
+      if (ok && t >= 2) ok = warp_wait(&s_free[t & 1], ((t >> 1) - 1) & 1, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t kd = k_desc + st * (kTileBytes >> 4);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f8(tmem, q_desc + part * (kQPart >> 4) + kk * 2, kd + kk * 2, id_s,
-                        part + kk > 0 ? 1u : 0u);
-          tc_commit(s_full);
-          tc_commit(&k_empty[st]);
-        }
-        __syncwarp();
-      }
-      if (t >= 1) {
-        const int u = t - 1, st = u % kAStages;
-        ok = warp_wait(&v_full[st], (u / kAStages) & 1, status);
-        if (ok) ok = warp_wait(p_full, u & 1, status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t vd = v_desc + st * (kTileBytes >> 4);
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f8(tmem + kTmemOCol, p_desc + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
-                      u + kk > 0 ? 1u : 0u);
-          tc_commit(pv_done);
-          tc_commit(&v_empty[st]);
-        }
-        __syncwarp();
+            tc_mma_f8(tmem + (t & 1) * kSOdd, q_desc + part * (kQPart >> 4) + kk * 2, kd + kk * 2, id_s,
+                      part + kk > 0 ? 1u : 0u);
+        tc_commit(&s_full[t & 1]);
+        tc_commit(&k_empty[st]);
       }
+      __syncwarp();
+    };
+    if (ok) scores(0);
+    if (ok && n_tiles > 1) scores(1);
+    for (int t = 0; ok && t < n_tiles; ++t) {
+      const int st = t % kAStages;
+      ok = warp_wait(&v_full[st], (t / kAStages) & 1, status);
+      if (ok) ok = warp_wait(p_full, t & 1, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t vd = v_desc + st * (kTileBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f8(tmem + kTmemOCol, p_desc + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
+                    t + kk > 0 ? 1u : 0u);
+        tc_commit(pv_done);
+        tc_commit(&v_empty[st]);
+      }
+      __syncwarp();
+      if (t + 2 < n_tiles) scores(t + 2);
     }
     __syncwarp();
   } else {
@@ -577,17 +582,18 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       ex = t + 1 < n_tiles ? exps_of(pg) : make_uint2(0u, 0u);
       const int stop = pg_now < 0 ? tile0 : k_stop;  // slots from here on are not seen
       const bool masked = tile0 + kTile > min(stop, mask_from);
-      if (!(ok = wait_for(s_full, t & 1))) break;
+      if (!(ok = wait_for(&s_full[t & 1], (t >> 1) & 1))) break;
       float s[64];
       if (warp_live) {
         tc_fence_after();
-        tmem_ld_half32_nowait<64>(lane_base, reinterpret_cast<uint32_t*>(s));
-        tmem_ld_half32_nowait<64>(lane_base + 32, reinterpret_cast<uint32_t*>(s) + 32);
+        const uint32_t s_base = lane_base + (t & 1) * kSOdd;
+        tmem_ld_half32_nowait<64>(s_base, reinterpret_cast<uint32_t*>(s));
+        tmem_ld_half32_nowait<64>(s_base + 32, reinterpret_cast<uint32_t*>(s) + 32);
         tmem_wait_ld();
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);
+      if (lane == 0) mbar_arrive(&s_free[t & 1]);
       float ck[4], ev[4], mx = -INFINITY;
       if (warp_live) {
         if (masked) {
