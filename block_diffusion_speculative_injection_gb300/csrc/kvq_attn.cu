@@ -162,6 +162,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 1 / l to one or two units in the last place (l is a sum of weights, or NaN), and
+// log2 within 2^-22
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // bits below n set (n clamped to 0..32)
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
@@ -263,6 +270,7 @@ struct KvqMaps {
 // here last).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   uint64_t t0 = 0;
+#pragma unroll 1
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 4095u) == 0) {
@@ -403,6 +411,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       return true;
     };
     int pg_k = kvq_page(p.c, seq, first_page), pg_v = 0;
+#pragma unroll 1
     for (int t = 0; t <= n_tiles; ++t) {
       const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, first_page + t + 1) : 0;
       if (t < n_tiles) {
@@ -418,8 +427,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       pg_k = pg_next;
     }
     // every issued copy has landed before this warp leaves
+#pragma unroll 1
     for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
       warp_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
+#pragma unroll 1
     for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
       warp_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
     __syncwarp();
@@ -455,6 +466,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     };
     if (ok) scores(0);
     if (ok && n_tiles > 1) scores(1);
+#pragma unroll 1
     for (int t = 0; ok && t < n_tiles; ++t) {
       const int st = t % kAStages;
       ok = warp_wait(&v_full[st], (t / kAStages) & 1, status);
@@ -502,40 +514,51 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         for (int i = 0; i < 8; ++i)
           top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint4 now = q_raw[0];
-        const uint32_t bits = max(top[0] & 0xffffu, top[0] >> 16) << 16;
+      for (int i = 0; i < 8; i += 2) {  // two of the lane's eight rows, for overlap
+        uint4 now[2];
+        uint32_t bits[2], w1[2][4], w2[2][4];
+        int e[2];
 #pragma unroll
-        for (int k = 0; k < 7; ++k) {  // keeps the loop rolled
-          q_raw[k] = q_raw[k + 1];
-          top[k] = top[k + 1];
+        for (int r = 0; r < 2; ++r) {
+          now[r] = q_raw[r];
+          bits[r] = max(top[r] & 0xffffu, top[r] >> 16) << 16;
+          // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
+          // magnitude above 448 * 2^118 becomes NaN
+          e[r] = max(-80, (int)(bits[r] >> 23) - 127 - ((bits[r] & 0x7fffff) > 0x600000 ? 7 : 8));
         }
-        const int qr = warp * 16 + 2 * i + h;
-        // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
-        // magnitude above 448 * 2^118 becomes NaN
-        const int e = max(-80, (int)(bits >> 23) - 127 - ((bits & 0x7fffff) > 0x600000 ? 7 : 8));
-        const bool row_bad = e > 118;
-        const float sc = pow2i(-min(e, 118) - 8);
-        float x[8];
-        bf16x8_to_f(now, x);
-        uint32_t w1[4], w2[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __half2 y = __floats2half2_rn(x[2 * k] * sc, x[2 * k + 1] * sc);
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
-          const uint32_t d = u & 0xff80ff80u;
-          const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
-          w1[k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
-          w2[k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
+        for (int k = 0; k < 6; ++k) {  // keeps the loop rolled
+          q_raw[k] = q_raw[k + 2];
+          top[k] = top[k + 2];
         }
-        const uint32_t off = (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
-        *reinterpret_cast<uint2*>(sm + off) =
-            make_uint2(__byte_perm(w1[0], w1[1], 0x7531), __byte_perm(w1[2], w1[3], 0x7531));
-        *reinterpret_cast<uint2*>(sm + kQPart + off) =
-            make_uint2(__byte_perm(w2[0], w2[1], 0x7531), __byte_perm(w2[2], w2[3], 0x7531));
-        // a bad row: minus its scale
-        if (t16 == 0) q_scales[2 * i + h] = row_bad ? -kScaleLog2 : pow2i(e) * kScaleLog2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float sc = pow2i(-min(e[r], 118) - 8);
+            const uint32_t q2 = k == 0 ? now[r].x : k == 1 ? now[r].y : k == 2 ? now[r].z : now[r].w;
+            const __half2 y = __floats2half2_rn(__uint_as_float(q2 << 16) * sc,
+                                                __uint_as_float(q2 & 0xffff0000u) * sc);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
+            const uint32_t d = u & 0xff80ff80u;
+            const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
+            w1[r][k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
+            w2[r][k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int qr = warp * 16 + 2 * (i + r) + h;
+          const uint32_t off =
+              (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
+          *reinterpret_cast<uint2*>(sm + off) = make_uint2(__byte_perm(w1[r][0], w1[r][1], 0x7531),
+                                                           __byte_perm(w1[r][2], w1[r][3], 0x7531));
+          *reinterpret_cast<uint2*>(sm + kQPart + off) = make_uint2(
+              __byte_perm(w2[r][0], w2[r][1], 0x7531), __byte_perm(w2[r][2], w2[r][3], 0x7531));
+          // a bad row: minus its scale
+          if (t16 == 0)
+            q_scales[2 * (i + r) + h] = e[r] > 118 ? -kScaleLog2 : pow2i(e[r]) * kScaleLog2;
+        }
       }
     }
     fence_proxy_async_smem();
@@ -573,6 +596,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     int pg = kvq_page(p.c, seq, first_page);
     int pg_next = n_tiles > 1 ? kvq_page(p.c, seq, first_page + 1) : -1;
     uint2 ex = exps_of(pg);
+#pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
       const int tile0 = k_begin + t * kTile;
       const int pg_now = pg;
@@ -676,6 +700,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         if (!(ok = wait_for(&v_full[st], (t / kAStages) & 1))) break;
         uint8_t* const vs = sm + kAOffV + st * kTileBytes;
         const int v_end = max(stop - tile0, 0), v_from = max(0, min(v_end, partial_from - tile0));
+#pragma unroll 1
         for (int i = v_from * 8 + (int)threadIdx.x; i < kTile * 8; i += 128) {
           const int vr = i >> 3, ch = i & 7;
           uint4* const at = reinterpret_cast<uint4*>(vs + vr * 128 + ((ch ^ (vr & 7)) << 4));
@@ -700,8 +725,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         }
         if (!warps_meet()) break;
         if (*nan_any) {
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t vis = visible32(p, tile0 + 64 * h + 32 * c, stop, ctx, jr, anc);
+#pragma unroll 1
             while (vis) {
               const int at = 64 * h + 32 * c + __ffs(vis) - 1;
               vis &= vis - 1;
@@ -742,14 +769,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         for (int i = 0; i < 8; ++i) at[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
       const long long rh = grow * p.H + hr;
+      const long long part_row = (long long)split * p.batch * p.block * p.H + rh;
+      const long long out_at = (whole ? rh : part_row) * kKvqHd;
       if (live && h == 0) {
         if (!whole)
-          *reinterpret_cast<float2*>(p.part_ml + ((long long)split * p.batch * p.block * p.H + rh) * 2) =
-              make_float2(m_used, l);
+          *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(m_used, l);
         else if (p.lse)
-          p.lse[rh] = none ? -INFINITY : (m_used + log2f(l)) * kLn2;
+          p.lse[rh] = none ? -INFINITY : (m_used + __log2f(l)) * kLn2;
       }
-      const float scale = none ? 0.f : (whole ? 1.f / l : 1.f);
+      const float scale = none ? 0.f : (whole ? rcp(l) : 1.f);
       const bool any_bad = __any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u);
       const int n_live = __popc(__ballot_sync(0xffffffffu, live) & 0xffffu);  // rows 0 .. n_live - 1
       __syncwarp();
@@ -758,9 +786,9 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         const float4 x = *reinterpret_cast<const float4*>(stage + i * kORow + 16 * lane);
         const float4 y = *reinterpret_cast<const float4*>(stage + (16 + i) * kORow + 16 * lane);
         const float sc = __shfl_sync(0xffffffffu, scale, i);
-        const long long at = __shfl_sync(0xffffffffu, rh, i) * kKvqHd + 4 * lane;
+        const long long at = __shfl_sync(0xffffffffu, out_at, i) + 4 * lane;
         const float s1 = sc * (1.f / 16), s2 = sc * (1.f / 256);
-        // (a row that saw nothing has sc = 0, and no NaN: its weights were zero)
+        // (a row that saw nothing has sc = 0: zeros, not 0 * NaN)
         float4 v = make_float4(x.x * s1 + y.x * s2, x.y * s1 + y.y * s2, x.z * s1 + y.z * s2,
                                x.w * s1 + y.w * s2);
         if (sc == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -783,7 +811,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           w.y = *reinterpret_cast<const uint32_t*>(&hi);
           *reinterpret_cast<uint2*>(p.out + at) = w;
         } else {
-          *reinterpret_cast<float4*>(p.part_o + (long long)split * p.batch * p.block * p.H * kKvqHd + at) = v;
+          *reinterpret_cast<float4*>(p.part_o + at) = v;
         }
       }
     }
@@ -794,23 +822,23 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
 }
 
 // Merge of the splits of a row: one warp per (row, head), lane l holding dims
-// 4 l .. 4 l + 3.  The used splits' (m, l) sit one a lane, their outputs are loaded eight
+// 4 l .. 4 l + 3.  The used splits' (m, l) sit one a lane, their outputs are loaded sixteen
 // at a time; sums run in split order.
 constexpr int kMergeWarps = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAttnK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const long long rh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const long long rows = (long long)p.batch * p.block, stride = rows * p.H;
+  // (rows x heads of a launch are below 2^31)
+  const int rh = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int64_t stride = (int64_t)p.batch * p.block * p.H;
   if (rh >= stride) return;
-  const long long row = rh / p.H;
-  const int b = (int)(row / p.block), j = (int)(row % p.block);
+  const int row = rh / p.H, b = row / p.block, j = row - b * p.block;
   const float2* const ml = reinterpret_cast<const float2*>(p.part_ml) + rh;
-  const float4* const po = reinterpret_cast<const float4*>(p.part_o + rh * kKvqHd) + lane;
+  const float4* const po = reinterpret_cast<const float4*>(p.part_o + (int64_t)rh * kKvqHd) + lane;
   // the first splits are read before it is known how many are used (the
   // partials of all of them are in bounds)
-  constexpr int kB = 8;
+  constexpr int kB = 16;
   float4 o[kB];
 #pragma unroll
   for (int i = 0; i < kB; ++i)
@@ -823,6 +851,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   if (span.used <= 1) return;  // written whole
   // a split whose sum is zero saw nothing (its m is -inf)
   float m = lane < span.used && x.y != 0.f ? x.x : -INFINITY;
+#pragma unroll 1
   for (int s = lane + 32; s < span.used; s += 32) {
     const float2 y = ml[s * stride];
     if (y.y != 0.f) m = fmaxf(m, y.x);
@@ -832,6 +861,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   if (m == -INFINITY) m = 0.f;
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
   for (int s0 = 0; s0 < span.used; s0 += kB) {
     if (s0 > 0) {
       if ((s0 & 31) == 0)
@@ -852,14 +882,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
       acc.w += wi * o[i].w;
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : rcp(l);
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 c = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 pk;
   pk.x = *reinterpret_cast<const uint32_t*>(&a);
   pk.y = *reinterpret_cast<const uint32_t*>(&c);
-  *reinterpret_cast<uint2*>(p.out + rh * kKvqHd + lane * 4) = pk;
-  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(p.out + (int64_t)rh * kKvqHd + lane * 4) = pk;
+  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
 // Splits of a launch of `ctas` CTAs over max_keys slots: the count that minimises
