@@ -26,7 +26,7 @@ struct KvqAttnK {
   float* score_out;
   float decay;
   int pos, g_inv;  // block positions of a CTA's 64 rows; row / G = row * g_inv >> 16 (row < 64)
-  int n_splits;
+  int q_tiles, n_splits;
   float *part_o, *part_ml;  // [split][row][head][128], [split][row][head] (m, l)
 };
 
@@ -260,6 +260,120 @@ __device__ __forceinline__ uint32_t visible32(const KvqAttnK& p, int kb, int sto
   return m & (bits_below(ctx - kb) | t);
 }
 
+// The 16 query rows of a warp, from global memory: two rows a load, lane l holds dims
+// 8 (l % 16) .. of row 2 i + l / 16 in raw[i].  Rows past a sequence's count are in
+// bounds (j < block) and dropped later.
+__device__ __forceinline__ void load_q(const KvqAttnK& p, int b, int kvh, int j0, int warp, int lane,
+                                       uint4* raw) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = warp * 16 + 2 * i + (lane >> 4), g = row_pos(p, row), j = j0 + g;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < p.pos * p.G && j < p.block)
+      raw[i] = *reinterpret_cast<const uint4*>(p.q + ((long long)b * p.block + j) * p.q_stride +
+                                               (kvh * p.G + row - g * p.G) * kKvqHd +
+                                               8 * (lane & 15));
+  }
+}
+
+// Those rows in two e4m3 parts, to dst [64][128] and dst + kQPart (128-byte
+// swizzle), and their scales 2^a log2(e) / sqrt(128) (minus that for a row with a
+// NaN, an infinity or a magnitude above 448 * 2^118: such a row is NaN).
+// y = q 2^-(a + 8) in fp16 is exact but for elements below 2^-15 of the largest; an
+// fp16 below 2 is an e4m3 code times 2^8 with three more significand bits, so the
+// parts come out of integer operations on its bits.
+__device__ __forceinline__ void convert_q(uint4* q_raw, int warp, int lane, uint8_t* dst,
+                                          float* q_scales) {
+  const int t16 = lane & 15, h = lane >> 4;
+        // largest magnitude of each row, on bf16 pairs (as integers, NaN above all)
+        uint32_t top[8];
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          constexpr uint32_t abs2 = 0x7fff7fffu;
+          top[i] = __vimax3_u16x2(q_raw[i].x & abs2, q_raw[i].y & abs2, q_raw[i].z & abs2);
+          top[i] = __vmaxu2(top[i], q_raw[i].w & abs2);
+        }
+  #pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+  #pragma unroll
+          for (int i = 0; i < 8; ++i)
+            top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+  #pragma unroll 1
+        for (int i = 0; i < 8; i += 2) {  // two of the lane's eight rows, for overlap
+          uint4 now[2];
+          uint32_t bits[2], w1[2][4], w2[2][4];
+          int e[2];
+  #pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            now[r] = q_raw[r];
+            bits[r] = max(top[r] & 0xffffu, top[r] >> 16) << 16;
+            // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
+            // magnitude above 448 * 2^118 becomes NaN
+            e[r] = max(-80, (int)(bits[r] >> 23) - 127 - ((bits[r] & 0x7fffff) > 0x600000 ? 7 : 8));
+          }
+  #pragma unroll
+          for (int k = 0; k < 6; ++k) {  // keeps the loop rolled
+            q_raw[k] = q_raw[k + 2];
+            top[k] = top[k + 2];
+          }
+  #pragma unroll
+          for (int k = 0; k < 4; ++k)
+  #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float sc = pow2i(-min(e[r], 118) - 8);
+              const uint32_t q2 = k == 0 ? now[r].x : k == 1 ? now[r].y : k == 2 ? now[r].z : now[r].w;
+              const __half2 y = __floats2half2_rn(__uint_as_float(q2 << 16) * sc,
+                                                  __uint_as_float(q2 & 0xffff0000u) * sc);
+              const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
+              const uint32_t d = u & 0xff80ff80u;
+              const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
+              w1[r][k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
+              w2[r][k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
+            }
+  #pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int qr = warp * 16 + 2 * (i + r) + h;
+            const uint32_t off =
+                (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
+            *reinterpret_cast<uint2*>(dst + off) = make_uint2(__byte_perm(w1[r][0], w1[r][1], 0x7531),
+                                                             __byte_perm(w1[r][2], w1[r][3], 0x7531));
+            *reinterpret_cast<uint2*>(dst + kQPart + off) = make_uint2(
+                __byte_perm(w2[r][0], w2[r][1], 0x7531), __byte_perm(w2[r][2], w2[r][3], 0x7531));
+            // a bad row: minus its scale
+            if (t16 == 0)
+              q_scales[2 * (i + r) + h] = e[r] > 118 ? -kScaleLog2 : pow2i(e[r]) * kScaleLog2;
+          }
+        }
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b));
+  return r;
+}
+
+// Rows of the q tile from block position j0 on that see block slot i (r rows in the
+// sequence), a bit each.
+__device__ __forceinline__ uint64_t score_rows_seeing(const KvqAttnK& p, int b, int i, int j0, int r) {
+  if (p.mask == DFLASH_MASK_CAUSAL) {
+    const int from = max(i - j0, 0);  // positions from here on
+    return from >= p.pos ? 0ull : ~0ull << (from * p.G);
+  }
+  uint64_t v = 0;
+  if ((i >> 6) >= p.anc_words) return 0;
+  const uint64_t* const a = p.anc + (long long)b * p.block * p.anc_words + (i >> 6);
+  const uint64_t head = p.G == 64 ? ~0ull : (1ull << p.G) - 1;
+#pragma unroll 1
+  for (int q = 0; q < p.pos && j0 + q < r; ++q)
+    if ((a[(long long)(j0 + q) * p.anc_words] >> (i & 63)) & 1ull) v |= head << (q * p.G);
+  return v;
+}
+
 struct KvqMaps {
   CUtensorMap k, v;
 };
@@ -303,18 +417,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   const int kvh = blockIdx.y, j0 = blockIdx.x * POS;
   int32_t* const status = p.c.status;
   const KvqEntry entry = kvq_entry_load(p, b);
-  // the query rows of a softmax warp, two a load (eight dims a lane); rows past the
-  // sequence's are in bounds (j < block) and dropped later
+  // the query rows' loads, under way during the set-up
   const int t16 = lane & 15, h = lane >> 4;
   uint4 q_raw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int qr = warp * 16 + 2 * i + h, qg = row_pos(p, qr), qj = j0 + qg;
-    q_raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (warp < 4 && qr < POS * p.G && qj < p.block)
-      q_raw[i] = *reinterpret_cast<const uint4*>(p.q + ((long long)b * p.block + qj) * p.q_stride +
-                                                 (kvh * p.G + qr - qg * p.G) * kKvqHd + 8 * t16);
-  }
+  if (warp < 4) load_q(p, b, kvh, j0, warp, lane, q_raw);
 
   uint8_t* const ps = sm + kAOffP;
   uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(sm + kAOffNan);
@@ -494,73 +600,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     const uint64_t* const anc =
         p.mask == DFLASH_MASK_TREE ? p.anc + (live ? grow : (long long)b * p.block + j0) * p.anc_words
                                    : nullptr;
-    // The warp's 16 query rows in two e4m3 parts.  y = q 2^-(a + 8) in fp16 is exact but
-    // for elements below 2^-15 of the largest; an fp16 below 2 is an e4m3 code
-    // times 2^8 with three more significand bits, so the parts come out of
-    // integer operations on its bits.
     float* const q_scales = reinterpret_cast<float*>(sm + kAOffQs) + warp * 16;
-    if (warp_live) {
-      // largest magnitude of each row, on bf16 pairs (as integers, NaN above all)
-      uint32_t top[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        constexpr uint32_t abs2 = 0x7fff7fffu;
-        top[i] = __vimax3_u16x2(q_raw[i].x & abs2, q_raw[i].y & abs2, q_raw[i].z & abs2);
-        top[i] = __vmaxu2(top[i], q_raw[i].w & abs2);
-      }
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
-#pragma unroll 1
-      for (int i = 0; i < 8; i += 2) {  // two of the lane's eight rows, for overlap
-        uint4 now[2];
-        uint32_t bits[2], w1[2][4], w2[2][4];
-        int e[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          now[r] = q_raw[r];
-          bits[r] = max(top[r] & 0xffffu, top[r] >> 16) << 16;
-          // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
-          // magnitude above 448 * 2^118 becomes NaN
-          e[r] = max(-80, (int)(bits[r] >> 23) - 127 - ((bits[r] & 0x7fffff) > 0x600000 ? 7 : 8));
-        }
-#pragma unroll
-        for (int k = 0; k < 6; ++k) {  // keeps the loop rolled
-          q_raw[k] = q_raw[k + 2];
-          top[k] = top[k + 2];
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float sc = pow2i(-min(e[r], 118) - 8);
-            const uint32_t q2 = k == 0 ? now[r].x : k == 1 ? now[r].y : k == 2 ? now[r].z : now[r].w;
-            const __half2 y = __floats2half2_rn(__uint_as_float(q2 << 16) * sc,
-                                                __uint_as_float(q2 & 0xffff0000u) * sc);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
-            const uint32_t d = u & 0xff80ff80u;
-            const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
-            w1[r][k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
-            w2[r][k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
-          }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int qr = warp * 16 + 2 * (i + r) + h;
-          const uint32_t off =
-              (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
-          *reinterpret_cast<uint2*>(sm + off) = make_uint2(__byte_perm(w1[r][0], w1[r][1], 0x7531),
-                                                           __byte_perm(w1[r][2], w1[r][3], 0x7531));
-          *reinterpret_cast<uint2*>(sm + kQPart + off) = make_uint2(
-              __byte_perm(w2[r][0], w2[r][1], 0x7531), __byte_perm(w2[r][2], w2[r][3], 0x7531));
-          // a bad row: minus its scale
-          if (t16 == 0)
-            q_scales[2 * (i + r) + h] = e[r] > 118 ? -kScaleLog2 : pow2i(e[r]) * kScaleLog2;
-        }
-      }
-    }
+    if (warp_live) convert_q(q_raw, warp, lane, sm, q_scales);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
@@ -928,44 +969,270 @@ static int kvq_sms() {
 
 static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64 / G); }
 
-// one warp per (sequence, KV head, slot): the rows in order
-__global__ void __launch_bounds__(128) kvq_score_kernel(const KvqAttnK p) {
-  pdl_trigger();
+// ---------------------------------------------------------------------------
+// Accumulated weights.  The same product the other way round: S^T = K Q^T, a page of
+// 128 slots as the M = 128 operand, 64 query rows (in their two e4m3 parts) as the
+// other, so a thread owns a slot and sums the weights of its row of 64 scores
+// without talking to another.  K alone is read, once: 128 bytes a slot and head.
+//
+// One CTA: a span of pages of one sequence and KV head, in groups of four; for each
+// group all q tiles in turn (one, unless a pass has more than 64 rows a KV head), so
+// the weights of a slot are summed in one register in a fixed order.
+// Shared memory: K ring [4][128][128], Q [2 buffers][2 parts][64][128], the rows'
+// (scale, log2 lse).  Tensor memory: four S^T tiles [128 slots][64 rows], one per
+// page of the group; two CTAs share an SM.
+// Warps 0-3: the rows' conversion (for the next q tile ahead of this one's sums),
+// weights and sums; warp 4: TMA of K; warp 5: MMAs.
+// ---------------------------------------------------------------------------
+constexpr int kSGroup = 4;
+constexpr uint32_t kSOffQ = kSGroup * kTileBytes;
+constexpr uint32_t kSOffRow = kSOffQ + 2 * 2 * kQPart;   // [3][64] float2
+constexpr uint32_t kSOffQs = kSOffRow + 3 * 64 * 8;      // [64] float, conversion scratch
+constexpr uint32_t kSOffBar = kSOffQs + 64 * 4;
+constexpr int kScoreSmem = (int)kSOffBar + 256 + 1024;
+constexpr uint32_t kScoreTmem = 256;
+
+__global__ void __launch_bounds__(kAttnQThreads, 2)
+    kvq_score_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
   pdl_wait();
-  const int k = blockIdx.x * 4 + (threadIdx.x >> 5), kvh = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31;
-  int seq, n, r, key_end;
-  if (!kvq_entry(p, b, seq, n, r, key_end)) return;
-  for (int s0 = k; s0 < key_end; s0 += gridDim.x * 4) {
-    const int page = kvq_page(p.c, seq, s0 / kPageSlots);
-    float w = 0.f;
-    if (page < 0) {
-      set_dev_status(p.c.status, kDevCapacity);
-    } else {
-      const int64_t ph = kvq_ph(p.c, page, kvh);
-      const int i = s0 % kPageSlots;
-      const float4 kk =
-          decode4(*reinterpret_cast<const uint32_t*>(p.c.c8[0] + ph * kKvqPageBytes + i * kKvqHd +
-                                                     lane * 4));
-      const float sc = pow2i(p.c.ex[0][ph * kKvqSubs + i / kKvqSub]) * kScaleLog2;
-      for (int j = 0; j < r; ++j) {
-        const long long row = (long long)b * p.block + j;
-        if (!kvq_sees(p, s0, n, r, j, p.mask == DFLASH_MASK_TREE ? p.anc + row * p.anc_words : nullptr))
-          continue;
-        for (int g = 0; g < p.G; ++g) {
-          const int h = kvh * p.G + g;
-          const float lse = p.lse[row * p.H + h];
-          if (lse == -INFINITY) continue;
-          const float4 q = load_q4(p.q + row * p.q_stride + h * kKvqHd + lane * 4);
-          w += exp2f(dot4(q, kk) * sc - lse * kLog2e);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  int32_t* const status = p.c.status;
+  const KvqEntry entry = kvq_entry_load(p, b);
+  uint4 q_raw[8];
+  if (warp < 4 && p.q_tiles == 1) load_q(p, b, kvh, 0, warp, lane, q_raw);
+
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kSOffBar);
+  uint64_t* const q_full = bars;
+  uint64_t* const k_full = bars + 1;
+  uint64_t* const k_empty = k_full + kSGroup;
+  uint64_t* const d_full = k_empty + kSGroup;
+  uint64_t* const d_free = d_full + kSGroup;
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(d_free + kSGroup);
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    for (int i = 0; i < kSGroup; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_free[i], 4);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(tslot, kScoreTmem);
+    tmem_relinquish();
+  }
+  int key_end;
+  const bool work = kvq_entry_check(p, entry, key_end);
+  const int seq = entry.seq, n = entry.n, r = entry.r, ctx = n - r;
+  const int tiles = work ? (key_end + kTile - 1) / kTile : 0;
+  const int per = max(1, (tiles + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int t_begin = blockIdx.x * per, t_end = min(tiles, t_begin + per);
+  const int n_tiles = max(0, t_end - t_begin);
+  // q tiles that can see a slot from `tile` on (causal: rows j >= slot - ctx)
+  const int q_tiles = (r + p.pos - 1) / p.pos;
+  auto q_first = [&](int tile) -> int {
+    if (p.mask != DFLASH_MASK_CAUSAL) return 0;
+    return min(max(0, tile * kTile - ctx) / p.pos, q_tiles);
+  };
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // every CTA holds its tensor memory (see kvq_attn_kernel)
+  const uint32_t tmem = *tslot;
+
+  if (n_tiles == 0) {
+  } else if (warp == 4) {
+    // ---- producer: page t of the span into stage t % 4
+    const bool leader = elect_one();
+    if (leader) tma_prefetch_desc(&maps.k);
+    int issued = 0;
+    int pg = kvq_page(p.c, seq, t_begin);
+#pragma unroll 1
+    for (int t = 0; t < n_tiles; ++t) {
+      const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, t_begin + t + 1) : 0;
+      const int st = t % kSGroup;
+      if (t >= kSGroup &&
+          !__all_sync(0xffffffffu, warp_wait(&k_empty[st], ((t / kSGroup) - 1) & 1, status)))
+        break;
+      if (pg < 0) set_dev_status(status, kDevCapacity);
+      if (leader) {
+        mbar_arrive_expect_tx(&k_full[st], kTileBytes);
+        tma_load_2d(sm + st * kTileBytes, &maps.k, 0, (max(pg, 0) * p.c.Hkv + kvh) * kPageSlots,
+                    &k_full[st]);
+      }
+      __syncwarp();
+      issued = t + 1;
+      pg = pg_next;
+    }
+#pragma unroll 1
+    for (int t = max(0, issued - kSGroup); t < issued; ++t)
+      warp_wait(&k_full[t % kSGroup], (t / kSGroup) & 1, status);
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---- MMA issuer
+    const uint32_t cols = (uint32_t)min(64, (min(p.block, p.pos) * p.G + 15) / 16 * 16);
+    const uint32_t id = idesc_e4m3_f32(128, 0) | ((cols >> 3) << 17);
+    const uint64_t k_desc = sw128_desc(smem_u32(sm)), q_desc = sw128_desc(smem_u32(sm + kSOffQ));
+    const bool leader = elect_one();
+    bool ok = true;
+    int conv = 0;          // conversions used so far
+    uint32_t used[kSGroup] = {0u, 0u, 0u, 0u};  // times each S^T tile was written
+#pragma unroll 1
+    for (int g = 0; ok && g < n_tiles; g += kSGroup) {
+      const int members = min(kSGroup, n_tiles - g);
+      const int q0 = q_first(t_begin + g);
+#pragma unroll 1
+      for (int qt = q0; ok && qt < max(q_tiles, q0 + 1); ++qt) {
+        // (a group no row sees still passes its pages through, with no q tile)
+        const bool any = qt < q_tiles;
+        if (any && (p.q_tiles > 1 || conv == 0)) {
+          ok = __all_sync(0xffffffffu, warp_wait(q_full, conv & 1, status));
+          ++conv;
+        }
+        const int buf = p.q_tiles > 1 ? (conv - 1) & 1 : 0;
+#pragma unroll
+        for (int m = 0; m < kSGroup; ++m) {
+          if (!ok || m >= members) continue;
+          if (qt == q0) ok = warp_wait(&k_full[m], (g / kSGroup) & 1, status);
+          if (ok && any && used[m] > 0) ok = warp_wait(&d_free[m], (used[m] - 1) & 1, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+          tc_fence_after();
+          const bool last = qt + 1 >= q_tiles;
+          if (leader) {
+            if (any) {
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_f8(tmem + m * 64, k_desc + m * (kTileBytes >> 4) + kk * 2,
+                            q_desc + (buf * 2 + part) * (kQPart >> 4) + kk * 2, id,
+                            part + kk > 0 ? 1u : 0u);
+              tc_commit(&d_full[m]);
+            }
+            if (last) tc_commit(&k_empty[m]);
+          }
+          __syncwarp();
+          if (any) ++used[m];
         }
       }
     }
-    if (lane == 0) {
-      const int64_t at = ((int64_t)seq * p.c.Hkv + kvh) * ((int64_t)p.c.pps * kPageSlots) + s0;
-      p.score_out[at] = (p.score_in ? p.decay * p.score_in[at] : 0.f) + w;
+    __syncwarp();
+  } else {
+    // ---- weights: thread = slot of the page
+    const int slot = warp * 32 + lane;
+    float* const q_scales = reinterpret_cast<float*>(sm + kSOffQs) + warp * 16;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    bool ok = true;
+    int conv = 0;
+    // q tile qt into Q buffer conv % 2 (its MMAs of two tiles ago are done: this warp
+    // has seen their results) and row buffer conv % 3 (a slower warp may still read
+    // those of two tiles ago, but not older ones: it has converted the last tile)
+    auto convert = [&](int qt) {
+      const int buf = conv & 1, j0 = qt * p.pos;
+      if (p.q_tiles > 1) load_q(p, b, kvh, j0, warp, lane, q_raw);
+      convert_q(q_raw, warp, lane, sm + kSOffQ + buf * 2 * kQPart, q_scales);
+      __syncwarp();
+      if (lane < 16) {
+        const int row = warp * 16 + lane, pos = row_pos(p, row), j = j0 + pos;
+        float2 v = make_float2(0.f, INFINITY);  // weight 2^-inf = 0
+        if (row < p.pos * p.G && j < r) {
+          const float sc = q_scales[lane];
+          const float lse = p.lse[((long long)b * p.block + j) * p.H + kvh * p.G + row - pos * p.G];
+          v.x = fabsf(sc);
+          v.y = sc < 0.f ? __int_as_float(0x7fffffff) : lse == -INFINITY ? INFINITY : lse * kLog2e;
+        }
+        reinterpret_cast<float2*>(sm + kSOffRow)[conv % 3 * 64 + row] = v;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      ++conv;
+    };
+    uint32_t used[kSGroup] = {0u, 0u, 0u, 0u};
+    const int chunks = (min(min(p.block, p.pos) * p.G, 64) + 15) / 16;
+#pragma unroll 1
+    for (int g = 0; ok && g < n_tiles; g += kSGroup) {
+      const int members = min(kSGroup, n_tiles - g);
+      const int q0 = q_first(t_begin + g);
+      float acc[kSGroup] = {0.f, 0.f, 0.f, 0.f};
+      float kscale[kSGroup];
+      bool mapped[kSGroup];
+#pragma unroll
+      for (int m = 0; m < kSGroup; ++m) {
+        const int pg = m < members ? kvq_page(p.c, seq, t_begin + g + m) : -1;
+        mapped[m] = pg >= 0;
+        kscale[m] =
+            pg >= 0 ? pow2i(p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]) : 0.f;
+      }
+      if (q0 < q_tiles && (p.q_tiles > 1 || conv == 0)) convert(q0);
+#pragma unroll 1
+      for (int qt = q0; ok && qt < q_tiles; ++qt) {
+        const int rbuf = (conv - 1) % 3;
+        // the rows' scales of all four warps
+        ok = __all_sync(0xffffffffu, warp_wait(q_full, (conv - 1) & 1, status));
+        if (!ok) break;
+        if (p.q_tiles > 1 && qt + 1 < q_tiles) convert(qt + 1);
+        const float4* const rows = reinterpret_cast<const float4*>(sm + kSOffRow) + rbuf * 32;
+        const int j0 = qt * p.pos;
+#pragma unroll
+        for (int m = 0; m < kSGroup; ++m) {
+          if (!ok || m >= members) continue;
+          ok = __all_sync(0xffffffffu, warp_wait(&d_full[m], used[m] & 1, status));
+          ++used[m];
+          if (!ok) continue;
+          tc_fence_after();
+          const int k = (t_begin + g + m) * kTile + slot;  // the thread's slot
+          // rows that see it, a bit each
+          const bool masked =
+              p.mask != DFLASH_MASK_NONE && (t_begin + g + m + 1) * kTile > ctx + (p.mask == DFLASH_MASK_CAUSAL ? j0 + 1 : 0);
+          uint64_t vis = ~0ull;
+          if (masked && k >= ctx) vis = score_rows_seeing(p, b, k - ctx, j0, r);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float s[16];
+            tmem_ld16(lane_base + m * 64 + 16 * c, s);
+            const uint32_t v16 = (uint32_t)(vis >> (16 * c));
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 rw = rows[8 * c + i / 2];
+              float2 x = mul2(make_float2(s[i], s[i + 1]), kscale[m]);
+              x.x = ex2(fmaf(x.x, rw.x, -rw.y));
+              x.y = ex2(fmaf(x.y, rw.z, -rw.w));
+              if (masked) {
+                x.x = (v16 >> i) & 1u ? x.x : 0.f;
+                x.y = (v16 >> i) & 2u ? x.y : 0.f;
+              }
+              sum = add2(sum, x);
+            }
+          }
+          acc[m] += sum.x + sum.y;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_free[m]);
+        }
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int m = 0; m < kSGroup; ++m) {
+        const int k = (t_begin + g + m) * kTile + slot;
+        if (m < members && k < key_end) {
+          const int64_t at = ((int64_t)seq * p.c.Hkv + kvh) * ((int64_t)p.c.pps * kPageSlots) + k;
+          const float old = p.score_in ? p.decay * p.score_in[at] : 0.f;
+          p.score_out[at] = mapped[m] ? old + acc[m] : old;
+        }
+      }
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tmem_dealloc(tmem, kScoreTmem);
 }
 
 static bool kvq_attn_shape_ok(int batch, int H, int Hkv, int block, int max_keys) {
@@ -1009,6 +1276,7 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   p->H = H;
   p->G = H / cache->n_kv_heads;
   p->pos = 64 / p->G;
+  p->q_tiles = (block + p->pos - 1) / p->pos;
   p->g_inv = (65536 + p->G - 1) / p->G;
   p->q = static_cast<const bf16*>(q);
   p->q_stride = q_row_stride;
@@ -1090,8 +1358,17 @@ dflash_status dflash_kvq_score(const dflash_kvq_cache* cache, int32_t batch, int
   p.decay = decay;
   p.score_in = score_in;
   p.score_out = score_out;
-  const dim3 grid((unsigned)((max_keys + 3) / 4), cache->n_kv_heads, batch);
-  if (launch_k(true, kvq_score_kernel, grid, dim3(128), 0, (cudaStream_t)stream, p) != cudaSuccess)
+  // spans of pages: as for the attention's splits
+  const int splits = kvq_plan_splits(kvq_sms(), (int64_t)cache->n_kv_heads * batch, max_keys, 65535);
+  KvqMaps maps;
+  const uint64_t kv_rows = (uint64_t)cache->n_pages * cache->n_kv_heads * kPageSlots;
+  if (!encode_tmap_rows128(&maps.k, cache->k8_dev, kv_rows, kTile)) return DFLASH_E_CUDA;
+  maps.v = maps.k;
+  static std::atomic<bool> smem_done[kMaxDevices];
+  if (ensure_smem_attr(smem_done, kvq_score_kernel, kScoreSmem) != cudaSuccess) return DFLASH_E_CUDA;
+  const dim3 grid(splits, cache->n_kv_heads, batch);
+  if (launch_k(true, kvq_score_kernel, grid, dim3(kAttnQThreads), kScoreSmem, (cudaStream_t)stream,
+               maps, p) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
