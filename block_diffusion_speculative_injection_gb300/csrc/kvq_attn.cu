@@ -379,15 +379,23 @@ struct KvqMaps {
 };
 
 // Bounded wait of a whole warp (every lane polls, so every lane has the
-// barrier's ordering): gives up after about 2 s, like mbar_wait, but looks at the
-// clock only once 4096 polls have failed (reading it costs more than most waits
-// here last).
+// barrier's ordering): gives up after about 2 s, like mbar_wait.  A poll may suspend
+// the warp for up to 20 us (a hint), so a waiting warp leaves its issue slots to
+// the others, and the clock is read only after such a poll has failed.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 4095u) == 0) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15u) == 0) {
       const uint64_t now = global_ns();
       if (t0 == 0) t0 = now;
       if (now - t0 > 2000000000ull) break;
@@ -988,7 +996,8 @@ constexpr int kSGroup = 4;
 constexpr uint32_t kSOffQ = kSGroup * kTileBytes;
 constexpr uint32_t kSOffRow = kSOffQ + 2 * 2 * kQPart;   // [3][64] float2
 constexpr uint32_t kSOffQs = kSOffRow + 3 * 64 * 8;      // [64] float, conversion scratch
-constexpr uint32_t kSOffBar = kSOffQs + 64 * 4;
+constexpr uint32_t kSOffSlot = kSOffQs + 64 * 4;         // [4][128] float2: K's scale, the sum
+constexpr uint32_t kSOffBar = kSOffSlot + kSGroup * kTile * 8;
 constexpr int kScoreSmem = (int)kSOffBar + 256 + 1024;
 constexpr uint32_t kScoreTmem = 256;
 
@@ -1075,13 +1084,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     __syncwarp();
   } else if (warp == 5) {
     // ---- MMA issuer
-    const uint32_t cols = (uint32_t)min(64, (min(p.block, p.pos) * p.G + 15) / 16 * 16);
+    const uint32_t cols = (uint32_t)min(p.block, p.pos) * p.G > 32 ? 64u : 32u;
     const uint32_t id = idesc_e4m3_f32(128, 0) | ((cols >> 3) << 17);
     const uint64_t k_desc = sw128_desc(smem_u32(sm)), q_desc = sw128_desc(smem_u32(sm + kSOffQ));
     const bool leader = elect_one();
     bool ok = true;
-    int conv = 0;          // conversions used so far
-    uint32_t used[kSGroup] = {0u, 0u, 0u, 0u};  // times each S^T tile was written
+    int conv = 0;    // conversions used so far
+    int rounds = 0;  // q tiles so far: writes of each S^T tile (only the last group is short)
 #pragma unroll 1
     for (int g = 0; ok && g < n_tiles; g += kSGroup) {
       const int members = min(kSGroup, n_tiles - g);
@@ -1089,37 +1098,36 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
 #pragma unroll 1
       for (int qt = q0; ok && qt < max(q_tiles, q0 + 1); ++qt) {
         // (a group no row sees still passes its pages through, with no q tile)
-        const bool any = qt < q_tiles;
+        const bool any = qt < q_tiles, last = qt + 1 >= q_tiles;
         if (any && (p.q_tiles > 1 || conv == 0)) {
           ok = __all_sync(0xffffffffu, warp_wait(q_full, conv & 1, status));
           ++conv;
         }
         const int buf = p.q_tiles > 1 ? (conv - 1) & 1 : 0;
-#pragma unroll
-        for (int m = 0; m < kSGroup; ++m) {
-          if (!ok || m >= members) continue;
+#pragma unroll 1
+        for (int m = 0; ok && m < members; ++m) {
           if (qt == q0) ok = warp_wait(&k_full[m], (g / kSGroup) & 1, status);
-          if (ok && any && used[m] > 0) ok = warp_wait(&d_free[m], (used[m] - 1) & 1, status);
+          if (ok && any && rounds > 0) ok = warp_wait(&d_free[m], (rounds - 1) & 1, status);
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) continue;
+          if (!ok) break;
           tc_fence_after();
-          const bool last = qt + 1 >= q_tiles;
           if (leader) {
             if (any) {
+              const uint64_t kd = k_desc + m * (kTileBytes >> 4);
+              const uint64_t qd = q_desc + buf * 2 * (kQPart >> 4);
 #pragma unroll
               for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  tc_mma_f8(tmem + m * 64, k_desc + m * (kTileBytes >> 4) + kk * 2,
-                            q_desc + (buf * 2 + part) * (kQPart >> 4) + kk * 2, id,
+                  tc_mma_f8(tmem + m * 64, kd + kk * 2, qd + part * (kQPart >> 4) + kk * 2, id,
                             part + kk > 0 ? 1u : 0u);
               tc_commit(&d_full[m]);
             }
             if (last) tc_commit(&k_empty[m]);
           }
           __syncwarp();
-          if (any) ++used[m];
         }
+        if (any) ++rounds;
       }
     }
     __syncwarp();
@@ -1154,25 +1162,30 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       if (lane == 0) mbar_arrive(q_full);
       ++conv;
     };
-    uint32_t used[kSGroup] = {0u, 0u, 0u, 0u};
-    const int chunks = (min(min(p.block, p.pos) * p.G, 64) + 15) / 16;
+    // the thread's slot of each page of the group: K's scale and the sum so far
+    float2* const mine = reinterpret_cast<float2*>(sm + kSOffSlot) + slot;
+    const int chunks = min(p.block, p.pos) * p.G > 32 ? 2 : 1;  // of 32 rows
+    const int64_t out_row = ((int64_t)seq * p.c.Hkv + kvh) * ((int64_t)p.c.pps * kPageSlots);
+    int rounds = 0;
 #pragma unroll 1
     for (int g = 0; ok && g < n_tiles; g += kSGroup) {
       const int members = min(kSGroup, n_tiles - g);
       const int q0 = q_first(t_begin + g);
-      float acc[kSGroup] = {0.f, 0.f, 0.f, 0.f};
-      float kscale[kSGroup];
-      bool mapped[kSGroup];
+      const int64_t out0 = out_row + (int64_t)(t_begin + g) * kTile + slot;
+      float old[kSGroup];  // loads under way during the sums
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m) {
+        const int k = (t_begin + g + m) * kTile + slot;
         const int pg = m < members ? kvq_page(p.c, seq, t_begin + g + m) : -1;
-        mapped[m] = pg >= 0;
-        kscale[m] =
-            pg >= 0 ? pow2i(p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]) : 0.f;
+        float ks = 0.f;
+        if (pg >= 0)
+          ks = pow2i(p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]);
+        mine[m * kTile] = make_float2(ks, 0.f);
+        old[m] = p.score_in && m < members && k < key_end ? p.score_in[out0 + m * kTile] : 0.f;
       }
       if (q0 < q_tiles && (p.q_tiles > 1 || conv == 0)) convert(q0);
 #pragma unroll 1
-      for (int qt = q0; ok && qt < q_tiles; ++qt) {
+      for (int qt = q0; ok && qt < q_tiles; ++qt, ++rounds) {
         const int rbuf = (conv - 1) % 3;
         // the rows' scales of all four warps
         ok = __all_sync(0xffffffffu, warp_wait(q_full, (conv - 1) & 1, status));
@@ -1180,39 +1193,47 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         if (p.q_tiles > 1 && qt + 1 < q_tiles) convert(qt + 1);
         const float4* const rows = reinterpret_cast<const float4*>(sm + kSOffRow) + rbuf * 32;
         const int j0 = qt * p.pos;
-#pragma unroll
-        for (int m = 0; m < kSGroup; ++m) {
-          if (!ok || m >= members) continue;
-          ok = __all_sync(0xffffffffu, warp_wait(&d_full[m], used[m] & 1, status));
-          ++used[m];
-          if (!ok) continue;
+        // block slots from here on are not seen by every row of the q tile
+        const int mask_from = p.mask == DFLASH_MASK_NONE     ? 0x7fffffff
+                              : p.mask == DFLASH_MASK_CAUSAL ? ctx + j0 + 1
+                                                             : ctx;
+#pragma unroll 1
+        for (int m = 0; m < members; ++m) {
+          ok = __all_sync(0xffffffffu, warp_wait(&d_full[m], rounds & 1, status));
+          if (!ok) break;
           tc_fence_after();
-          const int k = (t_begin + g + m) * kTile + slot;  // the thread's slot
-          // rows that see it, a bit each
-          const bool masked =
-              p.mask != DFLASH_MASK_NONE && (t_begin + g + m + 1) * kTile > ctx + (p.mask == DFLASH_MASK_CAUSAL ? j0 + 1 : 0);
-          uint64_t vis = ~0ull;
-          if (masked && k >= ctx) vis = score_rows_seeing(p, b, k - ctx, j0, r);
+          const float2 st = mine[m * kTile];
+          const int k = (t_begin + g + m) * kTile + slot;
+          const bool masked = (t_begin + g + m + 1) * kTile > mask_from;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int c = 0; c < chunks; ++c) {
-            float s[16];
-            tmem_ld16(lane_base + m * 64 + 16 * c, s);
-            const uint32_t v16 = (uint32_t)(vis >> (16 * c));
+            uint32_t s[32];
+            tmem_ld32_nowait(lane_base + m * 64 + 32 * c, s);
+            uint32_t vis = 0xffffffffu;  // rows of the chunk that see the slot
+            if (masked && k >= ctx)
+              vis = (uint32_t)(score_rows_seeing(p, b, k - ctx, j0, r) >> (32 * c));
+            tmem_wait_ld();
+            if (!masked) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float4 rw = rows[8 * c + i / 2];
-              float2 x = mul2(make_float2(s[i], s[i + 1]), kscale[m]);
-              x.x = ex2(fmaf(x.x, rw.x, -rw.y));
-              x.y = ex2(fmaf(x.y, rw.z, -rw.w));
-              if (masked) {
-                x.x = (v16 >> i) & 1u ? x.x : 0.f;
-                x.y = (v16 >> i) & 2u ? x.y : 0.f;
+              for (int i = 0; i < 32; i += 2) {
+                const float4 rw = rows[16 * c + i / 2];
+                const float2 x =
+                    mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
+                sum = add2(sum, make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w))));
               }
-              sum = add2(sum, x);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float4 rw = rows[16 * c + i / 2];
+                const float2 x =
+                    mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
+                const float2 w = make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w)));
+                sum = add2(sum, make_float2((vis >> i) & 1u ? w.x : 0.f, (vis >> i) & 2u ? w.y : 0.f));
+              }
             }
           }
-          acc[m] += sum.x + sum.y;
+          mine[m * kTile].y = st.y + (sum.x + sum.y);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&d_free[m]);
@@ -1223,9 +1244,9 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       for (int m = 0; m < kSGroup; ++m) {
         const int k = (t_begin + g + m) * kTile + slot;
         if (m < members && k < key_end) {
-          const int64_t at = ((int64_t)seq * p.c.Hkv + kvh) * ((int64_t)p.c.pps * kPageSlots) + k;
-          const float old = p.score_in ? p.decay * p.score_in[at] : 0.f;
-          p.score_out[at] = mapped[m] ? old + acc[m] : old;
+          const float2 st = mine[m * kTile];  // (a slot on no page has scale 0)
+          const float base = p.score_in ? p.decay * old[m] : 0.f;
+          p.score_out[out0 + m * kTile] = st.x > 0.f ? base + st.y : base;
         }
       }
     }
