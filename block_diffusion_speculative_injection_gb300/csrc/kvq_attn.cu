@@ -945,7 +945,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
 // waves of resident CTAs (two per SM) x (tiles per split + two tiles' worth of
 // fixed cost), as many as the workspace holds.
 constexpr int kKvqMaxSplits = 256;
-static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t max_splits) {
+static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t max_splits,
+                           int fixed = 2) {
   const int64_t tiles = (max_keys + kTile - 1) / kTile;
   const int64_t slots = 2 * (int64_t)sm_count;
   const int64_t top = std::min(std::min<int64_t>(kKvqMaxSplits, tiles), max_splits);
@@ -953,7 +954,7 @@ static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t
   for (int64_t sp = 1; sp <= top; ++sp) {
     const int64_t per = (tiles + sp - 1) / sp;
     if (sp > 1 && (tiles + per - 1) / per < sp) continue;  // some would be empty
-    const int64_t cost = ((ctas * sp + slots - 1) / slots) * (per + 2) + (sp > 1 ? 1 : 0);
+    const int64_t cost = ((ctas * sp + slots - 1) / slots) * (per + fixed) + (sp > 1 ? 1 : 0);
     if (cost < best_cost) {
       best_cost = cost;
       best = sp;
@@ -993,6 +994,7 @@ static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64
 // weights and sums; warp 4: TMA of K; warp 5: MMAs.
 // ---------------------------------------------------------------------------
 constexpr int kSGroup = 4;
+constexpr int kUnmapped = 127;  // in place of the exponent of a slot without a page
 constexpr uint32_t kSOffQ = kSGroup * kTileBytes;
 constexpr uint32_t kSOffRow = kSOffQ + 2 * 2 * kQPart;   // [3][64] float2
 constexpr uint32_t kSOffQs = kSOffRow + 3 * 64 * 8;      // [64] float, conversion scratch
@@ -1143,15 +1145,18 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     // those of two tiles ago, but not older ones: it has converted the last tile)
     auto convert = [&](int qt) {
       const int buf = conv & 1, j0 = qt * p.pos;
+      const int row = warp * 16 + (lane & 15), pos = row_pos(p, row), j = j0 + pos;
+      const bool live = row < p.pos * p.G && j < r;
+      float lse = 0.f;
+      if (live)
+        lse = p.lse[((long long)b * p.block + j) * p.H + kvh * p.G + row - pos * p.G];
       if (p.q_tiles > 1) load_q(p, b, kvh, j0, warp, lane, q_raw);
       convert_q(q_raw, warp, lane, sm + kSOffQ + buf * 2 * kQPart, q_scales);
       __syncwarp();
       if (lane < 16) {
-        const int row = warp * 16 + lane, pos = row_pos(p, row), j = j0 + pos;
         float2 v = make_float2(0.f, INFINITY);  // weight 2^-inf = 0
-        if (row < p.pos * p.G && j < r) {
+        if (live) {
           const float sc = q_scales[lane];
-          const float lse = p.lse[((long long)b * p.block + j) * p.H + kvh * p.G + row - pos * p.G];
           v.x = fabsf(sc);
           v.y = sc < 0.f ? __int_as_float(0x7fffffff) : lse == -INFINITY ? INFINITY : lse * kLog2e;
         }
@@ -1166,24 +1171,49 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     float2* const mine = reinterpret_cast<float2*>(sm + kSOffSlot) + slot;
     const int chunks = min(p.block, p.pos) * p.G > 32 ? 2 : 1;  // of 32 rows
     const int64_t out_row = ((int64_t)seq * p.c.Hkv + kvh) * ((int64_t)p.c.pps * kPageSlots);
+    // What a group's pages need is read ahead: the exponents and old scores of the
+    // next group, the page ids of the one after that (the raw values, so that no
+    // load is waited for before its group begins).
+    int page[kSGroup], exps[kSGroup];
+    float old[kSGroup];
+    auto read_pages = [&](int g) {
+#pragma unroll
+      for (int m = 0; m < kSGroup; ++m)
+        page[m] = g + m < n_tiles ? kvq_page(p.c, seq, t_begin + g + m) : -1;
+    };
+    auto read_group = [&](int g) {
+#pragma unroll
+      for (int m = 0; m < kSGroup; ++m) {
+        const int t = t_begin + g + m;
+        exps[m] = page[m] >= 0
+                      ? p.c.ex[0][kvq_ph(p.c, page[m], kvh) * kKvqSubs + slot / kKvqSub]
+                      : kUnmapped;
+        old[m] = p.score_in && g + m < n_tiles && t * kTile + slot < key_end
+                     ? p.score_in[out_row + (int64_t)t * kTile + slot]
+                     : 0.f;
+      }
+    };
+    read_pages(0);
+    if (q_first(t_begin) < q_tiles) convert(q_first(t_begin));
+    read_group(0);
+    read_pages(kSGroup);
     int rounds = 0;
 #pragma unroll 1
     for (int g = 0; ok && g < n_tiles; g += kSGroup) {
       const int members = min(kSGroup, n_tiles - g);
       const int q0 = q_first(t_begin + g);
       const int64_t out0 = out_row + (int64_t)(t_begin + g) * kTile + slot;
-      float old[kSGroup];  // loads under way during the sums
+      float base[kSGroup];
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m) {
-        const int k = (t_begin + g + m) * kTile + slot;
-        const int pg = m < members ? kvq_page(p.c, seq, t_begin + g + m) : -1;
-        float ks = 0.f;
-        if (pg >= 0)
-          ks = pow2i(p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]);
-        mine[m * kTile] = make_float2(ks, 0.f);
-        old[m] = p.score_in && m < members && k < key_end ? p.score_in[out0 + m * kTile] : 0.f;
+        mine[m * kTile] = make_float2(exps[m] == kUnmapped ? 0.f : pow2i(exps[m]), 0.f);
+        base[m] = p.score_in ? p.decay * old[m] : 0.f;
       }
-      if (q0 < q_tiles && (p.q_tiles > 1 || conv == 0)) convert(q0);
+      if (g + kSGroup < n_tiles) {
+        read_group(g + kSGroup);
+        read_pages(g + 2 * kSGroup);
+      }
+      if (g > 0 && p.q_tiles > 1 && q0 < q_tiles) convert(q0);
 #pragma unroll 1
       for (int qt = q0; ok && qt < q_tiles; ++qt, ++rounds) {
         const int rbuf = (conv - 1) % 3;
@@ -1206,31 +1236,26 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           const int k = (t_begin + g + m) * kTile + slot;
           const bool masked = (t_begin + g + m + 1) * kTile > mask_from;
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            uint32_t s[32];
-            tmem_ld32_nowait(lane_base + m * 64 + 32 * c, s);
-            uint32_t vis = 0xffffffffu;  // rows of the chunk that see the slot
-            if (masked && k >= ctx)
-              vis = (uint32_t)(score_rows_seeing(p, b, k - ctx, j0, r) >> (32 * c));
-            tmem_wait_ld();
-            if (!masked) {
+          uint32_t s[64];
+          tmem_ld32_nowait(lane_base + m * 64, s);
+          if (chunks > 1) tmem_ld32_nowait(lane_base + m * 64 + 32, s + 32);
+          uint64_t vis = ~0ull;  // rows that see the slot
+          if (masked && k >= ctx) vis = score_rows_seeing(p, b, k - ctx, j0, r);
+          tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float4 rw = rows[16 * c + i / 2];
-                const float2 x =
-                    mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
-                sum = add2(sum, make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w))));
-              }
-            } else {
+          for (int c = 0; c < 2; ++c) {
+            if (c >= chunks) break;
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float4 rw = rows[16 * c + i / 2];
-                const float2 x =
-                    mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
-                const float2 w = make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w)));
-                sum = add2(sum, make_float2((vis >> i) & 1u ? w.x : 0.f, (vis >> i) & 2u ? w.y : 0.f));
+            for (int i = 32 * c; i < 32 * c + 32; i += 2) {
+              const float4 rw = rows[i / 2];
+              const float2 x =
+                  mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
+              float2 w = make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w)));
+              if (masked) {
+                w.x = (vis >> i) & 1u ? w.x : 0.f;
+                w.y = (vis >> i) & 2u ? w.y : 0.f;
               }
+              sum = add2(sum, w);
             }
           }
           mine[m * kTile].y = st.y + (sum.x + sum.y);
@@ -1245,8 +1270,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         const int k = (t_begin + g + m) * kTile + slot;
         if (m < members && k < key_end) {
           const float2 st = mine[m * kTile];  // (a slot on no page has scale 0)
-          const float base = p.score_in ? p.decay * old[m] : 0.f;
-          p.score_out[out0 + m * kTile] = st.x > 0.f ? base + st.y : base;
+          p.score_out[out0 + m * kTile] = st.x > 0.f ? base[m] + st.y : base[m];
         }
       }
     }
@@ -1380,7 +1404,7 @@ dflash_status dflash_kvq_score(const dflash_kvq_cache* cache, int32_t batch, int
   p.score_in = score_in;
   p.score_out = score_out;
   // spans of pages: as for the attention's splits
-  const int splits = kvq_plan_splits(kvq_sms(), (int64_t)cache->n_kv_heads * batch, max_keys, 65535);
+  const int splits = kvq_plan_splits(kvq_sms(), (int64_t)cache->n_kv_heads * batch, max_keys, 65535, 4);
   KvqMaps maps;
   const uint64_t kv_rows = (uint64_t)cache->n_pages * cache->n_kv_heads * kPageSlots;
   if (!encode_tmap_rows128(&maps.k, cache->k8_dev, kv_rows, kTile)) return DFLASH_E_CUDA;
