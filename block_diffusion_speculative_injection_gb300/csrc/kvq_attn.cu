@@ -1193,34 +1193,55 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
                      : 0.f;
       }
     };
+    // conversions run one q tile ahead: the next one is tile cq, for group cg
+    int cg = 0, cq = q_first(t_begin);
+    bool more = cq < q_tiles;
+    // waits, once, for conversion c by all four warps (c in order: a phase's parity
+    // says nothing any more once the next one has completed)
+    int known = 0;
+    auto converted = [&](int c) -> bool {
+      if (known > c) return true;
+      known = c + 1;
+      return __all_sync(0xffffffffu, warp_wait(q_full, c & 1, status));
+    };
     read_pages(0);
-    if (q_first(t_begin) < q_tiles) convert(q_first(t_begin));
     read_group(0);
     read_pages(kSGroup);
     int rounds = 0;
+    int g = 0, qt = cq;
+    float base[kSGroup];
 #pragma unroll 1
-    for (int g = 0; ok && g < n_tiles; g += kSGroup) {
+    while (g < n_tiles) {
       const int members = min(kSGroup, n_tiles - g);
       const int q0 = q_first(t_begin + g);
-      const int64_t out0 = out_row + (int64_t)(t_begin + g) * kTile + slot;
-      float base[kSGroup];
-#pragma unroll
-      for (int m = 0; m < kSGroup; ++m) {
-        mine[m * kTile] = make_float2(exps[m] == kUnmapped ? 0.f : pow2i(exps[m]), 0.f);
-        base[m] = p.score_in ? p.decay * old[m] : 0.f;
-      }
-      if (g + kSGroup < n_tiles) {
-        read_group(g + kSGroup);
-        read_pages(g + 2 * kSGroup);
-      }
-      if (g > 0 && p.q_tiles > 1 && q0 < q_tiles) convert(q0);
+      const int now = p.q_tiles > 1 ? rounds : 0;  // this q tile's conversion
 #pragma unroll 1
-      for (int qt = q0; ok && qt < q_tiles; ++qt, ++rounds) {
-        const int rbuf = (conv - 1) % 3;
-        // the rows' scales of all four warps
-        ok = __all_sync(0xffffffffu, warp_wait(q_full, (conv - 1) & 1, status));
-        if (!ok) break;
-        if (p.q_tiles > 1 && qt + 1 < q_tiles) convert(qt + 1);
+      while (more && conv < now + 2) {
+        // the rows' scales of all four warps: before a buffer is written again
+        if (conv > now && !(ok = converted(now))) break;
+        convert(cq++);
+        if (p.q_tiles == 1) more = false;
+        while (more && cq >= q_tiles) {
+          cg += kSGroup;
+          more = cg < n_tiles;
+          cq = q_first(t_begin + cg);
+        }
+      }
+      if (!ok) break;
+      if (qt == q0) {
+#pragma unroll
+        for (int m = 0; m < kSGroup; ++m) {
+          mine[m * kTile] = make_float2(exps[m] == kUnmapped ? 0.f : pow2i(exps[m]), 0.f);
+          base[m] = p.score_in ? p.decay * old[m] : 0.f;
+        }
+        if (g + kSGroup < n_tiles) {
+          read_group(g + kSGroup);
+          read_pages(g + 2 * kSGroup);
+        }
+      }
+      if (qt < q_tiles) {
+        if (!(ok = converted(now))) break;
+        const int rbuf = now % 3;
         const float4* const rows = reinterpret_cast<const float4*>(sm + kSOffRow) + rbuf * 32;
         const int j0 = qt * p.pos;
         // block slots from here on are not seen by every row of the q tile
@@ -1263,16 +1284,21 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           __syncwarp();
           if (lane == 0) mbar_arrive(&d_free[m]);
         }
+        ++rounds;
       }
       if (!ok) break;
+      if (++qt < q_tiles) continue;
+      // the group's last q tile
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m) {
         const int k = (t_begin + g + m) * kTile + slot;
         if (m < members && k < key_end) {
           const float2 st = mine[m * kTile];  // (a slot on no page has scale 0)
-          p.score_out[out0 + m * kTile] = st.x > 0.f ? base[m] + st.y : base[m];
+          p.score_out[out_row + k] = st.x > 0.f ? base[m] + st.y : base[m];
         }
       }
+      g += kSGroup;
+      qt = q_first(t_begin + g);
     }
   }
   tc_fence_before();

@@ -601,3 +601,36 @@ def test_offsets_past_32_bits():
     mag = torch.einsum("bhn,bnhd->bhd", s.softmax(-1), vb.double().abs())
     assert ((out[:, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * mag).all()
     m.dflash_kvq_check(h)
+
+
+def test_score_many_q_tiles_and_pages():
+    """Passes of many q tiles over several groups of pages, and rows that see
+    only part of the pages."""
+    for heads, g, lens, block, q_lens, mask in ((2, 8, [900, 700, 70], 40, [40, 33, 5], "causal"),
+                                                (1, 5, [1300, 640], 300, None, "causal"),
+                                                (1, 2, [1100], 130, None, "none")):
+        c, rng = filled(heads, lens, seed=block)
+        B, H = len(lens), heads * g
+        t, qe = bf16(rng.normal(size=(B, block, H, HD)) * 1.5)
+        q_lens = q_lens or [block] * B
+        k = torch.from_numpy(np.stack([c.val["k"][b] for b in range(B)])).cuda()
+        q = torch.from_numpy(qe).cuda().view(B, block, heads, g, HD)
+        s = torch.einsum("bjhgd,bnhd->bjhgn", q, k) / HD ** 0.5
+        n = torch.tensor(lens).cuda()[:, None, None]
+        r = torch.tensor(q_lens).cuda()[:, None, None]
+        slot = torch.arange(k.shape[1]).cuda()[None, None]
+        row = torch.arange(block).cuda()[None, :, None]
+        seen = (slot < n) & (row < r) & ((slot - (n - r) <= row) | (mask == "none"))
+        s = s.masked_fill(~seen[:, :, None, None], float("-inf"))
+        lse = torch.logsumexp(s, dim=-1)
+        p = torch.where(seen[:, :, None, None], torch.exp(s - lse[..., None]), torch.zeros_like(s))
+        want = p.sum(dim=(1, 3))
+        out = torch.zeros(B, heads, k.shape[1], device="cuda")
+        lf = lse.reshape(B, block, H).float()
+        capi().dflash_kvq_score(c.h, B, H, block, {"none": 0, "causal": 1}[mask], None, i32(lens),
+                                i32(q_lens), None, max(lens), t, lf, 1.0, None, out)
+        # a weight is off by its score's error, see test_score; lse in fp32 by 2^-22
+        top = np.abs(qe).max() * float(k.abs().sum(-1).max()) / HD ** 0.5
+        tol = 2.0 ** -22 + (2.0 ** -17 * top + 2.0 ** -18) * want
+        assert ((out.double() - want).abs() <= tol).all()
+        capi().dflash_kvq_check(c.h)
