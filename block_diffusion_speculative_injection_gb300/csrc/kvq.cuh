@@ -31,12 +31,17 @@ __device__ __forceinline__ int kvq_seq(const KvqK& c, const int32_t* ids, int b)
   }
   return q;
 }
-// page of table entry i of a sequence, or -1 (past the table, unmapped or out of
-// the pool)
+// Page of table entry i of a sequence, or -1 (past the table, unmapped or out of the
+// pool): in two steps, so that a loop can read an entry some iterations before
+// anything waits for it.
+__device__ __forceinline__ int kvq_page_load(const KvqK& c, int seq, int i) {
+  return i >= 0 && i < c.pps ? c.tab[(int64_t)seq * c.pps + i] : -1;
+}
+__device__ __forceinline__ int kvq_page_check(const KvqK& c, int raw) {
+  return raw >= 0 && raw < c.n_pages ? raw : -1;
+}
 __device__ __forceinline__ int kvq_page(const KvqK& c, int seq, int i) {
-  if (i < 0 || i >= c.pps) return -1;
-  const int pg = c.tab[(int64_t)seq * c.pps + i];
-  return pg >= 0 && pg < c.n_pages ? pg : -1;
+  return kvq_page_check(c, kvq_page_load(c, seq, i));
 }
 // (page, head) index: times kKvqPageBytes the codes, times kKvqSubs the exponents
 __device__ __forceinline__ int64_t kvq_ph(const KvqK& c, int page, int head) {

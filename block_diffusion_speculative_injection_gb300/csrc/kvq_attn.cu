@@ -524,10 +524,11 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       __syncwarp();
       return true;
     };
-    int pg_k = kvq_page(p.c, seq, first_page), pg_v = 0;
+    int raw_k = kvq_page_load(p.c, seq, first_page), pg_v = 0;
 #pragma unroll 1
     for (int t = 0; t <= n_tiles; ++t) {
-      const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, first_page + t + 1) : 0;
+      const int pg_k = kvq_page_check(p.c, raw_k);
+      raw_k = t + 1 < n_tiles ? kvq_page_load(p.c, seq, first_page + t + 1) : 0;
       if (t < n_tiles) {
         if (pg_k < 0) set_dev_status(status, kDevCapacity);
         if (!load(t, false, pg_k)) break;
@@ -538,7 +539,6 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         v_issued = t;
       }
       pg_v = pg_k;
-      pg_k = pg_next;
     }
     // every issued copy has landed before this warp leaves
 #pragma unroll 1
@@ -643,15 +643,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       return ok;
     };
     int pg = kvq_page(p.c, seq, first_page);
-    int pg_next = n_tiles > 1 ? kvq_page(p.c, seq, first_page + 1) : -1;
+    int raw_next = n_tiles > 1 ? kvq_page_load(p.c, seq, first_page + 1) : -1;
     uint2 ex = exps_of(pg);
 #pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
       const int tile0 = k_begin + t * kTile;
       const int pg_now = pg;
       const uint2 ex_now = ex;
-      pg = pg_next;
-      pg_next = t + 2 < n_tiles ? kvq_page(p.c, seq, first_page + t + 2) : -1;
+      pg = kvq_page_check(p.c, raw_next);
+      raw_next = t + 2 < n_tiles ? kvq_page_load(p.c, seq, first_page + t + 2) : -1;
       ex = t + 1 < n_tiles ? exps_of(pg) : make_uint2(0u, 0u);
       const int stop = pg_now < 0 ? tile0 : k_stop;  // slots from here on are not seen
       const bool masked = tile0 + kTile > min(stop, mask_from);
@@ -1062,10 +1062,11 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     const bool leader = elect_one();
     if (leader) tma_prefetch_desc(&maps.k);
     int issued = 0;
-    int pg = kvq_page(p.c, seq, t_begin);
+    int raw = kvq_page_load(p.c, seq, t_begin);
 #pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
-      const int pg_next = t + 1 < n_tiles ? kvq_page(p.c, seq, t_begin + t + 1) : 0;
+      const int pg = kvq_page_check(p.c, raw);
+      raw = t + 1 < n_tiles ? kvq_page_load(p.c, seq, t_begin + t + 1) : 0;
       const int st = t % kSGroup;
       if (t >= kSGroup &&
           !__all_sync(0xffffffffu, warp_wait(&k_empty[st], ((t / kSGroup) - 1) & 1, status)))
@@ -1078,7 +1079,6 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       }
       __syncwarp();
       issued = t + 1;
-      pg = pg_next;
     }
 #pragma unroll 1
     for (int t = max(0, issued - kSGroup); t < issued; ++t)
@@ -1179,14 +1179,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     auto read_pages = [&](int g) {
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m)
-        page[m] = g + m < n_tiles ? kvq_page(p.c, seq, t_begin + g + m) : -1;
+        page[m] = g + m < n_tiles ? kvq_page_load(p.c, seq, t_begin + g + m) : -1;
     };
     auto read_group = [&](int g) {
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m) {
         const int t = t_begin + g + m;
-        exps[m] = page[m] >= 0
-                      ? p.c.ex[0][kvq_ph(p.c, page[m], kvh) * kKvqSubs + slot / kKvqSub]
+        const int pg = kvq_page_check(p.c, page[m]);
+        exps[m] = pg >= 0
+                      ? p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]
                       : kUnmapped;
         old[m] = p.score_in && g + m < n_tiles && t * kTile + slot < key_end
                      ? p.score_in[out_row + (int64_t)t * kTile + slot]
@@ -1248,41 +1249,58 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         const int mask_from = p.mask == DFLASH_MASK_NONE     ? 0x7fffffff
                               : p.mask == DFLASH_MASK_CAUSAL ? ctx + j0 + 1
                                                              : ctx;
+        // two pages at a time: a row's (scale, log2 lse) is read once for both
 #pragma unroll 1
-        for (int m = 0; m < members; ++m) {
-          ok = __all_sync(0xffffffffu, warp_wait(&d_full[m], rounds & 1, status));
+        for (int m = 0; m < members; m += 2) {
+          const int m1 = min(m + 1, members - 1);  // (a last page alone goes with itself)
+          ok = __all_sync(0xffffffffu, warp_wait(&d_full[m], rounds & 1, status) &&
+                                           warp_wait(&d_full[m1], rounds & 1, status));
           if (!ok) break;
           tc_fence_after();
-          const float2 st = mine[m * kTile];
-          const int k = (t_begin + g + m) * kTile + slot;
-          const bool masked = (t_begin + g + m + 1) * kTile > mask_from;
-          float2 sum = make_float2(0.f, 0.f);
-          uint32_t s[64];
-          tmem_ld32_nowait(lane_base + m * 64, s);
-          if (chunks > 1) tmem_ld32_nowait(lane_base + m * 64 + 32, s + 32);
-          uint64_t vis = ~0ull;  // rows that see the slot
-          if (masked && k >= ctx) vis = score_rows_seeing(p, b, k - ctx, j0, r);
-          tmem_wait_ld();
+          const float2 st0 = mine[m * kTile], st1 = mine[m1 * kTile];
+          const int k0 = (t_begin + g + m) * kTile + slot, k1 = (t_begin + g + m1) * kTile + slot;
+          const bool masked = (t_begin + g + m1 + 1) * kTile > mask_from;
+          uint64_t vis0 = ~0ull, vis1 = ~0ull;  // rows that see the slots
+          if (masked) {
+            if (k0 >= ctx) vis0 = score_rows_seeing(p, b, k0 - ctx, j0, r);
+            if (k1 >= ctx) vis1 = score_rows_seeing(p, b, k1 - ctx, j0, r);
+          }
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t s0[32], s1[32];
+            tmem_ld32_nowait(lane_base + m * 64 + 32 * c, s0);
+            tmem_ld32_nowait(lane_base + m1 * 64 + 32 * c, s1);
+            tmem_wait_ld();
+            const float4* const rc = rows + 16 * c;
+            const uint32_t v0 = (uint32_t)(vis0 >> (32 * c)), v1 = (uint32_t)(vis1 >> (32 * c));
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c >= chunks) break;
-#pragma unroll
-            for (int i = 32 * c; i < 32 * c + 32; i += 2) {
-              const float4 rw = rows[i / 2];
+            for (int i = 0; i < 32; i += 2) {
+              const float4 rw = rc[i / 2];
               const float2 x =
-                  mul2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), st.x);
+                  mul2(make_float2(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])), st0.x);
+              const float2 y =
+                  mul2(make_float2(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])), st1.x);
               float2 w = make_float2(ex2(fmaf(x.x, rw.x, -rw.y)), ex2(fmaf(x.y, rw.z, -rw.w)));
+              float2 z = make_float2(ex2(fmaf(y.x, rw.x, -rw.y)), ex2(fmaf(y.y, rw.z, -rw.w)));
               if (masked) {
-                w.x = (vis >> i) & 1u ? w.x : 0.f;
-                w.y = (vis >> i) & 2u ? w.y : 0.f;
+                w.x = (v0 >> i) & 1u ? w.x : 0.f;
+                w.y = (v0 >> i) & 2u ? w.y : 0.f;
+                z.x = (v1 >> i) & 1u ? z.x : 0.f;
+                z.y = (v1 >> i) & 2u ? z.y : 0.f;
               }
-              sum = add2(sum, w);
+              sum0 = add2(sum0, w);
+              sum1 = add2(sum1, z);
             }
           }
-          mine[m * kTile].y = st.y + (sum.x + sum.y);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&d_free[m]);
+          if (lane == 0) {
+            mbar_arrive(&d_free[m]);
+            if (m1 != m) mbar_arrive(&d_free[m1]);
+          }
+          mine[m * kTile].y = st0.y + (sum0.x + sum0.y);
+          if (m1 != m) mine[m1 * kTile].y = st1.y + (sum1.x + sum1.y);
         }
         ++rounds;
       }
