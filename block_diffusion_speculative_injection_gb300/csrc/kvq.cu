@@ -10,32 +10,27 @@
 
 namespace dflash {
 
-// ---------------------------------------------------------------------------
-// a warp's block: 16 rows of 128 values, eight consecutive values of row
-// 2 i + lane / 16 in x[i] (columns 8 (lane % 16) ..)
-// ---------------------------------------------------------------------------
-struct KvqRows {
-  float x[8][8];
-};
+// A warp's block is 16 rows of 128 values: eight consecutive values (columns
+// 8 (lane % 16) ..) of the rows 2 i + lane / 16, i < 8, in each lane.  The raw rows are kept
+// and decoded twice, for the maximum and for the codes: 32 registers instead of the 64 of
+// the values, so that twice as many blocks are in flight.
 
-// exponent of the block (rows not in use hold zeros): non-finite values do not count
-__device__ __forceinline__ int block_exponent(const KvqRows& r) {
-  float a = 0.f;
+// running maximum of the finite magnitudes
+__device__ __forceinline__ float finite_max(float a, const float* x) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float m = fabsf(r.x[i][j]);
-      a = m < INFINITY ? fmaxf(a, m) : a;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const float m = fabsf(x[j]);
+    a = m < INFINITY ? fmaxf(a, m) : a;
+  }
+  return a;
+}
+__device__ __forceinline__ float warp_max(float a) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-  return kvq_exponent(a);
+  return a;
 }
-
-// codes of eight values under exponent e; a non-finite value becomes NaN
-__device__ __forceinline__ uint2 code_row(const float* x, int e) {
-  const float s = pow2i(-e);
+// codes of eight values times s (a power of two); a non-finite value becomes NaN
+__device__ __forceinline__ uint2 code_row(const float* x, float s) {
   float y[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) y[j] = fabsf(x[j]) < INFINITY ? x[j] * s : __int_as_float(0x7fffffff);
@@ -55,7 +50,7 @@ struct AppendK {
   int batch, rows, n_blk;
 };
 
-__global__ void __launch_bounds__(128) kvq_append_kernel(const AppendK p) {
+__global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -105,24 +100,48 @@ __global__ void __launch_bounds__(128) kvq_append_kernel(const AppendK p) {
       raw[i] = *reinterpret_cast<const uint4*>(p.in[kv] + row * p.stride[kv] + head * kKvqHd + col);
     }
   }
-  KvqRows v;
   const float old_scale = pow2i(e_old);
+  auto values = [&](int i, float* x) {
+    if (2 * i + half < n_old) {
+      kvq_decode8(make_uint2(raw[i].x, raw[i].y), x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= old_scale;
+    } else {
+      bf16x8_to_f(raw[i], x);
+    }
+  };
+  // the largest magnitude: of new rows alone, from the bf16 pairs as integers (where
+  // a NaN or an infinity would come out on top: then, and with committed rows
+  // in the block, value by value)
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (2 * i + half < n_old) {
-      kvq_decode8(make_uint2(raw[i].x, raw[i].y), v.x[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v.x[i][j] *= old_scale;
-    } else {
-      bf16x8_to_f(raw[i], v.x[i]);
-    }
+    constexpr uint32_t abs2 = 0x7fff7fffu;
+    top = __vimax3_u16x2(top, raw[i].x & abs2, raw[i].y & abs2);
+    top = __vimax3_u16x2(top, raw[i].z & abs2, raw[i].w & abs2);
   }
-  const int e = block_exponent(v);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const uint32_t top1 = max(top & 0xffffu, top >> 16);
+  float a = __uint_as_float(top1 << 16);
+  if (n_old > 0 || top1 >= 0x7f80u) {
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x[8];
+      values(i, x);
+      a = finite_max(a, x);
+    }
+    a = warp_max(a);
+  }
+  const int e = kvq_exponent(a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 2 * i + half;
+    float x[8];
+    values(i, x);
     if (r < n_live && (r >= n_old || e != e_old))
-      *reinterpret_cast<uint2*>(codes + r * kKvqHd + col) = code_row(v.x[i], e);
+      *reinterpret_cast<uint2*>(codes + r * kKvqHd + col) = code_row(x, pow2i(-e));
   }
   if (lane == 0) *ex = (int8_t)e;
 }
@@ -184,8 +203,8 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const ReadK p) {
 // eviction.  Select: per (batch entry, head), the K-th largest score of the
 // slots before the window by a radix search over the scores mapped to unsigned
 // integers of the same order, then the kept slots in order by prefix sums.
-// Move: one warp per destination block of 16 gathers its rows and codes them
-// under the block's own exponent.
+// Move: each destination block of 16 gathers its rows and codes them under the
+// block's own exponent.
 // ---------------------------------------------------------------------------
 struct EvictK {
   KvqK c;
@@ -200,6 +219,12 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   if (f != f) return 0u;
   const uint32_t u = __float_as_uint(f + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// and back
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return k == 0u ? __int_as_float(0x7fffffff)
+                 : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 // lengths and ids of entry b; false: skip it
@@ -219,114 +244,205 @@ __device__ __forceinline__ bool evict_entry(const EvictK& p, int b, int& src, in
   return true;
 }
 
-constexpr int kSelThreads = 512;
+// Select: a cluster of C CTAs per (entry, head), CTA c on the slots [c, c + 1) * chunk of
+// the w0 slots before the window.  Three passes find the K-th largest key T eleven bits
+// at a time (the last one ten): a histogram of the candidates' next bits in each
+// CTA, summed over the cluster through distributed shared memory by every CTA for
+// itself.  The keys are held in shared memory after the first pass (what does
+// not fit is read again).  Then the kept slots (above T, and the first of those
+// equal to T) are counted per warp and written in order.
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kSelKeys = 8192;  // keys a CTA holds
+constexpr int kSelCluster = 8;  // most CTAs of a cluster
+// [3][bins] histograms, keys; the dynamic part of the shared memory
+constexpr int kSelSmem = (3 * kSelBins + kSelKeys) * 4;
 
-__global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const EvictK p) {
+__global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const EvictK p, const int C) {
   pdl_trigger();
   pdl_wait();
-  const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int head = blockIdx.x / C, rank = blockIdx.x % C, b = blockIdx.y, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   int src, dst, n;
-  if (!evict_entry(p, b, src, dst, n)) return;
-  const int cap = p.c.pps * kPageSlots;
+  if (!evict_entry(p, b, src, dst, n)) return;  // the whole cluster
+  const int64_t cap = (int64_t)p.c.pps * kPageSlots;
   const float* const sc = p.score + ((int64_t)src * p.c.Hkv + head) * cap;
   float* const dsc = p.score + ((int64_t)dst * p.c.Hkv + head) * cap;
   int32_t* const kept = p.kept + ((int64_t)b * p.c.Hkv + head) * p.budget;
   const int m = min(n, p.budget);
   const int w0 = n <= p.budget ? 0 : n - p.window;  // slots from here on are kept
   const int K = m - (n - w0);                       // kept slots before w0
-  if (head == 0 && tid == 0) p.new_lens[b] = m;
-
-  __shared__ int hist[256];
-  __shared__ int s_digit, s_left;
-  __shared__ int s_warp[2][kSelThreads / 32];
-  // threshold: the K-th largest key T, and how many keys equal to T are kept
-  uint32_t T = 0xffffffffu;
-  int ties = 0;
-  if (K > 0) {
-    uint32_t prefix = 0;
-    int left = K;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int i = tid; i < w0; i += kSelThreads) {
-        const uint32_t k = score_key(sc[i]);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_digit = d;
-        s_left = left;
-      }
-      __syncthreads();
-      prefix = (prefix << 8) | (uint32_t)s_digit;
-      left = s_left;
-      __syncthreads();
-    }
-    T = prefix;
-    ties = left;
-  }
-  // kept slots in order: above T, or one of the first `ties` equal to T
-  int above0 = 0, equal0 = 0;
-  for (int i0 = 0; i0 < w0; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    const float f = i < w0 ? sc[i] : 0.f;
-    const uint32_t k = score_key(f);
-    const bool gt = K > 0 && i < w0 && k > T, eq = K > 0 && i < w0 && k == T;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      s_warp[0][warp] = __popc(bg);
-      s_warp[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int above = above0, equal = equal0, ta = 0, te = 0;
-    for (int x = 0; x < kSelThreads / 32; ++x) {
-      if (x < warp) {
-        above += s_warp[0][x];
-        equal += s_warp[1][x];
-      }
-      ta += s_warp[0][x];
-      te += s_warp[1][x];
-    }
-    const uint32_t lt = (1u << lane) - 1u;
-    above += __popc(bg & lt);
-    equal += __popc(be & lt);
-    if (gt || (eq && equal < ties)) {
-      const int at = above + min(equal, ties);
-      kept[at] = i;
-      dsc[at] = f;
-    }
-    above0 += ta;
-    equal0 += te;
-    __syncthreads();
-  }
-  for (int i = w0 + tid; i < n; i += kSelThreads) {
+  const int all = C * kSelThreads, gid = rank * kSelThreads + tid;
+  if (head == 0 && gid == 0) p.new_lens[b] = m;
+  // what needs no selection: the window, and the ends of the lists
+  for (int i = w0 + gid; i < n; i += all) {
     kept[K + i - w0] = i;
     dsc[K + i - w0] = sc[i];
   }
-  for (int i = m + tid; i < p.budget; i += kSelThreads) kept[i] = -1;
-  for (int i = m + tid; i < cap; i += kSelThreads) dsc[i] = 0.f;
+  for (int i = m + gid; i < p.budget; i += all) kept[i] = -1;
+  for (int64_t i = m + gid; i < cap; i += all) dsc[i] = 0.f;
+  if (K == 0) return;
+
+  extern __shared__ uint32_t sel_smem[];
+  uint32_t* const hist = sel_smem;
+  uint32_t* const held = sel_smem + 3 * kSelBins;
+  __shared__ uint32_t s_digit, s_left;
+  __shared__ uint32_t s_cnt[2];               // this CTA's keys above and equal to T
+  __shared__ uint32_t s_warp[2][kSelWarps];
+  // whole warps' worth of slots per CTA, so that every warp's share is 32 x something
+  const int chunk = (w0 + C * kSelThreads - 1) / (C * kSelThreads) * kSelThreads;
+  const int i0 = rank * chunk, i1 = min(w0, i0 + chunk);
+  auto key_at = [&](int i) -> uint32_t {
+    return i - i0 < kSelKeys ? held[i - i0] : score_key(sc[i]);
+  };
+  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
+  // T's known high bits, and the rank of T among the keys that share them
+  uint32_t prefix = 0, left = (uint32_t)K;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    uint32_t* const h = hist + pass * kSelBins;
+    constexpr int kU = 8;  // loads in flight
+#pragma unroll 1
+    for (int i8 = i0 + tid; i8 - tid < i1; i8 += kU * kSelThreads) {
+      uint32_t k[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = i8 + u * kSelThreads;
+        k[u] = i >= i1 ? 0u : pass > 0 && i - i0 < kSelKeys ? held[i - i0] : __float_as_uint(sc[i]);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = i8 + u * kSelThreads;
+        if (i - tid >= i1) break;
+        bool in = i < i1;
+        if (pass == 0 || i - i0 >= kSelKeys) k[u] = score_key(__uint_as_float(k[u]));
+        if (pass == 0) {
+          if (in && i - i0 < kSelKeys) held[i - i0] = k[u];
+        } else {
+          in = in && (pass == 1 ? (k[u] >> 21) == prefix : (k[u] >> 10) == prefix);
+        }
+        // (a warp of one bin, as untouched scores of zero make it, adds once)
+        const uint32_t bin = (k[u] >> shift) & mask;
+        const uint32_t bin0 = __shfl_sync(0xffffffffu, bin, 0);
+        if (__all_sync(0xffffffffu, in && bin == bin0)) {
+          if (lane == 0) atomicAdd(&h[bin], 32u);
+        } else if (in) {
+          atomicAdd(&h[bin], 1u);
+        }
+      }
+    }
+    cluster_sync();
+    // the cluster's histogram, four bins a thread from the top down: thread t has
+    // bins 2047 - 4 t - {0, 1, 2, 3}
+    uint32_t cnt[4] = {0, 0, 0, 0}, mine = 0;
+    const int base = kSelBins - 4 - 4 * tid;
+    float4 peer[kSelCluster];
+#pragma unroll
+    for (int c = 0; c < kSelCluster; ++c)
+      if (c < C) peer[c] = ld_peer_f32x4(map_peer(smem_u32(h + base), c));
+#pragma unroll
+    for (int c = 0; c < kSelCluster; ++c)
+      if (c < C) {
+        cnt[0] += __float_as_uint(peer[c].w);
+        cnt[1] += __float_as_uint(peer[c].z);
+        cnt[2] += __float_as_uint(peer[c].y);
+        cnt[3] += __float_as_uint(peer[c].x);
+      }
+    mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) s_warp[0][warp] = incl;
+    __syncthreads();
+    // keys in higher bins
+    uint32_t before =
+        incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[0][lane] : 0u);
+    if (before < left && before + mine >= left) {
+      int k = 0;
+      while (before + cnt[k] < left) before += cnt[k++];
+      s_digit = (uint32_t)(base + 3 - k);
+      s_left = left - before;
+    }
+    __syncthreads();
+    prefix = pass == 0 ? s_digit : pass == 1 ? (prefix << 11) | s_digit : (prefix << 10) | s_digit;
+    left = s_left;
+  }
+  const uint32_t T = prefix, ties = left;
+  // each warp's contiguous share of the chunk: counts, then the kept slots in order
+  const int share = chunk / kSelWarps, j0 = i0 + warp * share, j1 = min(i1, j0 + share);
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += 32) {
+    const int i = j + lane;
+    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < j1 && k > T));
+    eq += __popc(__ballot_sync(0xffffffffu, i < j1 && k == T));
+  }
+  __syncthreads();  // s_warp is read above
+  if (lane == 0) {
+    s_warp[0][warp] = gt;
+    s_warp[1][warp] = eq;
+  }
+  __syncthreads();
+  if (warp < 2) {
+    const uint32_t sum =
+        __reduce_add_sync(0xffffffffu, lane < kSelWarps ? s_warp[warp][lane] : 0u);
+    if (lane == 0) s_cnt[warp] = sum;
+  }
+  cluster_sync();
+  // before this warp: the lower CTAs' (one a lane) and the lower warps' counts
+  uint32_t above = lane < warp ? s_warp[0][lane] : 0u, equal = lane < warp ? s_warp[1][lane] : 0u;
+  if (lane < rank) {
+    above += __float_as_uint(ld_peer_f32(map_peer(smem_u32(&s_cnt[0]), lane)));
+    equal += __float_as_uint(ld_peer_f32(map_peer(smem_u32(&s_cnt[1]), lane)));
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  const uint32_t lt = (1u << lane) - 1u;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += 32) {
+    const int i = j + lane;
+    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    const uint32_t bg = __ballot_sync(0xffffffffu, i < j1 && k > T);
+    const uint32_t be = __ballot_sync(0xffffffffu, i < j1 && k == T);
+    const uint32_t a = above + __popc(bg & lt), e = equal + __popc(be & lt);
+    if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < ties)) {
+      const uint32_t at = a + min(e, ties);
+      kept[at] = i;
+      dsc[at] = key_score(k);
+    }
+    above += __popc(bg);
+    equal += __popc(be);
+  }
+  cluster_sync();  // no CTA leaves while its counts may be read
 }
 
-__global__ void __launch_bounds__(128) kvq_evict_move_kernel(const EvictK p) {
+// Move: one warp per block of 16 destination rows of a head, K and V.
+__global__ void __launch_bounds__(128, 6) kvq_evict_move_kernel(const EvictK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int n_blk = (p.budget + kKvqSub - 1) / kKvqSub;
-  long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int kv = (int)(w & 1);
-  w >>= 1;
-  const int blk = (int)(w % n_blk);
-  w /= n_blk;
-  const int head = (int)(w % p.c.Hkv);
-  w /= p.c.Hkv;
-  if (w >= p.batch) return;
-  const int b = (int)w;
+  uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int blk = (int)(w % (uint32_t)n_blk);
+  w /= (uint32_t)n_blk;
+  const int head = (int)(w % (uint32_t)p.c.Hkv), b = (int)(w / (uint32_t)p.c.Hkv);
+  if (b >= p.batch) return;
+  const int d0 = blk * kKvqSub;
+  // lane r < 16: row r's source slot (in bounds of the list; used once it is known
+  // how many rows there are)
+  int from = -1;
+  if (lane < kKvqSub && d0 + lane < p.budget)
+    from = p.kept[((int64_t)b * p.c.Hkv + head) * p.budget + d0 + lane];
   int src, dst, n;
   if (!evict_entry(p, b, src, dst, n)) return;
-  const int m = min(n, p.budget), d0 = blk * kKvqSub;
+  const int m = min(n, p.budget);
   if (d0 >= m) return;
   const int n_live = min(kKvqSub, m - d0);
   const int dpage = kvq_page(p.c, dst, d0 / kPageSlots);
@@ -334,46 +450,54 @@ __global__ void __launch_bounds__(128) kvq_evict_move_kernel(const EvictK p) {
     set_dev_status(p.c.status, kDevCapacity);
     return;
   }
-  // lane r < 16: where row r comes from, and its exponent
-  int64_t at = -1;
-  int e_src = 0;
+  // its row in the pool (pages * heads * 128 < 2^31) and its exponents
+  int at = -1, e_src[2] = {0, 0};
   if (lane < n_live) {
-    const int s = p.kept[((int64_t)b * p.c.Hkv + head) * p.budget + d0 + lane];
-    const int page = kvq_page(p.c, src, s / kPageSlots);
+    const int page = kvq_page(p.c, src, from / kPageSlots);
     if (page >= 0) {
-      const int64_t ph = kvq_ph(p.c, page, head);
-      const int r = s % kPageSlots;
-      at = ph * kKvqPageBytes + (int64_t)r * kKvqHd;
-      e_src = p.c.ex[kv][ph * kKvqSubs + r / kKvqSub];
+      at = (int)kvq_ph(p.c, page, head) * kPageSlots + from % kPageSlots;
+      e_src[0] = p.c.ex[0][at / kKvqSub];
+      e_src[1] = p.c.ex[1][at / kKvqSub];
     } else {
       set_dev_status(p.c.status, kDevCapacity);
     }
   }
   const int half = lane >> 4, col = (lane & 15) * 8;
-  uint2 raw[8];
+  uint2 raw[2][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t a = __shfl_sync(0xffffffffu, at, 2 * i + half);
-    raw[i] = a >= 0 ? *reinterpret_cast<const uint2*>(p.c.c8[kv] + a + col) : make_uint2(0u, 0u);
-  }
-  KvqRows v;
+    const int a = __shfl_sync(0xffffffffu, at, 2 * i + half);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = pow2i(__shfl_sync(0xffffffffu, e_src, 2 * i + half));
-    kvq_decode8(raw[i], v.x[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v.x[i][j] *= s;
+    for (int kv = 0; kv < 2; ++kv)
+      raw[kv][i] = a >= 0 ? *reinterpret_cast<const uint2*>(p.c.c8[kv] + (int64_t)a * kKvqHd + col)
+                          : make_uint2(0u, 0u);
   }
-  const int e = block_exponent(v);
   const int r0 = d0 % kPageSlots;
   const int64_t ph = kvq_ph(p.c, dpage, head);
-  uint8_t* const codes = p.c.c8[kv] + ph * kKvqPageBytes + (int64_t)r0 * kKvqHd;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 2 * i + half;
-    if (r < n_live) *reinterpret_cast<uint2*>(codes + r * kKvqHd + col) = code_row(v.x[i], e);
+  for (int kv = 0; kv < 2; ++kv) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = pow2i(__shfl_sync(0xffffffffu, e_src[kv], 2 * i + half));
+      float x[8];
+      kvq_decode8(raw[kv][i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= s;
+      a = finite_max(a, x);
+    }
+    const int e = kvq_exponent(warp_max(a));
+    uint8_t* const codes = p.c.c8[kv] + ph * kKvqPageBytes + (int64_t)r0 * kKvqHd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 2 * i + half;
+      const float s = pow2i(__shfl_sync(0xffffffffu, e_src[kv], r) - e);
+      float x[8];
+      kvq_decode8(raw[kv][i], x);
+      if (r < n_live) *reinterpret_cast<uint2*>(codes + r * kKvqHd + col) = code_row(x, s);
+    }
+    if (lane == 0) p.c.ex[kv][ph * kKvqSubs + r0 / kKvqSub] = (int8_t)e;
   }
-  if (lane == 0) p.c.ex[kv][ph * kKvqSubs + r0 / kKvqSub] = (int8_t)e;
 }
 
 // ---------------------------------------------------------------------------
@@ -411,6 +535,19 @@ dflash_status kvq_cache_ptrs_ok(const dflash_kvq_cache* c) {
   const void* const p[] = {c->k8_dev,    c->v8_dev,         c->k_exp_dev,
                            c->v_exp_dev, c->page_table_dev, c->status_dev};
   return kvq_ptrs_ok(p, 6);
+}
+
+int kvq_sms() {
+  static std::atomic<int> sms[kMaxDevices];
+  const int dev = current_device_slot();
+  if (dev < 0) return 1;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 1;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 KvqK kvq_device_view(const dflash_kvq_cache* c) {
@@ -506,8 +643,7 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
       budget > cache->pages_per_seq * kPageSlots || window < 0 || window > budget || !score ||
       !kept || !new_lens || !kvq_aligned(score, 4) || !kvq_aligned(kept, 4))
     return DFLASH_E_INVALID_ARG;
-  const int64_t warps =
-      (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub) * 2;
+  const int64_t warps = (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub);
   if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
   const void* const ptrs[] = {src_ids, dst_ids, kv_lens, score, kept, new_lens};
   DF_TRY(kvq_cache_ptrs_ok(cache));
@@ -524,8 +660,17 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
   p.budget = budget;
   p.window = window;
   cudaStream_t st = (cudaStream_t)stream;
-  if (launch_k(true, kvq_evict_select_kernel, dim3(cache->n_kv_heads, batch), dim3(kSelThreads), 0,
-               st, p) != cudaSuccess ||
+  // a CTA for every 4096 slots, up to a cluster of eight, but no more than the two CTAs
+  // per SM that fit at once
+  int C = 1;
+  while (C < kSelCluster && (int64_t)C * 4096 < max_keys &&
+         (int64_t)C * 2 * cache->n_kv_heads * batch <= 2 * kvq_sms())
+    C *= 2;
+  static std::atomic<bool> smem_done[kMaxDevices];
+  if (ensure_smem_attr(smem_done, kvq_evict_select_kernel, kSelSmem) != cudaSuccess)
+    return DFLASH_E_CUDA;
+  if (launch_k_cluster(true, dim3(C, 1, 1), kvq_evict_select_kernel, dim3(cache->n_kv_heads * C, batch),
+                       dim3(kSelThreads), kSelSmem, st, p, C) != cudaSuccess ||
       launch_k(true, kvq_evict_move_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st,
                p) != cudaSuccess)
     return DFLASH_E_CUDA;

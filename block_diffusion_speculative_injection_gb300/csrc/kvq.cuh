@@ -107,6 +107,7 @@ bool kvq_cache_ok(const dflash_kvq_cache* c);
 dflash_status kvq_ptrs_ok(const void* const* ptrs, int n);
 dflash_status kvq_cache_ptrs_ok(const dflash_kvq_cache* c);
 KvqK kvq_device_view(const dflash_kvq_cache* c);
+int kvq_sms();  // SM count of the current device (cached per device)
 inline bool kvq_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }

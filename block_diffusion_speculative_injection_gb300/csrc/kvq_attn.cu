@@ -963,19 +963,6 @@ static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t
   return (int)best;
 }
 
-static int kvq_sms() {
-  static std::atomic<int> sms[kMaxDevices];
-  const int dev = current_device_slot();
-  if (dev < 0) return 1;
-  int n = sms[dev].load(std::memory_order_relaxed);
-  if (n <= 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 1;
-    sms[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64 / G); }
 
 // ---------------------------------------------------------------------------
