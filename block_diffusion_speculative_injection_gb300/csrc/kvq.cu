@@ -50,7 +50,7 @@ struct AppendK {
   int batch, rows, n_blk;
 };
 
-__global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
+__global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -80,8 +80,10 @@ __global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
   }
   const int r0 = (int)(slot0 % kPageSlots);
   const int64_t ph = kvq_ph(p.c, page, head);
-  uint8_t* const codes = p.c.c8[kv] + ph * kKvqPageBytes + (int64_t)r0 * kKvqHd;
-  int8_t* const ex = p.c.ex[kv] + ph * kKvqSubs + r0 / kKvqSub;
+  uint8_t* const codes = (kv ? p.c.c8[1] : p.c.c8[0]) + ph * kKvqPageBytes + (int64_t)r0 * kKvqHd;
+  int8_t* const ex = (kv ? p.c.ex[1] : p.c.ex[0]) + ph * kKvqSubs + r0 / kKvqSub;
+  const bf16* const in = kv ? p.in[1] : p.in[0];
+  const long long stride = kv ? p.stride[1] : p.stride[0];
   const int half = lane >> 4, col = (lane & 15) * 8;
   const int n_old = (int)min(16LL, max(0LL, s0 - slot0));
   const int n_live = (int)min(16LL, end - slot0);
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
       raw[i].y = c.y;
     } else if (r < n_live) {
       const long long row = (long long)b * p.rows + (slot0 + r - s0);
-      raw[i] = *reinterpret_cast<const uint4*>(p.in[kv] + row * p.stride[kv] + head * kKvqHd + col);
+      raw[i] = *reinterpret_cast<const uint4*>(in + row * stride + head * kKvqHd + col);
     }
   }
   const float old_scale = pow2i(e_old);
@@ -124,7 +126,8 @@ __global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
   for (int off = 16; off > 0; off >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, off));
   const uint32_t top1 = max(top & 0xffffu, top >> 16);
   float a = __uint_as_float(top1 << 16);
-  if (n_old > 0 || top1 >= 0x7f80u) {
+  const bool plain = n_old == 0 && top1 < 0x7f80u;
+  if (!plain) {
     a = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -135,6 +138,20 @@ __global__ void __launch_bounds__(128, 6) kvq_append_kernel(const AppendK p) {
     a = warp_max(a);
   }
   const int e = kvq_exponent(a);
+  if (plain) {
+    const float s = pow2i(-e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x[8];
+      bf16x8_to_f(raw[i], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= s;
+      if (2 * i + half < n_live)
+        *reinterpret_cast<uint2*>(codes + (2 * i + half) * kKvqHd + col) = kvq_encode8(x);
+    }
+    if (lane == 0) *ex = (int8_t)e;
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 2 * i + half;
@@ -423,13 +440,15 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   cluster_sync();  // no CTA leaves while its counts may be read
 }
 
-// Move: one warp per block of 16 destination rows of a head, K and V.
-__global__ void __launch_bounds__(128, 6) kvq_evict_move_kernel(const EvictK p) {
+// Move: one warp per block of 16 destination rows of a head, of K or of V.
+__global__ void __launch_bounds__(128, 10) kvq_evict_move_kernel(const EvictK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int n_blk = (p.budget + kKvqSub - 1) / kKvqSub;
   uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int kv = (int)(w & 1);
+  w >>= 1;
   const int blk = (int)(w % (uint32_t)n_blk);
   w /= (uint32_t)n_blk;
   const int head = (int)(w % (uint32_t)p.c.Hkv), b = (int)(w / (uint32_t)p.c.Hkv);
@@ -450,54 +469,92 @@ __global__ void __launch_bounds__(128, 6) kvq_evict_move_kernel(const EvictK p) 
     set_dev_status(p.c.status, kDevCapacity);
     return;
   }
-  // its row in the pool (pages * heads * 128 < 2^31) and its exponents
-  int at = -1, e_src[2] = {0, 0};
+  uint8_t* const c8 = kv ? p.c.c8[1] : p.c.c8[0];
+  int8_t* const ex = kv ? p.c.ex[1] : p.c.ex[0];
+  // its row in the pool (pages * heads * 128 < 2^31) and its exponent
+  int at = -1, e_src = 0;
   if (lane < n_live) {
     const int page = kvq_page(p.c, src, from / kPageSlots);
     if (page >= 0) {
       at = (int)kvq_ph(p.c, page, head) * kPageSlots + from % kPageSlots;
-      e_src[0] = p.c.ex[0][at / kKvqSub];
-      e_src[1] = p.c.ex[1][at / kKvqSub];
+      e_src = ex[at / kKvqSub];
     } else {
       set_dev_status(p.c.status, kDevCapacity);
     }
   }
   const int half = lane >> 4, col = (lane & 15) * 8;
-  uint2 raw[2][8];
+  uint2 raw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int a = __shfl_sync(0xffffffffu, at, 2 * i + half);
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-      raw[kv][i] = a >= 0 ? *reinterpret_cast<const uint2*>(p.c.c8[kv] + (int64_t)a * kKvqHd + col)
-                          : make_uint2(0u, 0u);
+    raw[i] = a >= 0 ? *reinterpret_cast<const uint2*>(c8 + (int64_t)a * kKvqHd + col)
+                    : make_uint2(0u, 0u);
   }
-  const int r0 = d0 % kPageSlots;
-  const int64_t ph = kvq_ph(p.c, dpage, head);
+  // the largest magnitude: of a row's codes as integers (they order like their
+  // values, NaN on top: then value by value)
+  float a = 0.f;
+  bool nan = false;
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    float a = 0.f;
+  for (int i = 0; i < 8; ++i) {
+    constexpr uint32_t abs2 = 0x007f007fu;
+    uint32_t t = __vimax3_u16x2(raw[i].x & abs2, (raw[i].x >> 8) & abs2, raw[i].y & abs2);
+    t = __vmaxu2(t, (raw[i].y >> 8) & abs2);
+    const uint32_t top = max(t & 0xffffu, t >> 16);
+    nan = nan || top == 0x7fu;
+    const __half_raw hv = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)top, __NV_E4M3);
+    a = fmaxf(a, __half2float(*reinterpret_cast<const __half*>(&hv)) *
+                     pow2i(__shfl_sync(0xffffffffu, e_src, 2 * i + half)));
+  }
+  if (__any_sync(0xffffffffu, nan)) {
+    a = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = pow2i(__shfl_sync(0xffffffffu, e_src[kv], 2 * i + half));
+      const float s = pow2i(__shfl_sync(0xffffffffu, e_src, 2 * i + half));
       float x[8];
-      kvq_decode8(raw[kv][i], x);
+      kvq_decode8(raw[i], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= s;
       a = finite_max(a, x);
     }
-    const int e = kvq_exponent(warp_max(a));
-    uint8_t* const codes = p.c.c8[kv] + ph * kKvqPageBytes + (int64_t)r0 * kKvqHd;
+  }
+  const int e = kvq_exponent(warp_max(a));
+  const int drow = (int)kvq_ph(p.c, dpage, head) * kPageSlots + d0 % kPageSlots;
+  uint8_t* const codes = c8 + (int64_t)(drow + half) * kKvqHd + col;
+  // Rows move by k binades, k = their exponent minus the block's.  Within an fp16's range of
+  // k the values go by pairs: a code times 2^k is exact in fp16, but for bits far
+  // below half a step of the smallest code, so it is rounded once.
+  const bool far = lane < n_live && abs(e_src - e) > 14;
+  if (!__any_sync(0xffffffffu, far || nan)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 2 * i + half;
-      const float s = pow2i(__shfl_sync(0xffffffffu, e_src[kv], r) - e);
-      float x[8];
-      kvq_decode8(raw[kv][i], x);
-      if (r < n_live) *reinterpret_cast<uint2*>(codes + r * kKvqHd + col) = code_row(x, s);
+      const int k = __shfl_sync(0xffffffffu, e_src, 2 * i + half) - e;
+      const uint32_t sb = (uint32_t)(k + 15) << 10;  // 2^k in fp16
+      const uint32_t s2 = sb | (sb << 16);
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = j < 2 ? raw[i].x : raw[i].y;
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (j & 1))), __NV_E4M3);
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h),
+                                  *reinterpret_cast<const __half2*>(&s2));
+        c[j] = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&y), __NV_SATFINITE,
+                                          __NV_E4M3);
+      }
+      if (2 * i + half < n_live)
+        *reinterpret_cast<uint2*>(codes + 2 * i * kKvqHd) =
+            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     }
-    if (lane == 0) p.c.ex[kv][ph * kKvqSubs + r0 / kKvqSub] = (int8_t)e;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = pow2i(__shfl_sync(0xffffffffu, e_src, 2 * i + half) - e);
+      float x[8];
+      kvq_decode8(raw[i], x);
+      if (2 * i + half < n_live) *reinterpret_cast<uint2*>(codes + 2 * i * kKvqHd) = code_row(x, s);
+    }
   }
+  if (lane == 0) ex[drow / kKvqSub] = (int8_t)e;
 }
 
 // ---------------------------------------------------------------------------
@@ -643,7 +700,7 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
       budget > cache->pages_per_seq * kPageSlots || window < 0 || window > budget || !score ||
       !kept || !new_lens || !kvq_aligned(score, 4) || !kvq_aligned(kept, 4))
     return DFLASH_E_INVALID_ARG;
-  const int64_t warps = (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub);
+  const int64_t warps = (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub) * 2;
   if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
   const void* const ptrs[] = {src_ids, dst_ids, kv_lens, score, kept, new_lens};
   DF_TRY(kvq_cache_ptrs_ok(cache));

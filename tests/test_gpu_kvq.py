@@ -634,3 +634,53 @@ def test_score_many_q_tiles_and_pages():
         tol = 2.0 ** -22 + (2.0 ** -17 * top + 2.0 ** -18) * want
         assert ((out.double() - want).abs() <= tol).all()
         capi().dflash_kvq_check(c.h)
+
+
+def test_evict_recodes_rows_of_far_exponents_and_nan():
+    """Kept rows whose source blocks differ by up to 60 binades land in one
+    block; NaN codes stay NaN and do not count for the exponent."""
+    n, budget = 256, 64
+    c = Cache(1, 2, 2, seed=7)
+    rng = np.random.default_rng(7)
+    x = rng.normal(size=(1, n, 1, HD)) * 2.0 ** np.repeat(rng.integers(-30, 31, n // SUB), SUB)[:, None, None]
+    near = rng.normal(size=(1, n, 1, HD)) * 2.0 ** np.repeat(rng.integers(-7, 8, n // SUB), SUB)[:, None, None]
+    near[0, 40, 0, 3], near[0, 100, 0, 9] = np.nan, np.inf
+    c.append([0], x, near, seqs=[0])
+    score = torch.from_numpy(rng.random((2, 1, n)).astype(np.float32)).cuda()
+    score[0, 0, [40, 100]] = 2.0
+    kept = torch.zeros(1, 1, budget, dtype=torch.int32, device="cuda")
+    nl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    capi().dflash_kvq_evict(c.h, 1, i32([0]), i32([1]), i32([n]), n, budget, 8, score, kept, nl)
+    capi().dflash_kvq_check(c.h)
+    pick = kept[0, 0].tolist()
+    assert 40 in pick and 100 in pick
+    for x in "kv":
+        got = c.values(x)[1, :budget, 0]
+        rows = c.val[x][0][pick, 0]
+        for s in range(0, budget, SUB):
+            np.testing.assert_array_equal(got[s:s + SUB], ok.code_block(rows[s:s + SUB])[0])
+
+
+@pytest.mark.parametrize("n,kind", [(40000, "random"), (9000, "zeros"), (100000, "ties")])
+def test_evict_long_lists(n, kind):
+    """Lists longer than a cluster holds in shared memory, and all-equal scores."""
+    budget, window, pages = 3000, 100, (n + PAGE - 1) // PAGE
+    c = Cache(1, 2, pages, spare=0)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    score = torch.rand(2, 1, pages * PAGE, device="cuda", generator=g)
+    if kind == "zeros":
+        score.zero_()
+    elif kind == "ties":
+        score = torch.round(score * 8) / 8
+    kept = torch.zeros(1, 1, budget, dtype=torch.int32, device="cuda")
+    nl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    src = score[0, 0].clone()
+    for mk in (n, 1):  # a cluster of eight, and one CTA
+        kept.zero_()
+        capi().dflash_kvq_evict(c.h, 1, i32([0]), i32([1]), i32([n]), mk, budget, window, score, kept, nl)
+        key = src[:n - window].double().cpu().numpy()
+        best = np.lexsort((np.arange(n - window), -key))[:budget - window]
+        want = np.sort(np.concatenate([best, np.arange(n - window, n)]))
+        np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), want)
+        assert torch.equal(score[1, 0, :budget], src[torch.from_numpy(want).cuda()])
+        assert (score[1, 0, budget:] == 0).all()
