@@ -447,31 +447,53 @@ def dflash_spec_accept_sampled(batch, block, vocab, draft_logits, target_logits,
 MASK_NONE, MASK_CAUSAL, MASK_TREE = 0, 1, 2
 
 
-def _kvq_need(ok: bool, what: str) -> None:
-    if not ok:
-        raise DFlashError(1, what)
+def _kvq_refuse(what: str) -> None:
+    raise DFlashError(1, what)
 
 
-def _kvq_dense(t, name: str, dtype: str, shape) -> None:
-    """A contiguous tensor of one of these dtypes and this shape (None passes)."""
+_KVQ_DTYPES: dict = {}
+
+
+def _kvq_dtypes() -> dict:
+    """torch dtypes by the short names used below (torch is imported on first use)."""
+    if not _KVQ_DTYPES:
+        import torch
+        _KVQ_DTYPES.update(
+            i32=(torch.int32,), i8=(torch.int8,), f32=(torch.float32,), bf16=(torch.bfloat16,),
+            codes=(torch.uint8, torch.float8_e4m3fn), bits=(torch.int64, torch.uint64),
+            stream=torch._C._cuda_getCurrentRawStream, device=torch.cuda.current_device)
+    return _KVQ_DTYPES
+
+
+def _kvq_dense(t, name: str, dtype: str, shape: tuple) -> Optional[int]:
+    """Address of a contiguous tensor of this kind and shape (None passes)."""
     if t is None:
-        return
-    _kvq_need(str(t.dtype)[6:] in dtype.split("|") and tuple(t.shape) == tuple(shape)
-              and t.is_contiguous(),
-              f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}")
+        return None
+    if (t.dtype not in (_KVQ_DTYPES or _kvq_dtypes())[dtype] or t.shape != shape
+            or not t.is_contiguous()):
+        _kvq_refuse(f"{name}: need a contiguous {dtype} tensor of shape {shape}")
+    return t.data_ptr()
 
 
 def _kvq_rows(t, name: str, batch: int, rows: int, heads: int) -> int:
     """Elements between the rows of a bf16 [batch][rows][heads][128] tensor
     whose rows may be slices of wider ones."""
-    _kvq_need(str(t.dtype) == "torch.bfloat16" and tuple(t.shape) == (batch, rows, heads, 128),
-              f"{name}: need bfloat16 of shape {(batch, rows, heads, 128)}")
+    if (t.dtype not in (_KVQ_DTYPES or _kvq_dtypes())["bf16"]
+            or t.shape != (batch, rows, heads, 128)):
+        _kvq_refuse(f"{name}: need bfloat16 of shape {(batch, rows, heads, 128)}")
     sb, sr, sh, sd = t.stride()
     if rows == 1:
         sr = sb if batch > 1 else heads * 128
-    _kvq_need(sd == 1 and (sh == 128 or heads == 1) and (sb == rows * sr or batch == 1),
-              f"{name}: rows of {heads} * 128 elements, equally spaced, are needed")
+    if sd != 1 or (sh != 128 and heads > 1) or (sb != rows * sr and batch > 1):
+        _kvq_refuse(f"{name}: rows of {heads} * 128 elements, equally spaced, are needed")
     return sr
+
+
+def _kvq_stream(stream) -> int:
+    if stream is not None:
+        return _stream(stream)
+    d = _KVQ_DTYPES or _kvq_dtypes()
+    return d["stream"](d["device"]())
 
 
 class KvqCache:
@@ -481,14 +503,15 @@ class KvqCache:
     status [1] int32 (zero at the start)."""
 
     def __init__(self, k8, v8, k_exp, v_exp, page_table, status):
+        if k8.dim() != 4 or page_table.dim() != 2:
+            _kvq_refuse("k8: need [n_pages][n_kv_heads][128][128], page_table: [n_seqs][pages]")
         n_pages, heads = k8.shape[0], k8.shape[1]
         for t, name in ((k8, "k8"), (v8, "v8")):
-            _kvq_dense(t, name, "uint8|float8_e4m3fn", (n_pages, heads, PAGE_SLOTS, 128))
+            _kvq_dense(t, name, "codes", (n_pages, heads, PAGE_SLOTS, 128))
         for t, name in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-            _kvq_dense(t, name, "int8", (n_pages, heads, PAGE_SLOTS // 16))
-        _kvq_need(page_table.dim() == 2, "page_table: need [n_seqs][pages_per_seq]")
-        _kvq_dense(page_table, "page_table", "int32", page_table.shape)
-        _kvq_dense(status, "status", "int32", (1,))
+            _kvq_dense(t, name, "i8", (n_pages, heads, PAGE_SLOTS // 16))
+        _kvq_dense(page_table, "page_table", "i32", tuple(page_table.shape))
+        _kvq_dense(status, "status", "i32", (1,))
         self.tensors = (k8, v8, k_exp, v_exp, page_table, status)
         self.n_kv_heads = heads
         self.n_seqs, self.pages_per_seq = page_table.shape
@@ -507,36 +530,33 @@ def dflash_kvq_append(cache: KvqCache, batch, rows, seq_ids, start, counts, k, v
                       stream=None) -> None:
     """Writes bf16 rows k, v [batch][rows][n_kv_heads][128] (rows may be slices
     of wider ones) to slots start[b] .. start[b] + counts[b] - 1."""
-    for t, name in ((seq_ids, "seq_ids"), (start, "start"), (counts, "counts")):
-        _kvq_dense(t, name, "int32", (batch,))
-    ks = _kvq_rows(k, "k", batch, rows, cache.n_kv_heads)
-    vs = _kvq_rows(v, "v", batch, rows, cache.n_kv_heads)
-    _kvq_check(load().dflash_kvq_append(cache.ref, batch, rows, _ptr(seq_ids), _ptr(start),
-                                        _ptr(counts), _ptr(k), _ptr(v), ks, vs, _stream(stream)),
-               "dflash_kvq_append")
+    one, heads = (batch,), cache.n_kv_heads
+    _kvq_check(load().dflash_kvq_append(
+        cache.ref, batch, rows, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(start, "start", "i32", one), _kvq_dense(counts, "counts", "i32", one),
+        k.data_ptr(), v.data_ptr(), _kvq_rows(k, "k", batch, rows, heads),
+        _kvq_rows(v, "v", batch, rows, heads), _kvq_stream(stream)), "dflash_kvq_append")
 
 
 def dflash_kvq_read(cache: KvqCache, batch, rows, seq_ids, start, counts, k_out, v_out,
                     stream=None) -> None:
     """Values of slots start[b] + j, j < counts[b], as bf16 [batch][rows][n_kv_heads][128]."""
-    for t, name in ((seq_ids, "seq_ids"), (start, "start"), (counts, "counts")):
-        _kvq_dense(t, name, "int32", (batch,))
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _kvq_dense(t, name, "bfloat16", (batch, rows, cache.n_kv_heads, 128))
-    _kvq_check(load().dflash_kvq_read(cache.ref, batch, rows, _ptr(seq_ids), _ptr(start),
-                                      _ptr(counts), _ptr(k_out), _ptr(v_out), _stream(stream)),
-               "dflash_kvq_read")
+    one, out = (batch,), (batch, rows, cache.n_kv_heads, 128)
+    _kvq_check(load().dflash_kvq_read(
+        cache.ref, batch, rows, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(start, "start", "i32", one), _kvq_dense(counts, "counts", "i32", one),
+        _kvq_dense(k_out, "k_out", "bf16", out), _kvq_dense(v_out, "v_out", "bf16", out),
+        _kvq_stream(stream)), "dflash_kvq_read")
 
 
-def _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q):
-    for t, name in ((seq_ids, "seq_ids"), (kv_lens, "kv_lens"), (q_lens, "q_lens")):
-        _kvq_dense(t, name, "int32", (batch,))
-    words = 0
-    if mask == MASK_TREE:
-        _kvq_need(anc is not None and anc.dim() == 3, "anc: need [batch][block][words]")
-        words = anc.shape[2]
-        _kvq_dense(anc, "anc", "int64|uint64", (batch, block, words))
-    return words, _kvq_rows(q, "q", batch, block, n_heads)
+def _kvq_anc(anc, mask, batch, block):
+    """(address, words) of the ancestor bits of a tree pass."""
+    if mask != MASK_TREE:
+        return None, 0
+    if anc is None or anc.dim() != 3:
+        _kvq_refuse("anc: need [batch][block][words]")
+    words = anc.shape[2]
+    return _kvq_dense(anc, "anc", "bits", (batch, block, words)), words
 
 
 def dflash_kvq_attention_workspace(batch, n_heads, n_kv_heads, block, max_keys) -> int:
@@ -547,48 +567,51 @@ def dflash_kvq_attention(cache: KvqCache, batch, n_heads, block, mask, seq_ids, 
                          anc, max_keys, q, out, lse=None, workspace=None, stream=None) -> None:
     """Attention of q [batch][block][n_heads][128] (rows may be slices of wider
     ones) over the cache: out of that shape, lse [batch][block][n_heads]."""
-    words, qs = _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q)
-    _kvq_dense(out, "out", "bfloat16", (batch, block, n_heads, 128))
-    _kvq_dense(lse, "lse", "float32", (batch, block, n_heads))
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _kvq_check(load().dflash_kvq_attention(cache.ref, batch, n_heads, block, mask, _ptr(seq_ids),
-                                           _ptr(kv_lens), _ptr(q_lens), _ptr(anc), words, max_keys,
-                                           _ptr(q), qs, _ptr(out), _ptr(lse), _ptr(workspace),
-                                           nbytes, _stream(stream)), "dflash_kvq_attention")
+    one = (batch,)
+    bits, words = _kvq_anc(anc, mask, batch, block)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _kvq_check(load().dflash_kvq_attention(
+        cache.ref, batch, n_heads, block, mask, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(kv_lens, "kv_lens", "i32", one), _kvq_dense(q_lens, "q_lens", "i32", one), bits,
+        words, max_keys, q.data_ptr(), _kvq_rows(q, "q", batch, block, n_heads),
+        _kvq_dense(out, "out", "bf16", (batch, block, n_heads, 128)),
+        _kvq_dense(lse, "lse", "f32", (batch, block, n_heads)), ws, nbytes, _kvq_stream(stream)),
+        "dflash_kvq_attention")
 
 
 def dflash_kvq_score(cache: KvqCache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc,
                      max_keys, q, lse, decay, score_in, score_out, stream=None) -> None:
     """score_out = decay * score_in + the weights each slot received; scores
     [n_seqs][n_kv_heads][pages_per_seq * 128] (score_in None: zero)."""
-    words, qs = _kvq_attn_args(cache, batch, n_heads, block, mask, seq_ids, kv_lens, q_lens, anc, q)
-    _kvq_dense(lse, "lse", "float32", (batch, block, n_heads))
-    for t, name in ((score_in, "score_in"), (score_out, "score_out")):
-        _kvq_dense(t, name, "float32", (cache.n_seqs, cache.n_kv_heads, cache.slots))
-    _kvq_check(load().dflash_kvq_score(cache.ref, batch, n_heads, block, mask, _ptr(seq_ids),
-                                       _ptr(kv_lens), _ptr(q_lens), _ptr(anc), words, max_keys,
-                                       _ptr(q), qs, _ptr(lse), decay, _ptr(score_in),
-                                       _ptr(score_out), _stream(stream)), "dflash_kvq_score")
+    one, row = (batch,), (cache.n_seqs, cache.n_kv_heads, cache.slots)
+    bits, words = _kvq_anc(anc, mask, batch, block)
+    _kvq_check(load().dflash_kvq_score(
+        cache.ref, batch, n_heads, block, mask, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(kv_lens, "kv_lens", "i32", one), _kvq_dense(q_lens, "q_lens", "i32", one), bits,
+        words, max_keys, q.data_ptr(), _kvq_rows(q, "q", batch, block, n_heads),
+        _kvq_dense(lse, "lse", "f32", (batch, block, n_heads)), decay,
+        _kvq_dense(score_in, "score_in", "f32", row), _kvq_dense(score_out, "score_out", "f32", row),
+        _kvq_stream(stream)), "dflash_kvq_score")
 
 
 def dflash_kvq_evict(cache: KvqCache, batch, src_ids, dst_ids, kv_lens, max_keys, budget, window,
                      score, kept, new_lens, stream=None) -> None:
     """Keeps the last `window` slots and the best-scored others of sequences
     src_ids, `budget` in all, in the pages of sequences dst_ids."""
-    for t, name in ((src_ids, "src_ids"), (dst_ids, "dst_ids"), (kv_lens, "kv_lens"),
-                    (new_lens, "new_lens")):
-        _kvq_dense(t, name, "int32", (batch,))
-    _kvq_dense(score, "score", "float32", (cache.n_seqs, cache.n_kv_heads, cache.slots))
-    _kvq_dense(kept, "kept", "int32", (batch, cache.n_kv_heads, budget))
-    _kvq_check(load().dflash_kvq_evict(cache.ref, batch, _ptr(src_ids), _ptr(dst_ids),
-                                       _ptr(kv_lens), max_keys, budget, window, _ptr(score),
-                                       _ptr(kept), _ptr(new_lens), _stream(stream)),
-               "dflash_kvq_evict")
+    one, heads = (batch,), cache.n_kv_heads
+    _kvq_check(load().dflash_kvq_evict(
+        cache.ref, batch, _kvq_dense(src_ids, "src_ids", "i32", one),
+        _kvq_dense(dst_ids, "dst_ids", "i32", one), _kvq_dense(kv_lens, "kv_lens", "i32", one),
+        max_keys, budget, window, _kvq_dense(score, "score", "f32", (cache.n_seqs, heads, cache.slots)),
+        _kvq_dense(kept, "kept", "i32", (batch, heads, budget)),
+        _kvq_dense(new_lens, "new_lens", "i32", one), _kvq_stream(stream)), "dflash_kvq_evict")
 
 
 def dflash_kvq_check(cache: KvqCache, stream=None) -> None:
     """Waits for the stream, clears the cache's status word and raises if it was set."""
-    _kvq_check(load().dflash_kvq_check(cache.ref, _stream(stream)), "dflash_kvq_check")
+    _kvq_check(load().dflash_kvq_check(cache.ref, _kvq_stream(stream)), "dflash_kvq_check")
 
 
 def dflash_debug_trace(ctx, dst=None) -> None:
