@@ -123,8 +123,8 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 //   of one warp.
 //
 // Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle):
-//   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB; two stages of K and two of
-//   V [128 slots][128], 16 KB each.  96 KB, so two CTAs share an SM: one's softmax
+//   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB, twice; two stages of K and two
+//   of V [128 slots][128], 16 KB each.  112 KB, so two CTAs share an SM: one's softmax
 //   runs beside the other's MMAs and loads.
 // Tensor memory: 256 columns, S [64 rows][128] twice and O [128 operand rows][128].  An
 // M = 64 accumulator keeps row m in lane (m / 16) * 32 + m % 16, so a second one fits
@@ -140,15 +140,15 @@ constexpr int kTile = kPageSlots;
 constexpr uint32_t kTileBytes = kTile * kKvqHd;  // one K or V tile, and P
 constexpr uint32_t kQPart = 64 * kKvqHd;
 constexpr uint32_t kAOffP = 2 * kQPart;
-constexpr uint32_t kAOffK = kAOffP + kTileBytes;
+constexpr uint32_t kAOffK = kAOffP + 2 * kTileBytes;
 constexpr int kAStages = 2;
 constexpr uint32_t kAOffV = kAOffK + kAStages * kTileBytes;
-constexpr uint32_t kAOffNan = kAOffV + kAStages * kTileBytes;  // [128 slots][4] bits of NaN dims
-constexpr uint32_t kAOffQs = kAOffNan + kTile * 16;  // scale of each query row
+constexpr uint32_t kAOffQs = kAOffV + kAStages * kTileBytes;  // scale of each query row
 constexpr uint32_t kAOffBar = kAOffQs + 64 * 4;
 constexpr uint32_t kORow = kKvqHd * 4 + 16;  // an accumulator row staged over the tiles, padded
-static_assert(128 * kORow <= kAOffNan, "accumulator rows fit");
-constexpr int kAttnQSmem = (int)kAOffBar + 256 + 1024;  // barriers, alignment slack
+static_assert(128 * kORow <= kAOffQs, "accumulator rows fit");
+constexpr int kAttnQSmem = (int)kAOffBar + 256;  // barriers
+static_assert(2 * (kAttnQSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
 constexpr int kAttnQThreads = 192;
 constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
 constexpr uint32_t kSOdd = 16u << 16;  // lane offset of the S buffer of odd tiles
@@ -382,7 +382,7 @@ struct KvqMaps {
 // barrier's ordering): gives up after about 2 s, like mbar_wait.  A poll may suspend
 // the warp for up to 20 us (a hint), so a waiting warp leaves its issue slots to
 // the others, and the clock is read only after such a poll has failed.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* status) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
@@ -392,7 +392,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "r"(bar), "r"(parity), "r"(20000u)
         : "memory");
     if (ok) return true;
     if ((i & 15u) == 0) {
@@ -403,6 +403,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
   }
   set_dev_status(status, kDevTimeout);
   return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return warp_wait(smem_u32(bar), parity, status);
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // one lane of a converged warp, the same one every time
 __device__ __forceinline__ bool elect_one() {
@@ -416,9 +422,10 @@ __device__ __forceinline__ bool elect_one() {
 __global__ void __launch_bounds__(kAttnQThreads, 2)
     kvq_attn_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
   pdl_wait();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // (the swizzled tiles want 1024-byte alignment, and two CTAs' shared memory leaves
+  // no slack for it)
+  uint8_t* const sm = smem_raw;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int POS = p.pos;
   const int b = blockIdx.z / p.n_splits, split = blockIdx.z % p.n_splits;
@@ -431,14 +438,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   if (warp < 4) load_q(p, b, kvh, j0, warp, lane, q_raw);
 
   uint8_t* const ps = sm + kAOffP;
-  uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(sm + kAOffNan);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kAOffBar);
   uint64_t* const q_full = bars;
   uint64_t* const s_full = bars + 1;  // two S buffers
   uint64_t* const s_free = bars + 3;
-  uint64_t* const p_full = bars + 5;
-  uint64_t* const pv_done = bars + 6;
-  uint64_t* const k_full = bars + 7;
+  uint64_t* const p_full = bars + 5;  // two P buffers
+  uint64_t* const pv_done = bars + 7;
+  uint64_t* const k_full = bars + 9;
   uint64_t* const k_empty = k_full + kAStages;
   uint64_t* const v_full = k_empty + kAStages;
   uint64_t* const v_empty = v_full + kAStages;
@@ -451,9 +457,9 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
     }
-    mbar_init(p_full, 4);
-    mbar_init(pv_done, 1);
     mbar_init(meet, 4);
     for (int i = 0; i < kAStages; ++i) {
       mbar_init(&k_full[i], 1);
@@ -464,13 +470,16 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     *nan_any = 0;
     mbar_fence_init();
   }
-  if (warp < 4) *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
   if (warp == 4) {
     tmem_alloc(tslot, kAttnQTmem);
     tmem_relinquish();
   }
   int key_end;
-  const bool work = kvq_entry_check(p, entry, key_end) && j0 < entry.r;
+  bool work = kvq_entry_check(p, entry, key_end) && j0 < entry.r;
+  if ((smem_u32(sm) & 1023u) != 0) {
+    set_dev_status(status, kDevCheck);
+    work = false;
+  }
   const int seq = entry.seq, n = entry.n, r = entry.r;
   const int j1 = min(j0 + POS, r), ctx = n - r;
   const KvqSpan span = kvq_span(p, n, r, key_end, j1);
@@ -584,17 +593,17 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     for (int t = 0; ok && t < n_tiles; ++t) {
       const int st = t % kAStages;
       ok = warp_wait(&v_full[st], (t / kAStages) & 1, status);
-      if (ok) ok = warp_wait(p_full, t & 1, status);
+      if (ok) ok = warp_wait(&p_full[t & 1], (t >> 1) & 1, status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       if (leader) {
-        const uint64_t vd = v_desc + st * (kTileBytes >> 4);
+        const uint64_t vd = v_desc + st * (kTileBytes >> 4), pd = p_desc + (t & 1) * (kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f8(tmem + kTmemOCol, p_desc + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
+          tc_mma_f8(tmem + kTmemOCol, pd + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
                     t + kk > 0 ? 1u : 0u);
-        tc_commit(pv_done);
+        tc_commit(&pv_done[t & 1]);
         tc_commit(&v_empty[st]);
       }
       __syncwarp();
@@ -624,14 +633,20 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     float m_used = -INFINITY, l = 0.f;
     uint32_t bad[4] = {0u, 0u, 0u, 0u};  // dims in which the row saw a NaN of V
     bool ok = true;
-    // page and exponents of tile t, read a tile ahead
-    auto exps_of = [&](int pg) -> uint2 {
-      if (pg < 0) return make_uint2(0u, 0u);
-      const int64_t at = kvq_ph(p.c, pg, kvh) * kKvqSubs + 4 * h;
-      return make_uint2(*reinterpret_cast<const uint32_t*>(p.c.ex[0] + at),
-                        *reinterpret_cast<const uint32_t*>(p.c.ex[1] + at));
+    // Page ids are read two tiles ahead, exponents one: from running pointers, few
+    // instructions each (a warp spends about four cycles on every one of them).
+    const int32_t* next_id = p.c.tab + (int64_t)seq * p.c.pps + first_page;
+    const int8_t* const k_ex = p.c.ex[0] + kvh * kKvqSubs + 4 * h;
+    const int8_t* const v_ex = p.c.ex[1] + kvh * kKvqSubs + 4 * h;
+    const int page_ex = p.c.Hkv * kKvqSubs;  // exponents of a page
+    auto exps_of = [&](int pg) -> uint2 {    // (of page 0 in place of an unmapped one)
+      const int64_t at = (int64_t)max(pg, 0) * page_ex;
+      return make_uint2(*reinterpret_cast<const uint32_t*>(k_ex + at),
+                        *reinterpret_cast<const uint32_t*>(v_ex + at));
     };
-    auto wait_for = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const uint32_t b_s_full = smem_u32(s_full), b_s_free = smem_u32(s_free);
+    const uint32_t b_p_full = smem_u32(p_full), b_pv = smem_u32(pv_done);
+    auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, warp_wait(bar, parity, status));
     };
     // a barrier of the four warps whose wait is bounded like every other
@@ -639,23 +654,26 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     auto warps_meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(meet);
-      ok = wait_for(meet, met++ & 1);
+      ok = wait_for(smem_u32(meet), met++ & 1);
       return ok;
     };
-    int pg = kvq_page(p.c, seq, first_page);
-    int raw_next = n_tiles > 1 ? kvq_page_load(p.c, seq, first_page + 1) : -1;
+    int pg = kvq_page_check(p.c, *next_id++);
+    int raw_next = n_tiles > 1 ? *next_id++ : -1;
     uint2 ex = exps_of(pg);
 #pragma unroll 1
     for (int t = 0; t < n_tiles; ++t) {
       const int tile0 = k_begin + t * kTile;
       const int pg_now = pg;
       const uint2 ex_now = ex;
-      pg = kvq_page_check(p.c, raw_next);
-      raw_next = t + 2 < n_tiles ? kvq_page_load(p.c, seq, first_page + t + 2) : -1;
-      ex = t + 1 < n_tiles ? exps_of(pg) : make_uint2(0u, 0u);
+      const uint32_t odd8 = (t & 1) * 8, phase = (t >> 1) & 1;
+      if (t + 1 < n_tiles) {
+        pg = kvq_page_check(p.c, raw_next);
+        ex = exps_of(pg);
+        if (t + 2 < n_tiles) raw_next = *next_id++;
+      }
       const int stop = pg_now < 0 ? tile0 : k_stop;  // slots from here on are not seen
       const bool masked = tile0 + kTile > min(stop, mask_from);
-      if (!(ok = wait_for(&s_full[t & 1], (t >> 1) & 1))) break;
+      if (!(ok = wait_for(b_s_full + odd8, phase))) break;
       float s[64];
       if (warp_live) {
         tc_fence_after();
@@ -666,7 +684,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[t & 1]);
+      if (lane == 0) bar_arrive(b_s_free + odd8);
       float ck[4], ev[4], mx = -INFINITY;
       if (warp_live) {
         if (masked) {
@@ -689,14 +707,16 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       }
-      // P V(t - 1) done: P is free, and O holds tiles 0 .. t - 1 (a warp without
-      // rows waits too: its arrival below must not count for an earlier tile)
-      if (t > 0 && !(ok = wait_for(pv_done, (t - 1) & 1))) break;
+      // P V(t - 2) done: this P buffer is free (a warp without rows waits too: its
+      // arrival below must not count for an earlier tile)
+      if (t >= 2 && !(ok = wait_for(b_pv + odd8, phase ^ 1))) break;
       if (warp_live) {
         const bool grow_m = mx > m_used + kLazyLog2;
         if (__any_sync(0xffffffffu, grow_m)) {
           const float alpha = grow_m ? ex2(m_used - mx) : 1.f;
           if (t > 0) {
+            // O holds tiles 0 .. t - 1 once P V(t - 1) is done
+            if (!(ok = wait_for(b_pv + (odd8 ^ 8), ((t - 1) >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -734,7 +754,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
             split_weights(z, 4 * w, c1[w], c2[w]);
           }
           l = fmaf(sum.x + sum.y, pow2i(-(int)ev[i]), l);
-          const uint32_t off = (uint32_t)(32 * warp + t16) * 128 +
+          const uint32_t off = (t & 1) * kTileBytes + (uint32_t)(32 * warp + t16) * 128 +
                                ((uint32_t)((4 * h + i) ^ (t16 & 7)) << 4);
           *reinterpret_cast<uint4*>(ps + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
           *reinterpret_cast<uint4*>(ps + off + 16 * 128) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
@@ -743,10 +763,16 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       // V rows that are not seen must not hold NaN codes (0 * NaN): those behind
       // the split's slots, or on no page, are zeroed; in rows that some query
       // rows see and others do not, NaN codes are zeroed and noted for the rows
-      // that see them
+      // that see them (in a table [128 slots][4] of dims' bits, over the other P
+      // buffer)
       if (tile0 + kTile > min(stop, partial_from)) {
         const int st = t % kAStages;
-        if (!(ok = wait_for(&v_full[st], (t / kAStages) & 1))) break;
+        ok = wait_for(smem_u32(&v_full[st]), (t / kAStages) & 1);
+        if (ok && t > 0) ok = wait_for(b_pv + (odd8 ^ 8), ((t - 1) >> 1) & 1);
+        if (!ok) break;
+        uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(ps + (~t & 1) * kTileBytes);
+        *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
+        if (!warps_meet()) break;
         uint8_t* const vs = sm + kAOffV + st * kTileBytes;
         const int v_end = max(stop - tile0, 0), v_from = max(0, min(v_end, partial_from - tile0));
 #pragma unroll 1
@@ -785,7 +811,6 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
             }
           }
           if (!warps_meet()) break;
-          *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
           if (threadIdx.x == 0) *nan_any = 0;
           if (!warps_meet()) break;
         }
@@ -793,13 +818,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) bar_arrive(b_p_full + odd8);
     }
     // ---- epilogue: lanes t and t + 16 hold the P1 and the P2 part of row t's O
     l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k) bad[k] |= __shfl_xor_sync(0xffffffffu, bad[k], 16);
-    if (ok) ok = wait_for(pv_done, (n_tiles - 1) & 1);
+    if (ok) ok = wait_for(b_pv + ((n_tiles - 1) & 1) * 8, ((n_tiles - 1) >> 1) & 1);
     if (ok && warp_live) {
       tc_fence_after();
       const bool none = l == 0.f;
