@@ -966,21 +966,27 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
 }
 
-// Splits of a launch of `ctas` CTAs over max_keys slots: the count that minimises
-// waves of resident CTAs (two per SM) x (tiles per split + two tiles' worth of
-// fixed cost), as many as the workspace holds.
+// Splits of a launch of `ctas` CTAs over max_keys slots: the count, as many as the
+// workspace holds, that minimises the time of the fullest SM in units of a tile when
+// two CTAs share the SM.  Such a pair takes 2 units a tile of each, a CTA alone 1.4; a CTA's
+// set-up and output cost 6 beside its tiles; merging costs a unit for every 7200
+// (row, head) outputs of a split.  (Measured at a batch of 8, 16,400 slots, 16 rows, 32 heads
+// over 8: 1 to 9 splits 150, 86, 78, 64, 84, 81, 74, 76, 67 us, 4 taken; 1000 rows over about
+// 4000 slots: 226 us unsplit, 265 with 2 splits.)
 constexpr int kKvqMaxSplits = 256;
 static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t max_splits,
-                           int fixed = 2) {
+                           int64_t merge_rows) {
   const int64_t tiles = (max_keys + kTile - 1) / kTile;
-  const int64_t slots = 2 * (int64_t)sm_count;
   const int64_t top = std::min(std::min<int64_t>(kKvqMaxSplits, tiles), max_splits);
-  int64_t best = 1, best_cost = INT64_MAX;
+  int64_t best = 1;
+  double best_cost = 0;
   for (int64_t sp = 1; sp <= top; ++sp) {
     const int64_t per = (tiles + sp - 1) / sp;
     if (sp > 1 && (tiles + per - 1) / per < sp) continue;  // some would be empty
-    const int64_t cost = ((ctas * sp + slots - 1) / slots) * (per + fixed) + (sp > 1 ? 1 : 0);
-    if (cost < best_cost) {
+    const int64_t on_sm = (ctas * sp + sm_count - 1) / sm_count;
+    const double cost = (on_sm / 2) * (2.0 * per + 6) + (on_sm % 2) * (1.4 * per + 6) +
+                        (sp > 1 ? sp * (merge_rows / 7200.0) + 1 : 0);
+    if (sp == 1 || cost < best_cost) {
       best_cost = cost;
       best = sp;
     }
@@ -1394,7 +1400,8 @@ int64_t dflash_kvq_attention_workspace(int32_t batch, int32_t n_heads, int32_t n
                                        int32_t block, int32_t max_keys) {
   if (!kvq_attn_shape_ok(batch, n_heads, n_kv_heads, block, max_keys)) return -1;
   const int64_t ctas = kvq_q_tiles(block, n_heads / n_kv_heads) * n_kv_heads * batch;
-  const int splits = kvq_plan_splits(kvq_sms(), ctas, max_keys, 65535 / batch);
+  const int splits = kvq_plan_splits(kvq_sms(), ctas, max_keys, 65535 / batch,
+                                     (int64_t)batch * block * n_heads);
   return splits == 1 ? 0 : splits * kvq_part_bytes(batch, block, n_heads);
 }
 
@@ -1418,7 +1425,7 @@ dflash_status dflash_kvq_attention(const dflash_kvq_cache* cache, int32_t batch,
   const int64_t q_tiles = kvq_q_tiles(block, p.G), rh = (int64_t)batch * block * n_heads;
   const int64_t room = workspace ? workspace_bytes / kvq_part_bytes(batch, block, n_heads) : 0;
   p.n_splits = kvq_plan_splits(kvq_sms(), q_tiles * cache->n_kv_heads * batch, max_keys,
-                               std::max<int64_t>(1, std::min<int64_t>(room, 65535 / batch)));
+                               std::max<int64_t>(1, std::min<int64_t>(room, 65535 / batch)), rh);
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = p.part_o + p.n_splits * rh * kKvqHd;
   KvqMaps maps;
@@ -1459,8 +1466,8 @@ dflash_status dflash_kvq_score(const dflash_kvq_cache* cache, int32_t batch, int
   p.decay = decay;
   p.score_in = score_in;
   p.score_out = score_out;
-  // spans of pages: as for the attention's splits
-  const int splits = kvq_plan_splits(kvq_sms(), (int64_t)cache->n_kv_heads * batch, max_keys, 65535, 4);
+  // spans of pages: as for the attention's splits, with nothing to merge
+  const int splits = kvq_plan_splits(kvq_sms(), (int64_t)cache->n_kv_heads * batch, max_keys, 65535, 0);
   KvqMaps maps;
   const uint64_t kv_rows = (uint64_t)cache->n_pages * cache->n_kv_heads * kPageSlots;
   if (!encode_tmap_rows128(&maps.k, cache->k8_dev, kv_rows, kTile)) return DFLASH_E_CUDA;
