@@ -1012,7 +1012,6 @@ static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64
 // weights and sums; warp 4: TMA of K; warp 5: MMAs.
 // ---------------------------------------------------------------------------
 constexpr int kSGroup = 4;
-constexpr int kUnmapped = 127;  // in place of the exponent of a slot without a page
 constexpr uint32_t kSOffQ = kSGroup * kTileBytes;
 constexpr uint32_t kSOffRow = kSOffQ + 2 * 2 * kQPart;   // [3][64] float2
 constexpr uint32_t kSOffQs = kSOffRow + 3 * 64 * 8;      // [64] float, conversion scratch
@@ -1065,8 +1064,9 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   // q tiles that can see a slot from `tile` on (causal: rows j >= slot - ctx)
   const int q_tiles = (r + p.pos - 1) / p.pos;
   auto q_first = [&](int tile) -> int {
-    if (p.mask != DFLASH_MASK_CAUSAL) return 0;
-    return min(max(0, tile * kTile - ctx) / p.pos, q_tiles);
+    const int i = tile * kTile - ctx;  // block slot of the page's first one
+    if (p.mask != DFLASH_MASK_CAUSAL || i <= 0) return 0;
+    return min(i / p.pos, q_tiles);
   };
   tc_fence_before();
   __syncthreads();
@@ -1194,22 +1194,24 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     // load is waited for before its group begins).
     int page[kSGroup], exps[kSGroup];
     float old[kSGroup];
+    uint32_t mapped = 0;  // a bit for each page of the group just read
+    const int32_t* const ids = p.c.tab + (int64_t)seq * p.c.pps + t_begin;
+    const int8_t* const k_ex = p.c.ex[0] + kvh * kKvqSubs + slot / kKvqSub;
+    const int page_ex = p.c.Hkv * kKvqSubs;
+    const float* const in_row = p.score_in ? p.score_in + out_row + (int64_t)t_begin * kTile : nullptr;
+    const int last_slot = key_end - 1 - t_begin * kTile;  // of the span's, from t_begin on
     auto read_pages = [&](int g) {
 #pragma unroll
-      for (int m = 0; m < kSGroup; ++m)
-        page[m] = g + m < n_tiles ? kvq_page_load(p.c, seq, t_begin + g + m) : -1;
+      for (int m = 0; m < kSGroup; ++m) page[m] = ids[min(g + m, n_tiles - 1)];
     };
-    auto read_group = [&](int g) {
+    auto read_group = [&](int g) {  // (loads without conditions: nothing waits for them here)
+      mapped = 0;
 #pragma unroll
       for (int m = 0; m < kSGroup; ++m) {
-        const int t = t_begin + g + m;
         const int pg = kvq_page_check(p.c, page[m]);
-        exps[m] = pg >= 0
-                      ? p.c.ex[0][kvq_ph(p.c, pg, kvh) * kKvqSubs + slot / kKvqSub]
-                      : kUnmapped;
-        old[m] = p.score_in && g + m < n_tiles && t * kTile + slot < key_end
-                     ? p.score_in[out_row + (int64_t)t * kTile + slot]
-                     : 0.f;
+        mapped |= (pg >= 0 ? 1u : 0u) << m;
+        exps[m] = k_ex[(int64_t)max(pg, 0) * page_ex];
+        old[m] = in_row ? in_row[min((g + m) * kTile + slot, last_slot)] : 0.f;
       }
     };
     // conversions run one q tile ahead: the next one is tile cq, for group cg
@@ -1250,8 +1252,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       if (qt == q0) {
 #pragma unroll
         for (int m = 0; m < kSGroup; ++m) {
-          mine[m * kTile] = make_float2(exps[m] == kUnmapped ? 0.f : pow2i(exps[m]), 0.f);
-          base[m] = p.score_in ? p.decay * old[m] : 0.f;
+          mine[m * kTile] = make_float2((mapped >> m) & 1u ? pow2i(exps[m]) : 0.f, 0.f);
+          base[m] = in_row ? p.decay * old[m] : 0.f;
         }
         if (g + kSGroup < n_tiles) {
           read_group(g + kSGroup);
