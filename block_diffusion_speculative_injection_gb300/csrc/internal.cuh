@@ -470,6 +470,10 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// adds to a word of a cluster CTA's shared memory (map_peer's address)
+__device__ __forceinline__ void red_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // four consecutive fp32 (16-byte aligned address)
 __device__ __forceinline__ float4 ld_peer_f32x4(uint32_t addr) {
   float4 v;

@@ -264,16 +264,16 @@ __device__ __forceinline__ bool evict_entry(const EvictK& p, int b, int& src, in
 // Select: a cluster of C CTAs per (entry, head), CTA c on the slots [c, c + 1) * chunk of
 // the w0 slots before the window.  Three passes find the K-th largest key T eleven bits
 // at a time (the last one ten): a histogram of the candidates' next bits in each
-// CTA, summed over the cluster through distributed shared memory by every CTA for
-// itself.  The keys are held in shared memory after the first pass (what does
+// CTA, whose bins that are not empty are added to the cluster's totals (a quarter of
+// the bins in each of four CTAs, say) through distributed shared memory.  The keys are held in shared memory after the first pass (what does
 // not fit is read again).  Then the kept slots (above T, and the first of those
 // equal to T) are counted per warp and written in order.
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelKeys = 8192;  // keys a CTA holds
 constexpr int kSelCluster = 8;  // most CTAs of a cluster
-// [3][bins] histograms, keys; the dynamic part of the shared memory
-constexpr int kSelSmem = (3 * kSelBins + kSelKeys) * 4;
+// [3][bins] histograms, [3][bins] totals, keys; the dynamic part of the shared memory
+constexpr int kSelSmem = (6 * kSelBins + kSelKeys) * 4;
 
 __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const EvictK p, const int C) {
   pdl_trigger();
@@ -292,17 +292,23 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   const int all = C * kSelThreads, gid = rank * kSelThreads + tid;
   if (head == 0 && gid == 0) p.new_lens[b] = m;
   // what needs no selection: the window, and the ends of the lists
-  for (int i = w0 + gid; i < n; i += all) {
-    kept[K + i - w0] = i;
-    dsc[K + i - w0] = sc[i];
+  auto rest = [&]() {
+    for (int i = w0 + gid; i < n; i += all) {
+      kept[K + i - w0] = i;
+      dsc[K + i - w0] = sc[i];
+    }
+    for (int i = m + gid; i < p.budget; i += all) kept[i] = -1;
+    for (int64_t i = m + gid; i < cap; i += all) dsc[i] = 0.f;
+  };
+  if (K == 0) {
+    rest();
+    return;
   }
-  for (int i = m + gid; i < p.budget; i += all) kept[i] = -1;
-  for (int64_t i = m + gid; i < cap; i += all) dsc[i] = 0.f;
-  if (K == 0) return;
 
   extern __shared__ uint32_t sel_smem[];
   uint32_t* const hist = sel_smem;
-  uint32_t* const held = sel_smem + 3 * kSelBins;
+  uint32_t* const total = C > 1 ? sel_smem + 3 * kSelBins : hist;
+  uint32_t* const held = sel_smem + 6 * kSelBins;
   __shared__ uint32_t s_digit, s_left;
   __shared__ uint32_t s_cnt[2];               // this CTA's keys above and equal to T
   __shared__ uint32_t s_warp[2][kSelWarps];
@@ -312,8 +318,15 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   auto key_at = [&](int i) -> uint32_t {
     return i - i0 < kSelKeys ? held[i - i0] : score_key(sc[i]);
   };
-  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) hist[i] = 0;
-  __syncthreads();
+  for (int i = tid; i < 6 * kSelBins; i += kSelThreads) sel_smem[i] = 0;
+  // (before another CTA adds to the totals)
+  auto sync_all = [&]() {
+    if (C > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  };
+  sync_all();
   // T's known high bits, and the rank of T among the keys that share them
   uint32_t prefix = 0, left = (uint32_t)K;
 #pragma unroll 1
@@ -351,23 +364,28 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
         }
       }
     }
-    cluster_sync();
     // the cluster's histogram, four bins a thread from the top down: thread t has
-    // bins 2047 - 4 t - {0, 1, 2, 3}
-    uint32_t cnt[4] = {0, 0, 0, 0}, mine = 0;
+    // bins 2047 - 4 t - {0, 1, 2, 3}, whose totals are kept by CTA t % C
+    uint32_t cnt[4], mine = 0;
     const int base = kSelBins - 4 - 4 * tid;
-    float4 peer[kSelCluster];
+    uint32_t* const sum = total + pass * kSelBins + base;
+    if (C > 1) {
+      __syncthreads();
+      const uint32_t owner = map_peer(smem_u32(sum), tid % C);
 #pragma unroll
-    for (int c = 0; c < kSelCluster; ++c)
-      if (c < C) peer[c] = ld_peer_f32x4(map_peer(smem_u32(h + base), c));
+      for (int j = 0; j < 4; ++j)
+        if (h[base + j]) red_peer_u32(owner + 4 * j, h[base + j]);
+      cluster_sync();
+      const float4 v = ld_peer_f32x4(owner);
+      cnt[0] = __float_as_uint(v.w);
+      cnt[1] = __float_as_uint(v.z);
+      cnt[2] = __float_as_uint(v.y);
+      cnt[3] = __float_as_uint(v.x);
+    } else {
+      __syncthreads();
 #pragma unroll
-    for (int c = 0; c < kSelCluster; ++c)
-      if (c < C) {
-        cnt[0] += __float_as_uint(peer[c].w);
-        cnt[1] += __float_as_uint(peer[c].z);
-        cnt[2] += __float_as_uint(peer[c].y);
-        cnt[3] += __float_as_uint(peer[c].x);
-      }
+      for (int j = 0; j < 4; ++j) cnt[j] = sum[3 - j];
+    }
     mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
     uint32_t incl = mine;
 #pragma unroll
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
         __reduce_add_sync(0xffffffffu, lane < kSelWarps ? s_warp[warp][lane] : 0u);
     if (lane == 0) s_cnt[warp] = sum;
   }
-  cluster_sync();
+  sync_all();
   // before this warp: the lower CTAs' (one a lane) and the lower warps' counts
   uint32_t above = lane < warp ? s_warp[0][lane] : 0u, equal = lane < warp ? s_warp[1][lane] : 0u;
   if (lane < rank) {
@@ -437,7 +455,8 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
     above += __popc(bg);
     equal += __popc(be);
   }
-  cluster_sync();  // no CTA leaves while its counts may be read
+  rest();
+  if (C > 1) cluster_sync();  // no CTA leaves while its counts may be read
 }
 
 // Move: one warp per block of 16 destination rows of a head, of K or of V.
