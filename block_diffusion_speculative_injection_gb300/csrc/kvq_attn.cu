@@ -27,6 +27,7 @@ struct KvqAttnK {
   float decay;
   int pos, g_inv;  // block positions of a CTA's 64 rows; row / G = row * g_inv >> 16 (row < 64)
   int q_tiles, n_splits;
+  uint32_t two;  // 2, see split_weights
   float *part_o, *part_ml;  // [split][row][head][128], [split][row][head] (m, l)
 };
 
@@ -182,7 +183,10 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 // of them, so codes and roundings are integer operations on its bits:
 //   p1 / 2^8 = y rounded to 4 bits, y = z / 16 (exponent bits - 4; zero for y < 2^-14,
 //   which p2 holds alone), p2 / 2^8 = z - 16 y rounded to 4 bits with a dither.
-__device__ __forceinline__ void split_weights(const float* z, int at, uint32_t& c1, uint32_t& c2) {
+// The doublings are multiply-adds by `two` (a 2 the compiler cannot see): they run
+// beside the logic operations, whose pipe bounds this code.
+__device__ __forceinline__ void split_weights(const float* z, int at, uint32_t two, uint32_t& c1,
+                                              uint32_t& c2) {
   uint32_t d[2], w[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {  // slots at + k and at + k + 2
@@ -197,10 +201,11 @@ __device__ __forceinline__ void split_weights(const float* z, int at, uint32_t& 
     const int i = at + k;
     const uint32_t rev = ((i & 1) << 3) | ((i & 2) << 1) | ((i & 4) >> 1) | ((i & 8) >> 3);
     const uint32_t dither = (4 + 8 * rev) | ((4 + 8 * (rev | 4)) << 16);  // i + 2: bit 1 set
-    w[k] = ((rb + rb + 2 * dither) & 0x7fff7fffu) | (rb & 0x80008000u);
+    w[k] = ((rb * two + 2 * dither) & 0x7fff7fffu) | (rb & 0x80008000u);
+    d[k] = d[k] * two;
   }
-  c1 = (d[0] >> 7) + (d[1] << 1);  // codes in bits 14..7 of each half
-  c2 = __byte_perm(w[0], w[1], 0x7351);  // codes in the high bytes
+  c1 = __byte_perm(d[0], d[1], 0x7351);  // codes in the high byte of each half
+  c2 = __byte_perm(w[0], w[1], 0x7351);
 }
 
 // (a0, a1) * b + c and (a0, a1) + (b0, b1) in one instruction each
@@ -751,7 +756,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
               z[k + 1] = ex2(x.y);
               sum = add2(sum, make_float2(z[k], z[k + 1]));
             }
-            split_weights(z, 4 * w, c1[w], c2[w]);
+            split_weights(z, 4 * w, p.two, c1[w], c2[w]);
           }
           l = fmaf(sum.x + sum.y, pow2i(-(int)ev[i]), l);
           const uint32_t off = (t & 1) * kTileBytes + (uint32_t)(32 * warp + t16) * 128 +
@@ -1385,6 +1390,7 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   p->H = H;
   p->G = H / cache->n_kv_heads;
   p->pos = 64 / p->G;
+  p->two = 2;
   p->q_tiles = (block + p->pos - 1) / p->pos;
   p->g_inv = (65536 + p->G - 1) / p->G;
   p->q = static_cast<const bf16*>(q);
