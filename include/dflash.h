@@ -586,7 +586,8 @@ DFLASH_API dflash_status dflash_kvq_evict(const dflash_kvq_cache *cache, int32_t
                                           int32_t *kept_dev, int32_t *new_lens_dev,
                                           dflash_stream_t stream);
 
-/* Waits for `stream`, then returns and clears the cache's status word. */
+/* Waits for `stream`, then returns and clears the cache's status word (not for use
+ * inside a stream capture). */
 DFLASH_API dflash_status dflash_kvq_check(const dflash_kvq_cache *cache, dflash_stream_t stream);
 
 /* ---- temperature-1 drafting and acceptance ------------------------------------
