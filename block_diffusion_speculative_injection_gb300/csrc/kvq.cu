@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
     const uint32_t bg = __ballot_sync(0xffffffffu, i < j1 && k > T);
     const uint32_t be = __ballot_sync(0xffffffffu, i < j1 && k == T);
     const uint32_t a = above + __popc(bg & lt), e = equal + __popc(be & lt);
-    if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < ties)) {
-      const uint32_t at = a + min(e, ties);
+    // (at < K unless the scores changed meanwhile: then no count is to be relied on)
+    const uint32_t at = a + min(e, ties);
+    if ((((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < ties)) && at < (uint32_t)K) {
       kept[at] = i;
       dsc[at] = key_score(k);
     }

@@ -570,7 +570,8 @@ DFLASH_API dflash_status dflash_kvq_score(
  * mapped (dflash_kv_pool_reserve of another slot; the source's pages can be
  * released after).  Blocks take their exponents anew.  Sources are only read.  An
  * entry with dst_ids[b] == src_ids[b] is refused on the device
- * (DFLASH_E_DEVICE_CHECK, entry skipped); rows for unmapped destination pages are
+ * (DFLASH_E_DEVICE_CHECK, entry skipped); a destination that is another entry's source
+ * or destination gives unspecified rows in both; rows for unmapped destination pages are
  * dropped, source slots on unmapped pages read as zero (DFLASH_E_CAPACITY).
  *   score_dev    [n_seqs][n_kv_heads][pages_per_seq * 128]: row src_ids[b] is read,
  *                row dst_ids[b] gets the kept slots' scores, then zeros

@@ -684,3 +684,22 @@ def test_evict_long_lists(n, kind):
         np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), want)
         assert torch.equal(score[1, 0, :budget], src[torch.from_numpy(want).cuda()])
         assert (score[1, 0, budget:] == 0).all()
+
+
+def test_evict_into_another_entry_s_source_stays_in_bounds():
+    """Scores that change while they are searched leave the choice open, not where it
+    is written: nothing beside the lists changes, and no slot is out of range."""
+    n, budget, window = 20000, 3000, 100
+    c = Cache(1, 3, (n + PAGE - 1) // PAGE, spare=0)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    score = torch.rand(3, 1, c.pages * PAGE, device="cuda", generator=g)
+    room = torch.full((4, 1, budget), -7, dtype=torch.int32, device="cuda")
+    nl = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for mk in (n, 1):
+        room[1:3] = 0
+        capi().dflash_kvq_evict(c.h, 2, i32([0, 1]), i32([1, 2]), i32([n, n]), mk, budget, window,
+                                score, room[1:3], nl)
+        assert (room[0] == -7).all() and (room[3] == -7).all()
+        assert (room[1:3] >= 0).all() and (room[1:3] < n).all()
+        assert nl.tolist() == [budget, budget]
+    capi().dflash_kvq_check(c.h)
