@@ -665,7 +665,8 @@ dflash_status dflash_kvq_append(const dflash_kvq_cache* cache, int32_t batch, in
                                 dflash_stream_t stream) {
   if (!kvq_cache_ok(cache) || batch < 1 || rows < 1 || !start || !k || !v || !kvq_aligned(k, 16) ||
       !kvq_aligned(v, 16) || !row_stride_ok(k_row_stride, cache->n_kv_heads) ||
-      !row_stride_ok(v_row_stride, cache->n_kv_heads) || rows >= (1 << 30))
+      !row_stride_ok(v_row_stride, cache->n_kv_heads) || rows >= (1 << 30) ||
+      !kvq_ints_aligned({seq_ids, start, counts}))
     return DFLASH_E_INVALID_ARG;
   AppendK p;
   p.n_blk = (rows + 2 * kKvqSub - 2) / kKvqSub;  // blocks that `rows` slots can touch
@@ -694,7 +695,8 @@ dflash_status dflash_kvq_read(const dflash_kvq_cache* cache, int32_t batch, int3
                               const int32_t* seq_ids, const int32_t* start, const int32_t* counts,
                               void* k_out, void* v_out, dflash_stream_t stream) {
   if (!kvq_cache_ok(cache) || batch < 1 || rows < 1 || (!k_out && !v_out) ||
-      !kvq_aligned(k_out, 16) || !kvq_aligned(v_out, 16))
+      !kvq_aligned(k_out, 16) || !kvq_aligned(v_out, 16) ||
+      !kvq_ints_aligned({seq_ids, start, counts}))
     return DFLASH_E_INVALID_ARG;
   if ((int64_t)batch * rows >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
   const int64_t threads = (int64_t)batch * rows * cache->n_kv_heads * 16;
@@ -724,7 +726,8 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
   if (!kvq_cache_ok(cache) || batch < 1 || batch > 65535 || !src_ids || !dst_ids || !kv_lens ||
       max_keys < 1 || max_keys > (1 << 29) || budget < 1 ||
       budget > cache->pages_per_seq * kPageSlots || window < 0 || window > budget || !score ||
-      !kept || !new_lens || !kvq_aligned(score, 4) || !kvq_aligned(kept, 4))
+      !kept || !new_lens || !kvq_aligned(score, 4) ||
+      !kvq_ints_aligned({src_ids, dst_ids, kv_lens, kept, new_lens}))
     return DFLASH_E_INVALID_ARG;
   const int64_t warps = (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub) * 2;
   if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;

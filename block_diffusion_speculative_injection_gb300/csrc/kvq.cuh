@@ -4,6 +4,8 @@
 
 #include <cuda_fp8.h>
 
+#include <initializer_list>
+
 #include "internal.cuh"
 
 namespace dflash {
@@ -110,6 +112,11 @@ KvqK kvq_device_view(const dflash_kvq_cache* c);
 int kvq_sms();  // SM count of the current device (cached per device)
 inline bool kvq_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+inline bool kvq_ints_aligned(std::initializer_list<const int32_t*> ptrs) {
+  for (const int32_t* p : ptrs)
+    if (!kvq_aligned(p, 4)) return false;
+  return true;
 }
 
 }  // namespace dflash

@@ -1386,7 +1386,7 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   if (!kvq_cache_ok(cache) || !kvq_attn_shape_ok(batch, H, cache->n_kv_heads, block, max_keys) ||
       mask < DFLASH_MASK_NONE || mask > DFLASH_MASK_TREE || !kv_lens || !q || !kvq_aligned(q, 16) ||
       q_row_stride < (int64_t)H * kKvqHd || q_row_stride % 8 != 0 ||
-      q_row_stride >= ((int64_t)1 << 31))
+      q_row_stride >= ((int64_t)1 << 31) || !kvq_ints_aligned({seq_ids, kv_lens, q_lens}))
     return DFLASH_E_INVALID_ARG;
   if (mask == DFLASH_MASK_TREE && (!anc || !kvq_aligned(anc, 8) || anc_words < 1))
     return DFLASH_E_INVALID_ARG;

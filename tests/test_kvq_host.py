@@ -164,3 +164,15 @@ def test_wrappers_check_tensors():
     for bad in (x[:, :, 2:4].float(), x[:, :2, :2], x[:, :, ::3], x[..., :2, :64]):
         with pytest.raises(capi.DFlashError):
             capi._kvq_rows(bad, "k", 2, bad.shape[1], 2)
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("append", {"start": A + 2}), ("append", {"k": A, "cnt": A + 1}), ("append", {"k": A, "ids": A + 2}),
+    ("read", {"ko": A, "start": A + 2}), ("read", {"ko": A, "cnt": A + 3}), ("read", {"ko": A, "ids": A + 1}),
+    ("attention", {"lens": A + 2}), ("attention", {"q": A, "cnt": A + 2}), ("attention", {"q": A, "ids": A + 2}),
+    ("score", {"lens": A + 1}), ("score", {"q": A, "cnt": A + 1}), ("score", {"q": A, "ids": A + 1}),
+    ("evict", {"src": A + 2}), ("evict", {"dst": A + 2}), ("evict", {"lens": A + 2}),
+    ("evict", {"kept": A + 2}), ("evict", {"nl": A + 2}),
+])
+def test_misaligned_integer_arrays_are_refused(lib, name, kw):
+    assert dict(calls(lib, cache(), **kw))[name] == 1
