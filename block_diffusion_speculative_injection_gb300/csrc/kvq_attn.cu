@@ -1039,6 +1039,7 @@ constexpr uint32_t kSOffQs = kSOffRow + 3 * 64 * 8;      // [64] float, conversi
 constexpr uint32_t kSOffSlot = kSOffQs + 64 * 4;         // [4][128] float2: K's scale, the sum
 constexpr uint32_t kSOffBar = kSOffSlot + kSGroup * kTile * 8;
 constexpr int kScoreSmem = (int)kSOffBar + 256 + 1024;
+constexpr uint32_t kSOffMute = kSOffBar + 192;  // [3][64] bits: rows with lse -inf
 constexpr uint32_t kScoreTmem = 256;
 
 __global__ void __launch_bounds__(kAttnQThreads, 2)
@@ -1201,6 +1202,10 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         }
         reinterpret_cast<float2*>(sm + kSOffRow)[conv % 3 * 64 + row] = v;
       }
+      // (such a row adds nothing, and its weights are 0 * NaN where K or it holds a NaN)
+      const uint32_t mute = __ballot_sync(0xffffffffu, live && lse == -INFINITY) & 0xffffu;
+      if (lane == 0)
+        reinterpret_cast<uint16_t*>(sm + kSOffMute)[conv % 3 * 4 + warp] = (uint16_t)mute;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -1290,6 +1295,12 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         const int mask_from = p.mask == DFLASH_MASK_NONE     ? 0x7fffffff
                               : p.mask == DFLASH_MASK_CAUSAL ? ctx + j0 + 1
                                                              : ctx;
+        // rows that count; where all do, or those that do not are behind the last row
+        // (whose weights are zero, and which see a NaN of K only beside a row that counts),
+        // no bit is looked at
+        const uint64_t mute = *reinterpret_cast<const uint64_t*>(sm + kSOffMute + rbuf * 8);
+        const int n_rows = min(p.pos, r - j0) * p.G;
+        const uint64_t count = mute == 0 ? ~0ull : ~mute & (n_rows < 64 ? (1ull << n_rows) - 1 : ~0ull);
         // two pages at a time: a row's (scale, log2 lse) is read once for both
 #pragma unroll 1
         for (int m = 0; m < members; m += 2) {
@@ -1300,11 +1311,12 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           tc_fence_after();
           const float2 st0 = mine[m * kTile], st1 = mine[m1 * kTile];
           const int k0 = (t_begin + g + m) * kTile + slot, k1 = (t_begin + g + m1) * kTile + slot;
-          const bool masked = (t_begin + g + m1 + 1) * kTile > mask_from;
-          uint64_t vis0 = ~0ull, vis1 = ~0ull;  // rows that see the slots
-          if (masked) {
-            if (k0 >= ctx) vis0 = score_rows_seeing(p, b, k0 - ctx, j0, r);
-            if (k1 >= ctx) vis1 = score_rows_seeing(p, b, k1 - ctx, j0, r);
+          const bool partly = (t_begin + g + m1 + 1) * kTile > mask_from;
+          const bool masked = partly || mute != 0;
+          uint64_t vis0 = count, vis1 = count;  // rows that see the slots
+          if (partly) {
+            if (k0 >= ctx) vis0 &= score_rows_seeing(p, b, k0 - ctx, j0, r);
+            if (k1 >= ctx) vis1 &= score_rows_seeing(p, b, k1 - ctx, j0, r);
           }
           float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
 #pragma unroll 1

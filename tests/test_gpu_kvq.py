@@ -703,3 +703,33 @@ def test_evict_into_another_entry_s_source_stays_in_bounds():
         assert (room[1:3] >= 0).all() and (room[1:3] < n).all()
         assert nl.tolist() == [budget, budget]
     capi().dflash_kvq_check(c.h)
+
+
+@pytest.mark.parametrize("mask", ["none", "causal"])
+def test_score_rows_with_lse_minus_infinity_add_nothing(mask):
+    """Not where the row itself or K holds a NaN either: sequence 0 has one such row, of
+    NaN; all of sequence 1's are, and its K holds a NaN in slot 3."""
+    lens, block, heads, g = [300, 140], 6, 2, 3
+    c, rng = filled(heads, lens, seed=9)
+    k = c.val["k"][1:2, :4].copy()
+    k[0, 3, :, 5] = np.nan
+    c.append([0], k, c.val["v"][1:2, :4], seqs=[1], oracle=False)
+    # (appending restarts the block of 16: its later slots are junk now, NaN among it)
+    q = rng.normal(size=(2, block, heads * g, HD))
+    t, qe = bf16(q)
+    lse = np.full((2, block, heads * g), -np.inf)
+    vis = ok.visible(mask, 300, block)
+    lse[0] = ok.attend(qe[0], c.val["k"][0, :300], c.val["v"][0, :300], vis)[1]
+    lse[0, 2] = -np.inf
+    t[0, 2] = float("nan")
+    old = torch.from_numpy(rng.random(size=(2, heads, c.pages * PAGE))).float().cuda()
+    out = torch.zeros_like(old)
+    capi().dflash_kvq_score(c.h, 2, heads * g, block, {"none": 0, "causal": 1}[mask], None, i32(lens),
+                            None, None, 300, t, torch.from_numpy(lse).float().cuda(), 0.5, old, out)
+    assert torch.equal(out[1, :, :140], 0.5 * old[1, :, :140])
+    w = ok.score(qe[0], c.val["k"][0, :300], vis, np.float32(lse[0]).astype(np.float64))
+    top = np.abs(qe[0]).max() * np.abs(c.val["k"][0, :300]).sum(axis=-1).max() / np.sqrt(HD)
+    want = 0.5 * old[0, :, :300].double().cpu().numpy() + w
+    tol = 2.0 ** -22 + 2.0 ** -20 * want + (2.0 ** -17 * top + 2.0 ** -20) * w
+    assert (np.abs(out[0, :, :300].double().cpu().numpy() - want) <= tol).all()
+    capi().dflash_kvq_check(c.h)
