@@ -1012,7 +1012,7 @@ static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t
   return (int)best;
 }
 
-static int64_t kvq_q_tiles(int block, int G) { return (block + 64 / G - 1) / (64 / G); }
+static int64_t kvq_q_tiles(int block, int G) { return ((int64_t)block + 64 / G - 1) / (64 / G); }
 
 // ---------------------------------------------------------------------------
 // Accumulated weights.  The same product the other way round: S^T = K Q^T, a page of
@@ -1419,7 +1419,7 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   p->G = H / cache->n_kv_heads;
   p->pos = 64 / p->G;
   p->two = 2;
-  p->q_tiles = (block + p->pos - 1) / p->pos;
+  p->q_tiles = (int)kvq_q_tiles(block, p->G);
   p->g_inv = (65536 + p->G - 1) / p->G;
   p->q = static_cast<const bf16*>(q);
   p->q_stride = q_row_stride;

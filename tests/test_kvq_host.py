@@ -176,3 +176,9 @@ def test_wrappers_check_tensors():
 ])
 def test_misaligned_integer_arrays_are_refused(lib, name, kw):
     assert dict(calls(lib, cache(), **kw))[name] == 1
+
+
+def test_workspace_of_the_longest_blocks(lib):
+    """Far more CTAs than SMs: nothing is gained by splitting."""
+    for block in (2 ** 31 - 1, 2 ** 31 - 64):
+        assert capi.dflash_kvq_attention_workspace(1, 1, 1, block, 4096) == 0
