@@ -66,35 +66,6 @@ __device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, in
   return kvq_entry_check(p, e, key_end);
 }
 
-// does row j of a sequence (n slots, r rows) see slot k < n?
-__device__ __forceinline__ bool kvq_sees(const KvqAttnK& p, int k, int n, int r, int j,
-                                         const uint64_t* anc_row) {
-  const int i = k - (n - r);
-  if (p.mask == DFLASH_MASK_NONE || i < 0) return true;
-  if (p.mask == DFLASH_MASK_CAUSAL) return i <= j;
-  return (i >> 6) < p.anc_words && ((anc_row[i >> 6] >> (i & 63)) & 1ull);
-}
-
-// four codes of a lane as floats, without the exponent
-__device__ __forceinline__ float4 decode4(uint32_t w) {
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  return make_float4(x.x, x.y, y.x, y.y);
-}
-__device__ __forceinline__ float4 load_q4(const bf16* q) {
-  const uint2 w = *reinterpret_cast<const uint2*>(q);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-  float d = a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-  return d;
-}
-
 // ---------------------------------------------------------------------------
 // Attention on the 5th-generation tensor cores, both products in 8 bits.
 //
@@ -143,9 +114,8 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 // thread and tile take about 630 cycles of a scheduler (256 of them the exponentials)
 // and what is around them as much again, 1400 cycles a tile of an SM, which is about the
 // memory's rate too; a CTA's set-up, first loads and output add some 10,000 cycles that
-// the other CTA of the SM hides in part.  Leaving the
-// MMAs out of a copy made for timing changed nothing.  Tried and slower: eight
-// softmax warps of 32 slots a thread (16 rows at a batch of 8: 93 us against 70), the
+// the other CTA of the SM hides in part.  Leaving the MMAs out of a copy made for
+// timing changed nothing.  Tried and slower: eight softmax warps of 32 slots a thread (16 rows at a batch of 8: 93 us against 70), the
 // tile's maximum looked for only after a weight overflowed (88), S read from tensor memory
 // twice instead of held in registers (95), shares of the longest sequence instead of
 // each sequence's own (32 ragged sequences: 70 against 55).
@@ -188,8 +158,6 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
 }
 
-// Slots of a split, and whose rows of a q tile they are.  A sequence's slots are
-// shared out over the launch's splits in whole pages; `used` splits are not empty.
 // Four weights z <= 16 of consecutive slots, the first a multiple of 4 in its block,
 // as four codes of p1 and four of p2, z = (p1 + p2 / 16) / 16.  z in fp16 carries 11
 // significand bits; an fp16 below 2 is an e4m3 code (times 2^8) with three more
@@ -244,6 +212,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // block position (within the CTA's) of one of its 64 rows
 __device__ __forceinline__ int row_pos(const KvqAttnK& p, int row) { return row * p.g_inv >> 16; }
 
+// Slots of a split: a sequence's are shared out over the launch's splits in whole pages;
+// `used` splits are not empty.
 struct KvqSpan {
   int key_end, per_split, used;
 };
@@ -303,66 +273,66 @@ __device__ __forceinline__ void load_q(const KvqAttnK& p, int b, int kvh, int j0
 __device__ __forceinline__ void convert_q(uint4* q_raw, int warp, int lane, uint8_t* dst,
                                           float* q_scales) {
   const int t16 = lane & 15, h = lane >> 4;
-        // largest magnitude of each row, on bf16 pairs (as integers, NaN above all)
-        uint32_t top[8];
-  #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          constexpr uint32_t abs2 = 0x7fff7fffu;
-          top[i] = __vimax3_u16x2(q_raw[i].x & abs2, q_raw[i].y & abs2, q_raw[i].z & abs2);
-          top[i] = __vmaxu2(top[i], q_raw[i].w & abs2);
-        }
-  #pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-  #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
-  #pragma unroll 1
-        for (int i = 0; i < 8; i += 2) {  // two of the lane's eight rows, for overlap
-          uint4 now[2];
-          uint32_t bits[2], w1[2][4], w2[2][4];
-          int e[2];
-  #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            now[r] = q_raw[r];
-            bits[r] = max(top[r] & 0xffffu, top[r] >> 16) << 16;
-            // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
-            // magnitude above 448 * 2^118 becomes NaN
-            e[r] = max(-80, (int)(bits[r] >> 23) - 127 - ((bits[r] & 0x7fffff) > 0x600000 ? 7 : 8));
-          }
-  #pragma unroll
-          for (int k = 0; k < 6; ++k) {  // keeps the loop rolled
-            q_raw[k] = q_raw[k + 2];
-            top[k] = top[k + 2];
-          }
-  #pragma unroll
-          for (int k = 0; k < 4; ++k)
-  #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float sc = pow2i(-min(e[r], 118) - 8);
-              const uint32_t q2 = k == 0 ? now[r].x : k == 1 ? now[r].y : k == 2 ? now[r].z : now[r].w;
-              const __half2 y = __floats2half2_rn(__uint_as_float(q2 << 16) * sc,
-                                                  __uint_as_float(q2 & 0xffff0000u) * sc);
-              const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
-              const uint32_t d = u & 0xff80ff80u;
-              const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
-              const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
-              w1[r][k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
-              w2[r][k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
-            }
-  #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int qr = warp * 16 + 2 * (i + r) + h;
-            const uint32_t off =
-                (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
-            *reinterpret_cast<uint2*>(dst + off) = make_uint2(__byte_perm(w1[r][0], w1[r][1], 0x7531),
-                                                             __byte_perm(w1[r][2], w1[r][3], 0x7531));
-            *reinterpret_cast<uint2*>(dst + kQPart + off) = make_uint2(
-                __byte_perm(w2[r][0], w2[r][1], 0x7531), __byte_perm(w2[r][2], w2[r][3], 0x7531));
-            // a bad row: minus its scale
-            if (t16 == 0)
-              q_scales[2 * (i + r) + h] = e[r] > 118 ? -kScaleLog2 : pow2i(e[r]) * kScaleLog2;
-          }
-        }
+  // largest magnitude of each row, on bf16 pairs (as integers, NaN above all)
+  uint32_t top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    constexpr uint32_t abs2 = 0x7fff7fffu;
+    top[i] = __vimax3_u16x2(q_raw[i].x & abs2, q_raw[i].y & abs2, q_raw[i].z & abs2);
+    top[i] = __vmaxu2(top[i], q_raw[i].w & abs2);
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+#pragma unroll 1
+  for (int i = 0; i < 8; i += 2) {  // two of the lane's eight rows, for overlap
+    uint4 now[2];
+    uint32_t bits[2], w1[2][4], w2[2][4];
+    int e[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      now[r] = q_raw[r];
+      bits[r] = max(top[r] & 0xffffu, top[r] >> 16) << 16;
+      // the smallest e with a <= 448 * 2^e; a row with a NaN, an infinity or a
+      // magnitude above 448 * 2^118 becomes NaN
+      e[r] = max(-80, (int)(bits[r] >> 23) - 127 - ((bits[r] & 0x7fffff) > 0x600000 ? 7 : 8));
+    }
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {  // keeps the loop rolled
+      q_raw[k] = q_raw[k + 2];
+      top[k] = top[k + 2];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float sc = pow2i(-min(e[r], 118) - 8);
+        const uint32_t q2 = k == 0 ? now[r].x : k == 1 ? now[r].y : k == 2 ? now[r].z : now[r].w;
+        const __half2 y = __floats2half2_rn(__uint_as_float(q2 << 16) * sc,
+                                            __uint_as_float(q2 & 0xffff0000u) * sc);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&y) + 0x00400040u;
+        const uint32_t d = u & 0xff80ff80u;
+        const __half2 res = __hsub2(y, *reinterpret_cast<const __half2*>(&d));
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(&res) + 0x00400040u;
+        w1[r][k] = ((u + u) & 0x7fff7fffu) | (u & 0x80008000u);
+        w2[r][k] = ((v + v) & 0x7fff7fffu) | (v & 0x80008000u);
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int qr = warp * 16 + 2 * (i + r) + h;
+      const uint32_t off =
+          (uint32_t)qr * 128 + ((uint32_t)((t16 >> 1) ^ (qr & 7)) << 4) + 8 * (t16 & 1);
+      *reinterpret_cast<uint2*>(dst + off) = make_uint2(__byte_perm(w1[r][0], w1[r][1], 0x7531),
+                                                       __byte_perm(w1[r][2], w1[r][3], 0x7531));
+      *reinterpret_cast<uint2*>(dst + kQPart + off) = make_uint2(
+          __byte_perm(w2[r][0], w2[r][1], 0x7531), __byte_perm(w2[r][2], w2[r][3], 0x7531));
+      // a bad row: minus its scale
+      if (t16 == 0)
+        q_scales[2 * (i + r) + h] = e[r] > 118 ? -kScaleLog2 : pow2i(e[r]) * kScaleLog2;
+    }
+  }
 }
 
 __device__ __forceinline__ float2 mul2(float2 a, float b) {
