@@ -998,7 +998,7 @@ static int64_t kvq_q_tiles(int block, int G) { return ((int64_t)block + 64 / G -
 // page of the group; two CTAs share an SM.
 // Warps 0-3: the rows' conversion (for the next q tile ahead of this one's sums),
 // weights and sums; warp 4: TMA of K; warp 5: MMAs.
-// Measured: 8 sequences of 16 rows x 32 heads over 16,400 slots (144 MB) 47 us, 3.1 TB/s: of
+// Measured: 8 sequences of 16 rows x 32 heads over 16,400 slots (144 MB) 46 us, 3.1 TB/s: of
 // a page's cycles in a CTA about 1050 are the weights (two pages at a time share the
 // rows' scales), the rest waits and the group's set-up and output; two CTAs share an SM.
 // ---------------------------------------------------------------------------
