@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     for (int t = 0; t < n_tiles; ++t) {
       const int tile0 = k_begin + t * kTile;
       const int pg_now = pg;
-      const uint2 ex_now = ex;
+      uint2 ex_now = ex;
       const uint32_t odd8 = (t & 1) * 8, phase = (t >> 1) & 1;
       if (t + 1 < n_tiles) {
         pg = kvq_page_check(p.c, raw_next);
@@ -676,6 +676,12 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       float ck[4], ev[4], mx = -INFINITY;
       if (warp_live) {
         if (masked) {
+          // Blocks from `stop` on may never have been written, and an unmapped page has page
+          // 0's exponents: any byte.  They count as 0, for -inf * 2^e is a NaN where 2^e
+          // leaves fp32's range.
+          const uint32_t written = bits_below((stop - tile0 - 64 * h + kKvqSub - 1) / kKvqSub * 8);
+          ex_now.x &= written;
+          ex_now.y &= written;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint32_t vis = visible32(p, tile0 + 64 * h + 32 * c, stop, ctx, jr, anc);

@@ -454,7 +454,8 @@ DFLASH_API dflash_status dflash_block_attention_noalloc(int32_t batch, int32_t n
  *                 (dflash_kvq_check reads and clears it)
  * All pointers are device memory of the device that is current at the call
  * (any other pointer: DFLASH_E_INVALID_ARG): k8 and v8 16-byte aligned, k_exp
- * and v_exp 8-byte aligned, n_pages * n_kv_heads * 128 < 2^31.
+ * and v_exp 8-byte aligned, n_pages * n_kv_heads * 128 < 2^31. Codes and
+ * exponents of slots that nothing was written to may hold any bytes.
  * The exponent of a block of 16 slots is the smallest e in [-40, 40] with
  * max |x| <= 448 * 2^e over its rows, codes are rounded to nearest even.  A
  * power of two makes scaling exact: a code is off by at most 2^-4 of its value

@@ -1,0 +1,66 @@
+"""Uninitialised memory in the places of the 8-bit cache that no result depends on."""
+import numpy as np
+import pytest
+import torch
+
+from kvq_util import HD, PAGE, Cache, bf16
+from test_gpu_kvq import check_rows, i32, run_attention
+from oracle import kvq as ok
+
+pytestmark = pytest.mark.gpu
+
+
+def capi():
+    from block_diffusion_speculative_injection_gb300 import capi as c
+    return c
+
+
+def fill_exponents(c, junk, seed=0):
+    """Every exponent of the pool, before anything is written: one byte, or all 256."""
+    rng = np.random.default_rng(seed)
+    for x in "kv":
+        t = c.t[x + "e"]
+        e = rng.integers(-128, 128, tuple(t.shape), dtype=np.int8) if junk is None else \
+            np.full(tuple(t.shape), junk, dtype=np.int8)
+        t.copy_(torch.from_numpy(e))
+
+
+@pytest.mark.parametrize("junk", [None, -128, -127, -70, 127])
+@pytest.mark.parametrize("lens,block,mask", [
+    ([1, 16, 17, 129], 1, "none"), ([300, 5, 128, 64], 16, "causal"), ([1600, 33, 240, 700], 3, "none"),
+])
+def test_attention_with_junk_exponents_behind_the_last_slot(junk, lens, block, mask):
+    c = Cache(2, len(lens), 13, seed=3)
+    fill_exponents(c, junk)
+    rng = np.random.default_rng(block)
+    c.append([0] * len(lens), rng.normal(size=(len(lens), max(lens), 2, HD)),
+             rng.normal(size=(len(lens), max(lens), 2, HD)), lens)
+    q = rng.normal(size=(len(lens), block, 8, HD))
+    q[:, block - 1, 3] = 0  # a row of zeros has the smallest scale
+    for ws in (True, False):
+        got, lse, qe = run_attention(c, q, mask, lens, ws=ws)
+        for b, n in enumerate(lens):
+            check_rows(c, qe, got, lse, mask, n, block, b, b)
+    capi().dflash_kvq_check(c.h)
+
+
+@pytest.mark.parametrize("junk", [None, -128, -127, -70, 127])
+def test_attention_with_junk_exponents_of_page_zero(junk):
+    """An unmapped page counts as unseen, whatever page 0 of the pool holds."""
+    c = Cache(1, 1, 3, seed=4, spare=2)
+    tab = np.array([[1, 2, 3]], dtype=np.int32)  # page 0 belongs to nobody
+    c.h.tensors[4].copy_(torch.from_numpy(tab))
+    c.table[:] = tab
+    fill_exponents(c, junk)
+    rng = np.random.default_rng(8)
+    c.append([0], rng.normal(size=(1, 384, 1, HD)), rng.normal(size=(1, 384, 1, HD)))
+    c.h.tensors[4][0, 1] = -1
+    q = rng.normal(size=(1, 3, 4, HD))
+    q[0, 1, 2] = 0
+    vis = np.ones((3, 384), dtype=bool)
+    vis[:, 128:256] = False
+    for ws in (True, False):
+        got, lse, qe = run_attention(c, q, "none", [384], ws=ws)
+        check_rows(c, qe, got, lse, "none", 384, 3, 0, 0, ok_mask=vis)
+        with pytest.raises(capi().DFlashError):
+            capi().dflash_kvq_check(c.h)
