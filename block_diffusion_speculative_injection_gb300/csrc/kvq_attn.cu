@@ -1167,6 +1167,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       if (live)
         lse = p.lse[((long long)b * p.block + j) * p.H + kvh * p.G + row - pos * p.G];
       if (p.q_tiles > 1) load_q(p, b, kvh, j0, warp, lane, q_raw);
+      // Rows behind the sequence's last one hold anything: as zeros, for an element that
+      // becomes the code of NaN would be 0 * NaN in every slot's sum.
+      if (j0 + p.pos > r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j0 + row_pos(p, warp * 16 + 2 * i + (lane >> 4)) >= r) q_raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
       convert_q(q_raw, warp, lane, sm + kSOffQ + buf * 2 * kQPart, q_scales);
       __syncwarp();
       if (lane < 16) {
@@ -1272,8 +1279,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
                               : p.mask == DFLASH_MASK_CAUSAL ? ctx + j0 + 1
                                                              : ctx;
         // rows that count; where all do, or those that do not are behind the last row
-        // (whose weights are zero, and which see a NaN of K only beside a row that counts),
-        // no bit is looked at
+        // (zeros, so their weights are zero too, and they see a NaN of K only beside a row that
+        // counts), no bit is looked at
         const uint64_t mute = *reinterpret_cast<const uint64_t*>(sm + kSOffMute + rbuf * 8);
         const int n_rows = min(p.pos, r - j0) * p.G;
         const uint64_t count = mute == 0 ? ~0ull : ~mute & (n_rows < 64 ? (1ull << n_rows) - 1 : ~0ull);

@@ -64,3 +64,39 @@ def test_attention_with_junk_exponents_of_page_zero(junk):
         check_rows(c, qe, got, lse, "none", 384, 3, 0, 0, ok_mask=vis)
         with pytest.raises(capi().DFlashError):
             capi().dflash_kvq_check(c.h)
+
+
+@pytest.mark.parametrize("mask", ["none", "causal", "tree"])
+@pytest.mark.parametrize("g,block,q_lens", [(4, 16, [5, 16, 0]), (8, 40, [33, 1, 20]), (5, 7, [6, 2, 7])])
+def test_score_with_junk_rows_past_q_lens(mask, g, block, q_lens):
+    """Whatever bits the rows behind a sequence's last one hold, the scores are the same."""
+    lens, heads = [300, 140, 90], 2
+    c = Cache(heads, 3, 3, seed=6)
+    rng = np.random.default_rng(g)
+    c.append([0] * 3, rng.normal(size=(3, 300, heads, HD)), rng.normal(size=(3, 300, heads, HD)), lens)
+    H = heads * g
+    t, _ = bf16(rng.normal(size=(3, block, H, HD)))
+    lse = torch.full((3, block, H), 8.0, device="cuda")
+    anc = torch.full((3, block, 1), -1, dtype=torch.int64, device="cuda") if mask == "tree" else None
+    code = {"none": 0, "causal": 1, "tree": 2}[mask]
+
+    def call():
+        out = torch.zeros(3, heads, c.pages * PAGE, device="cuda")
+        capi().dflash_kvq_score(c.h, 3, H, block, code, None, i32(lens), i32(q_lens), anc, 300, t, lse,
+                                1.0, None, out)
+        capi().dflash_kvq_check(c.h)
+        return out
+    for b, r in enumerate(q_lens):
+        t[b, r:] = 0
+    want = call()
+    assert torch.isfinite(want).all() and (want[0, :, :300] > 0).all()
+    junk = torch.from_numpy(rng.integers(-2 ** 15, 2 ** 15, (block, H, HD)).astype(np.int16)).cuda()
+    junk = junk.view(torch.bfloat16)
+    big = torch.full_like(junk, 1.875 * 2.0 ** 126)
+    lone = torch.zeros_like(big)
+    lone[..., 77] = 1.875 * 2.0 ** 126
+    for rows in (junk, big, lone, torch.full_like(big, float("nan")), torch.full_like(big, float("inf"))):
+        for b, r in enumerate(q_lens):
+            t[b, r:] = rows[r:]
+            lse[b, r:] = float("nan")
+        assert torch.equal(call(), want)
