@@ -499,7 +499,9 @@ __global__ void __launch_bounds__(128, 10) kvq_evict_move_kernel(const EvictK p)
   int8_t* const ex = kv ? p.c.ex[1] : p.c.ex[0];
   // its row in the pool (pages * heads * 128 < 2^31) and its exponent
   int at = -1, e_src = 0;
-  if (lane < n_live) {
+  // (an entry of the list that the selection left open, because scores changed under it, is
+  // whatever the caller's memory held: a negative one is no slot, and reads as zero)
+  if (lane < n_live && from >= 0) {
     const int page = kvq_page(p.c, src, from / kPageSlots);
     if (page >= 0) {
       at = (int)kvq_ph(p.c, page, head) * kPageSlots + from % kPageSlots;

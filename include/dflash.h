@@ -572,7 +572,8 @@ DFLASH_API dflash_status dflash_kvq_score(
  * released after).  Blocks take their exponents anew.  Sources are only read.  An
  * entry with dst_ids[b] == src_ids[b] is refused on the device
  * (DFLASH_E_DEVICE_CHECK, entry skipped); a destination that is another entry's source
- * or destination gives unspecified rows in both; rows for unmapped destination pages are
+ * or destination gives unspecified rows, scores and entries of kept in both (entries may stay
+ * as they were); rows for unmapped destination pages are
  * dropped, source slots on unmapped pages read as zero (DFLASH_E_CAPACITY).
  *   score_dev    [n_seqs][n_kv_heads][pages_per_seq * 128]: row src_ids[b] is read,
  *                row dst_ids[b] gets the kept slots' scores, then zeros

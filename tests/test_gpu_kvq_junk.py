@@ -100,3 +100,35 @@ def test_score_with_junk_rows_past_q_lens(mask, g, block, q_lens):
             t[b, r:] = rows[r:]
             lse[b, r:] = float("nan")
         assert torch.equal(call(), want)
+
+
+def test_evict_with_junk_in_the_list_of_kept_slots():
+    """The call whose choice is open (a destination that is another entry's source) may leave
+    entries of `kept` unwritten: negative ones must not be read as slots.  The rows that come out
+    are open too, but come from the pool's (ones), whose blocks move under their readers, or are
+    zero; exponents are the format's."""
+    n, budget, window = 20000, 3000, 100
+    pages = (n + PAGE - 1) // PAGE
+    guard = 8  # exponents of another page lie before the pool's
+    c = Cache(1, 3, pages, spare=0)
+    room = torch.full((c.t["ke"].shape[0] + guard, 1, 8), 127, dtype=torch.int8, device="cuda")
+    room[guard:] = -8
+    one = torch.full_like(c.t["k8"], 0x78)  # 256 * 2^-8
+    tab = np.arange(3 * pages, dtype=np.int32).reshape(3, pages)
+    h = capi().KvqCache(one, one.clone(), room[guard:], room[guard:].clone(), torch.from_numpy(tab).cuda(),
+                        c.status)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    nl = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for junk in (-1, -127, -128, -2 ** 31):
+        for mk in (n, 1):
+            score = torch.rand(3, 1, pages * PAGE, device="cuda", generator=g)
+            kept = torch.full((2, 1, budget), junk, dtype=torch.int32, device="cuda")
+            capi().dflash_kvq_evict(h, 2, i32([0, 1]), i32([1, 2]), i32([n, n]), mk, budget, window,
+                                    score, kept, nl)
+            assert nl.tolist() == [budget, budget]
+            assert ((kept == junk) | ((kept >= 0) & (kept < n))).all()
+            out = torch.empty(2, budget, 1, HD, dtype=torch.bfloat16, device="cuda")
+            capi().dflash_kvq_read(h, 2, budget, i32([1, 2]), None, None, out, None)
+            assert ((out >= 0) & (out <= 1)).all()
+    assert (room[:guard] == 127).all() and (room[guard:] >= -40).all() and (room[guard:] <= 40).all()
+    capi().dflash_kvq_check(c.h)
