@@ -294,7 +294,6 @@ __global__ void __launch_bounds__(kSelThreads) kvq_evict_select_kernel(const Evi
   const int w0 = n <= p.budget ? 0 : n - p.window;  // slots from here on are kept
   const int K = m - (n - w0);                       // kept slots before w0
   const int all = C * kSelThreads, gid = rank * kSelThreads + tid;
-  if (head == 0 && gid == 0) p.new_lens[b] = m;
   // what needs no selection: the window, and the ends of the lists
   auto rest = [&]() {
     for (int i = w0 + gid; i < n; i += all) {
@@ -488,6 +487,9 @@ __global__ void __launch_bounds__(128, 10) kvq_evict_move_kernel(const EvictK p)
   int src, dst, n;
   if (!evict_entry(p, b, src, dst, n)) return;
   const int m = min(n, p.budget);
+  // Not earlier: new_lens may be kv_lens, which the selection reads everywhere.  Here m is
+  // the same from the old length and from the new one.
+  if (blk == 0 && head == 0 && kv == 0 && lane == 0) p.new_lens[b] = m;
   if (d0 >= m) return;
   const int n_live = min(kKvqSub, m - d0);
   const int dpage = kvq_page(p.c, dst, d0 / kPageSlots);
@@ -650,6 +652,16 @@ KvqK kvq_device_view(const dflash_kvq_cache* c) {
   return k;
 }
 
+// n 32-bit words from p on
+struct KvqRange {
+  const void* p;
+  int64_t n;
+};
+static bool kvq_overlap(const KvqRange& a, const KvqRange& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y ? y - x < (uint64_t)a.n * 4 : x - y < (uint64_t)b.n * 4;
+}
+
 static bool row_stride_ok(int64_t stride, int heads) {
   return stride >= (int64_t)heads * kKvqHd && stride % 8 == 0 && stride < ((int64_t)1 << 31);
 }
@@ -733,6 +745,23 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
     return DFLASH_E_INVALID_ARG;
   const int64_t warps = (int64_t)batch * cache->n_kv_heads * ((budget + kKvqSub - 1) / kKvqSub) * 2;
   if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
+  // What is written must not be what other CTAs still read; only the lengths may be updated in
+  // place (the move kernel writes them).
+  const int64_t rows = (int64_t)cache->n_seqs * cache->n_kv_heads;
+  const int64_t cap = (int64_t)cache->pages_per_seq * kPageSlots;
+  const KvqRange in[] = {{kv_lens, batch},
+                         {src_ids, batch},
+                         {dst_ids, batch},
+                         {cache->page_table_dev, (int64_t)cache->n_seqs * cache->pages_per_seq}};
+  const KvqRange out[] = {{new_lens, batch},
+                          {kept, (int64_t)batch * cache->n_kv_heads * budget},
+                          {score, rows > (INT64_MAX >> 3) / cap ? INT64_MAX >> 3 : rows * cap}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = new_lens == kv_lens && i == 0 ? 1 : 0; j < 4; ++j)
+      if (kvq_overlap(out[i], in[j])) return DFLASH_E_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (kvq_overlap(out[i], out[j])) return DFLASH_E_INVALID_ARG;
+  }
   const void* const ptrs[] = {src_ids, dst_ids, kv_lens, score, kept, new_lens};
   DF_TRY(kvq_cache_ptrs_ok(cache));
   DF_TRY(kvq_ptrs_ok(ptrs, 6));

@@ -579,7 +579,10 @@ DFLASH_API dflash_status dflash_kvq_score(
  *                row dst_ids[b] gets the kept slots' scores, then zeros
  *   kept_dev     [batch][n_kv_heads][budget] int32 out: source slot of each kept
  *                row, -1 past min(n, budget)
- *   new_lens_dev [batch] int32 out: min(n, budget)
+ *   new_lens_dev [batch] int32 out: min(n, budget); may be kv_lens_dev, whose lengths are
+ *                then updated in place
+ * Apart from that the arrays written must not overlap one another, the ids, the lengths or
+ * the page table (DFLASH_E_INVALID_ARG).
  *   max_keys     host bound on the lengths, for planning only (1..2^29)
  * budget 1..pages_per_seq * 128, window 0..budget. */
 DFLASH_API dflash_status dflash_kvq_evict(const dflash_kvq_cache *cache, int32_t batch,

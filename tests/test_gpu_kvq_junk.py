@@ -132,3 +132,35 @@ def test_evict_with_junk_in_the_list_of_kept_slots():
             assert ((out >= 0) & (out <= 1)).all()
     assert (room[:guard] == 127).all() and (room[guard:] >= -40).all() and (room[guard:] <= 40).all()
     capi().dflash_kvq_check(c.h)
+
+
+@pytest.mark.parametrize("heads,lens,budget,window", [(3, [9000, 700, 40, 0], 256, 16), (1, [40000], 300, 7)])
+def test_evict_updates_lengths_in_place(heads, lens, budget, window):
+    """new_lens may be kv_lens: the same slots, rows and scores as with an array of its own."""
+    B = len(lens)
+    pages = (max(lens) + PAGE - 1) // PAGE
+    rng = np.random.default_rng(budget)
+    scores = rng.random((2 * B, heads, pages * PAGE)).astype(np.float32)
+    runs = []
+    for in_place in (False, True, True, True):
+        c = Cache(heads, 2 * B, pages, seed=11, spare=0)
+        for x in "kv":
+            c.t[x + "e"].zero_()
+        torch.manual_seed(0)
+        c.t["k8"].copy_(torch.randint(0, 0x78, tuple(c.t["k8"].shape), dtype=torch.uint8, device="cuda"))
+        c.t["v8"].copy_(torch.randint(0, 0x78, tuple(c.t["v8"].shape), dtype=torch.uint8, device="cuda"))
+        score, n = torch.from_numpy(scores).cuda(), i32(lens)
+        new = n if in_place else torch.zeros_like(n)
+        kept = torch.zeros(B, heads, budget, dtype=torch.int32, device="cuda")
+        capi().dflash_kvq_evict(c.h, B, i32(list(range(B))), i32(list(range(B, 2 * B))), n, max(lens),
+                                budget, window, score, kept, new)
+        capi().dflash_kvq_check(c.h)
+        assert new.tolist() == [min(x, budget) for x in lens]
+        runs.append((kept, score, c.t["k8"], c.t["v8"], c.t["ke"], c.t["ve"]))
+    for b, x in enumerate(lens):
+        for h in range(heads):
+            pick = ok.evict_pick(scores[b, h], x, budget, window)
+            assert runs[0][0][b, h, :len(pick)].tolist() == pick
+    for run in runs[1:]:
+        for a, z in zip(run, runs[0]):
+            assert torch.equal(a, z)
