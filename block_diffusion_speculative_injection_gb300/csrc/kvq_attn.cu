@@ -1032,14 +1032,15 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   if (warp < 4 && p.q_tiles == 1) load_q(p, b, kvh, 0, warp, lane, q_raw);
 
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kSOffBar);
-  uint64_t* const q_full = bars;
-  uint64_t* const k_full = bars + 1;
+  uint64_t* const q_full = bars;  // one for each Q buffer
+  uint64_t* const k_full = bars + 2;
   uint64_t* const k_empty = k_full + kSGroup;
   uint64_t* const d_full = k_empty + kSGroup;
   uint64_t* const d_free = d_full + kSGroup;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(d_free + kSGroup);
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 4);
+    mbar_init(&q_full[0], 4);
+    mbar_init(&q_full[1], 4);
     for (int i = 0; i < kSGroup; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -1118,7 +1119,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         // (a group no row sees still passes its pages through, with no q tile)
         const bool any = qt < q_tiles, last = qt + 1 >= q_tiles;
         if (any && (p.q_tiles > 1 || conv == 0)) {
-          ok = __all_sync(0xffffffffu, warp_wait(q_full, conv & 1, status));
+          ok = __all_sync(0xffffffffu, warp_wait(&q_full[conv & 1], (conv >> 1) & 1, status));
           ++conv;
         }
         const int buf = p.q_tiles > 1 ? (conv - 1) & 1 : 0;
@@ -1191,7 +1192,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         reinterpret_cast<uint16_t*>(sm + kSOffMute)[conv % 3 * 4 + warp] = (uint16_t)mute;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(&q_full[buf]);
       ++conv;
     };
     // the thread's slot of each page of the group: K's scale and the sum so far
@@ -1226,13 +1227,14 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     // conversions run one q tile ahead: the next one is tile cq, for group cg
     int cg = 0, cq = q_first(t_begin);
     bool more = cq < q_tiles;
-    // waits, once, for conversion c by all four warps (c in order: a phase's parity
-    // says nothing any more once the next one has completed)
+    // waits, once, for conversion c by all four warps (c in order).  Each buffer has a barrier
+    // of its own, whose next phase begins only after this warp and the MMAs have used the
+    // buffer: a phase's parity says nothing any more once the next one has completed.
     int known = 0;
     auto converted = [&](int c) -> bool {
       if (known > c) return true;
       known = c + 1;
-      return __all_sync(0xffffffffu, warp_wait(q_full, c & 1, status));
+      return __all_sync(0xffffffffu, warp_wait(&q_full[c & 1], (c >> 1) & 1, status));
     };
     read_pages(0);
     read_group(0);
