@@ -571,6 +571,8 @@ def dflash_kvq_attention(cache: KvqCache, batch, n_heads, block, mask, seq_ids, 
     bits, words = _kvq_anc(anc, mask, batch, block)
     ws, nbytes = None, 0
     if workspace is not None:
+        if not workspace.is_contiguous():  # its elements would not be all of its address range
+            _kvq_refuse("workspace: need a contiguous tensor")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _kvq_check(load().dflash_kvq_attention(
         cache.ref, batch, n_heads, block, mask, _kvq_dense(seq_ids, "seq_ids", "i32", one),

@@ -51,3 +51,31 @@ def test_distinct_arrays_and_lengths_in_place_pass(lib):
 ])
 def test_evict_refuses_overlaps(lib, kw):
     assert evict(lib, **kw) == 1
+
+
+def test_workspace_has_to_be_contiguous(monkeypatch):
+    """A strided or expanded view is refused before the library sees its address."""
+    calls = []
+
+    class Lib:
+        def dflash_kvq_attention(self, *args):
+            calls.append(args)
+            return 0
+    monkeypatch.setattr(capi, "load", Lib)
+    k8 = torch.zeros(4, 2, 128, 128, dtype=torch.uint8)
+    e = torch.zeros(4, 2, 8, dtype=torch.int8)
+    c = capi.KvqCache(k8, k8.clone(), e, e.clone(), torch.zeros(1, 4, dtype=torch.int32),
+                      torch.zeros(1, dtype=torch.int32))
+    q = torch.zeros(1, 3, 4, 128, dtype=torch.bfloat16)
+    lens = torch.zeros(1, dtype=torch.int32)
+
+    def run(ws):
+        capi.dflash_kvq_attention(c, 1, 4, 3, 0, None, lens, None, None, 500, q, q.clone(), None, ws, stream=0)
+    room = torch.zeros(1 << 16)
+    for bad in (room[::2], room[:1].expand(1 << 20), room.view(256, 256)[:, :128], room.view(256, 256).t()):
+        with pytest.raises(capi.DFlashError, match="workspace"):
+            run(bad)
+    assert not calls
+    for good in (room, room[64:], room.view(256, 256)[:16], torch.zeros(0)):
+        run(good)
+        assert calls[-1][-2] == good.numel() * 4
