@@ -27,7 +27,6 @@ struct KvqAttnK {
   float decay;
   int pos, g_inv;  // block positions of a CTA's 64 rows; row / G = row * g_inv >> 16 (row < 64)
   int q_tiles, n_splits;
-  uint32_t two;  // 2, see split_weights
   float *part_o, *part_ml;  // [split][row][head][128], [split][row][head] (m, l)
 };
 
@@ -67,13 +66,12 @@ __device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, in
 }
 
 // ---------------------------------------------------------------------------
-// Attention on the 5th-generation tensor cores, both products in 8 bits.
+// Attention on the 5th-generation tensor cores: q . K in 8 bits, the weights times V in 16.
 //
 // One CTA: 64 query rows (64 / G block positions x the G query heads of a KV
 // head) against one split of the sequence's slots, a page (128 slots) a tile.
-// K and V go from the pages to the tensor cores as they are (e4m3, TMA): no
-// conversion, so a tile costs half of the bytes and of the shared memory of a
-// bf16 one.  What is not 8-bit is split into e4m3 parts:
+// K goes from the pages to the tensor cores as it is (e4m3, TMA); q, which is not 8-bit, in
+// two e4m3 parts:
 //
 //   q = 2^a (q1 + q2): q1 = e4m3(q 2^-a), q2 = e4m3 of what q1 leaves.  The parts'
 //   4 + 4 significand bits hold a bf16 (8 bits) exactly where the element is above
@@ -81,65 +79,75 @@ __device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, in
 //   two MMAs (M = 64) into one accumulator.
 //
 //   The weights carry V's exponents: with u_k = log2(e) s_k + eV_k (eV_k the exponent of
-//   slot k's block of V) and m >= max u - 4, z_k = 2^(u_k - m) <= 16 is the weight
-//   of the CODES of V, and the softmax sum is sum z_k 2^-eV_k.  So neither K's
-//   exponents (a factor of S) nor V's (an addend of the exponent) cost a
-//   multiplication an element, and errors in z are relative to the largest
-//   contribution to the output.  16 z = p1 + p2 / 16: p1 has the leading 4 bits, p2 (on a
-//   16 times finer scale) the residual, of either sign, rounded with a fixed dither
-//   over the 16 slots of a block: an error below 2^-8 z, without bias, down to z = 2^-10;
-//   smaller weights are held to 2^-17 (dithered down to 2^-22: many small ones add
-//   up).  P1 and P2 are the halves of one M = 128 operand, so both products cost one
-//   full-rate MMA; row r of P1 is operand row 32 (r / 16) + r % 16 and of P2 the one
-//   16 further, which puts the two halves of an output row into lanes t and t + 16
-//   of one warp.
+//   slot k's block of V), z_k = 2^(u_k - m) is the weight of the CODES of V, and the
+//   softmax sum is sum z_k 2^-eV_k.  So neither K's exponents (a factor of S) nor V's (an
+//   addend of the exponent) cost a multiplication an element.
+//
+//   z is held in fp16, with m so that the largest z of a row lies in [2^11, 2^15]: off by at most
+//   2^-11 of itself down to 2^-14, by 2^-25 below, which is 2^-36 of the largest.  So the
+//   thin tail beside a slot that draws nearly all of the weight keeps its 11 bits, and
+//   131,072 slots below that floor sum to less than 2^-18 of the largest.  (Two e4m3 parts of z
+//   lose the tail: their codes end some 17 binades below the largest.)
+//   V's codes are exact in fp16.  Four warps convert each tile once, transposed, into tensor memory:
+//   O^T = V^T Z^T is an M = 128 MMA (full rate) with A = V^T there and B = Z in shared memory.
+//   Through shared memory the fp16 V would be written and read again at twice the bytes of its
+//   codes, and shared memory would bound the loop (1800 of 2190 cycles a tile, measured so).
 //
 // Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle):
-//   Q1, Q2 [64][128] 8 KB each; P [128][128 slots] 16 KB, twice; two stages of K and two
-//   of V [128 slots][128], 16 KB each.  112 KB, so two CTAs share an SM: one's softmax
-//   runs beside the other's MMAs and loads.
-// Tensor memory: 256 columns, S [64 rows][128] twice and O [128 operand rows][128].  An
-// M = 64 accumulator keeps row m in lane (m / 16) * 32 + m % 16, so a second one fits
-// into the other 16 lanes of each quarter: S of odd tiles starts at lane 16.
+//   Q1, Q2 [64][128] 8 KB each; Z fp16 [2][64 rows][64 slots] 16 KB, twice; two stages of K and
+//   two of V [128 slots][128], 16 KB each.  112 KB, so two CTAs share an SM: one's softmax runs
+//   beside the other's MMAs and loads.
+// Tensor memory: 256 columns, S [64 rows][128] twice, V^T [128 dims][128 slots] in fp16 (64
+// columns), O^T [128 dims][64 rows].  An M = 64 accumulator keeps row m in lane
+// (m / 16) * 32 + m % 16, so a second one fits into the other 16 lanes of each quarter: S of
+// odd tiles starts at lane 16.
 //
-// Warps 0-3 (softmax): two threads per row (lanes t, t + 16), 64 slots each, held
-// in registers.  O and the sum are rescaled when the maximum grows by more
-// than a factor 16.  Warp 4 (producer): TMA of K and V.  Warp 5: the MMAs, S two
-// tiles ahead of P V.
-// A warp none of whose rows is in use only takes part in the barriers.
+// Warps 0-3 (softmax): two threads per row (lanes t, t + 16), 64 slots each, held in registers.
+// Warps 4-7: V to fp16, and O's rescaling when a row's maximum has grown by more than a factor
+// 16 (its columns are all four's).  Warp 8 (producer): TMA of K and V.  Warp 9: the MMAs, S two
+// tiles ahead of O^T.  (Warps 10 and 11 only complete a warpgroup, whose registers the softmax takes
+// over.)  A softmax warp none of whose rows is in use only takes part in the barriers.
 //
-// Measured: 32 sequences of one row over 24,000 to 32,768 slots (1.89 GB) 285 us, 6.6 TB/s, the
-// memory's rate; 8 sequences of 16 rows over 16,400 slots (271 MB) 60 us, 4.5 TB/s.  With
-// 64 rows in use the loop is bound by the softmax warps' issue: the 64 weights of a
-// thread and tile take about 630 cycles of a scheduler (256 of them the exponentials)
-// and what is around them as much again, 1400 cycles a tile of an SM, which is about the
-// memory's rate too; a CTA's set-up, first loads and output add some 10,000 cycles that
-// the other CTA of the SM hides in part.  Leaving the MMAs out of a copy made for
-// timing changed nothing.  Tried and slower: eight softmax warps of 32 slots a thread (16 rows at a batch of 8: 93 us against 70), the
-// tile's maximum looked for only after a weight overflowed (88), S read from tensor memory
-// twice instead of held in registers (95), shares of the longest sequence instead of
-// each sequence's own (32 ragged sequences: 70 against 55).
+// Measured: 32 sequences of one row over 24,000 to 32,769 slots (1.89 GB) 307 us, 6.2 TB/s; 8
+// sequences of 16 rows over 16,400 slots (271 MB) 57 us, 4.8 TB/s; 1000 rows of 2 sequences
+// over 2500 to 5097 slots 214 us.
+// Tried and slower (8 sequences of 8 KV heads over 16,384 slots, 1 and 16 rows a sequence; kept form
+// 50 and 56 us): the conversion in rolled loops (81, 85), on eight warps instead of four (66, 76),
+// with the header's 16-bit operands instead of both halves of a register at once (56, 64); V in
+// fp16 through shared memory, one buffer, a ring of quarters or Z in halves (32,769 slots a row: 388 to
+// 407 us against 307); softmax warps without rows left out of the barriers (54, 62: spills).
+// Earlier forms: S re-read from tensor memory instead of held in registers, eight softmax warps of 32
+// slots a thread, the tile's maximum looked for only after a weight overflowed, shares of the longest
+// sequence instead of each sequence's own: each 20 % and more slower.
 // ---------------------------------------------------------------------------
 constexpr int kTile = kPageSlots;
-constexpr uint32_t kTileBytes = kTile * kKvqHd;  // one K or V tile, and P
+constexpr uint32_t kTileBytes = kTile * kKvqHd;  // one K or V tile in codes, and Z
 constexpr uint32_t kQPart = 64 * kKvqHd;
-constexpr uint32_t kAOffP = 2 * kQPart;
-constexpr uint32_t kAOffK = kAOffP + 2 * kTileBytes;
-constexpr int kAStages = 2;
+constexpr uint32_t kZBlock = 64 * 128;       // Z of 64 slots
+constexpr uint32_t kAOffZ = 2 * kQPart;
+constexpr uint32_t kAOffK = kAOffZ + 2 * 2 * kZBlock;
+constexpr int kAStages = 2;  // of K and of V
 constexpr uint32_t kAOffV = kAOffK + kAStages * kTileBytes;
-constexpr uint32_t kAOffQs = kAOffV + kAStages * kTileBytes;  // scale of each query row
-constexpr uint32_t kAOffBar = kAOffQs + 64 * 4;
-constexpr uint32_t kORow = kKvqHd * 4 + 16;  // an accumulator row staged over the tiles, padded
-static_assert(128 * kORow <= kAOffQs, "accumulator rows fit");
+constexpr uint32_t kAOffQs = kAOffV + kAStages * kTileBytes;  // scale of each query row; later
+constexpr uint32_t kAOffAlpha = kAOffQs;                      // [2][64] factors of rescaling
+constexpr uint32_t kAOffGrown = kAOffAlpha + 2 * 64 * 4;      // [2][4] whether a warp has any
+constexpr uint32_t kAOffBar = kAOffGrown + 2 * 4 * 4;
+constexpr uint32_t kORow = kKvqHd * 4 + 16;  // an accumulator row staged over Q and Z, padded
+static_assert(64 * kORow <= kAOffK, "accumulator rows fit");
 constexpr int kAttnQSmem = (int)kAOffBar + 256;  // barriers
 static_assert(2 * (kAttnQSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
-constexpr int kAttnQThreads = 192;
-constexpr uint32_t kAttnQTmem = 256, kTmemOCol = 128;
+// Three warpgroups of 80 registers a thread: the softmax takes over what the others leave.
+constexpr int kAttnQThreads = 384;
+constexpr int kAttnRegs = 80, kSoftmaxRegs = 128, kConvertRegs = 56, kIssueRegs = 56;
+static_assert(2 * kAttnQThreads * kAttnRegs <= 65536, "two CTAs on an SM");
+static_assert(kSoftmaxRegs + kConvertRegs + kIssueRegs <= 3 * kAttnRegs,
+              "what one takes the others leave");
+constexpr uint32_t kAttnQTmem = 256, kTmemVCol = 128, kTmemOCol = 192;
 constexpr uint32_t kSOdd = 16u << 16;  // lane offset of the S buffer of odd tiles
-// Growth of the maximum that is not yet rescaled: z <= 2^4.  (At a factor of 2, 58 %
-// of the warps' tiles rescaled O on 33-page splits, at 16 one in ten does; the headroom costs
-// p2 that many binades at the bottom.)
-constexpr float kLazyLog2 = 4.f;
+// z of the largest weight, when it is met, and its growth that is not yet rescaled: z <= 2^15.
+// (Rescaling at a factor of 2, 58 % of the warps' tiles rescaled O on 33-page splits, at 16
+// one in ten does.)
+constexpr float kTopLog2 = 11.f, kLazyLog2 = 4.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -153,40 +161,67 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// log of a softmax sum l held relative to 2^m; l of a short tail is about 2^kTopLog2, where
+// log2 would lose bits that m has room for
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return ((m + kTopLog2) + __log2f(l * (1.f / 2048))) * kLn2;
+}
+static_assert(kTopLog2 == 11.f, "2^kTopLog2 = 2048");
+// the values of four e4m3 codes, two a word
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// where the NaN bits of a slot of the tile in stage st lie, for the dims 32 cw .. + 31: in the
+// codes they stand for
+__device__ __forceinline__ uint8_t* nan_bits(uint8_t* sm, int st, int slot, int cw) {
+  return sm + kAOffV + st * kTileBytes + slot * 128 + ((2 * cw ^ (slot & 7)) << 4);
+}
+// V's codes of 32 dims in shared memory: zeros from slot `end` on, and in place of NaN from slot
+// `from` on, noted in a bit for each dim of the lane's slots lane + 32 k.
+__device__ __forceinline__ void clean_v(uint8_t* sm, int st, int cw, int lane, int end, int from,
+                                        uint32_t* found) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int slot = lane + 32 * k;
+    found[k] = 0;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      uint4* const at = reinterpret_cast<uint4*>(sm + kAOffV + st * kTileBytes + slot * 128 +
+                                                 (((2 * cw + hh) ^ (slot & 7)) << 4));
+      if (slot >= end) {
+        *at = make_uint4(0u, 0u, 0u, 0u);
+      } else if (slot >= from) {
+        const uint4 v = *at;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w}, bits = 0;  // a bit per byte
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+          w[i] &= ~(m | (m - (m >> 7)));
+          bits |= ((m >> 7) * 0x10204080u >> 28) << (4 * i);
+        }
+        if (bits) *at = make_uint4(w[0], w[1], w[2], w[3]);
+        found[k] |= bits << (16 * hh);
+      }
+    }
+  }
+}
+// Registers a thread of this warpgroup gives back or takes over (all its warps together).
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 // bits below n set (n clamped to 0..32)
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
-}
-
-// Four weights z <= 16 of consecutive slots, the first a multiple of 4 in its block,
-// as four codes of p1 and four of p2, z = (p1 + p2 / 16) / 16.  z in fp16 carries 11
-// significand bits; an fp16 below 2 is an e4m3 code (times 2^8) with three more
-// of them, so codes and roundings are integer operations on its bits:
-//   p1 / 2^8 = y rounded to 4 bits, y = z / 16 (exponent bits - 4; zero for y < 2^-14,
-//   which p2 holds alone), p2 / 2^8 = z - 16 y rounded to 4 bits with a dither.
-// The doublings are multiply-adds by `two` (a 2 the compiler cannot see): they run
-// beside the logic operations, whose pipe bounds this code.
-__device__ __forceinline__ void split_weights(const float* z, int at, uint32_t two, uint32_t& c1,
-                                              uint32_t& c2) {
-  uint32_t d[2], w[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {  // slots at + k and at + k + 2
-    const __half2 zh = __floats2half2_rn(z[k], z[k + 2]);
-    const uint32_t u = __viaddmax_s16x2_relu(*reinterpret_cast<const uint32_t*>(&zh),
-                                             0xf040f040u /* 0x40 - 0x1000 */, 0u);
-    d[k] = u & 0xff80ff80u;
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&d[k]), __float2half2_rn(-16.f), zh);
-    const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);  // exact, either sign
-    // slot i's dither, of the 128 units below a step of the code: 4 + 8 (i's four
-    // bits reversed)
-    const int i = at + k;
-    const uint32_t rev = ((i & 1) << 3) | ((i & 2) << 1) | ((i & 4) >> 1) | ((i & 8) >> 3);
-    const uint32_t dither = (4 + 8 * rev) | ((4 + 8 * (rev | 4)) << 16);  // i + 2: bit 1 set
-    w[k] = ((rb * two + 2 * dither) & 0x7fff7fffu) | (rb & 0x80008000u);
-    d[k] = d[k] * two;
-  }
-  c1 = __byte_perm(d[0], d[1], 0x7351);  // codes in the high byte of each half
-  c2 = __byte_perm(w[0], w[1], 0x7351);
 }
 
 // (a0, a1) * b + c and (a0, a1) + (b0, b1) in one instruction each
@@ -425,40 +460,49 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   uint4 q_raw[8];
   if (warp < 4) load_q(p, b, kvh, j0, warp, lane, q_raw);
 
-  uint8_t* const ps = sm + kAOffP;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kAOffBar);
   uint64_t* const q_full = bars;
-  uint64_t* const s_full = bars + 1;  // two S buffers
-  uint64_t* const s_free = bars + 3;
-  uint64_t* const p_full = bars + 5;  // two P buffers
-  uint64_t* const pv_done = bars + 7;
-  uint64_t* const k_full = bars + 9;
+  uint64_t* const meet = bars + 1;  // the softmax warps among themselves
+  uint64_t* const o_ready = bars + 2;   // O is rescaled for the tile
+  uint64_t* const nan_full = bars + 3;  // NaN's places in a tile, see below
+  uint64_t* const nan_read = bars + 4;
+  uint64_t* const s_full = bars + 5;  // two S buffers
+  uint64_t* const a_full = bars + 7;  // two buffers of the rows' rescaling factors
+  uint64_t* const z_full = bars + 9;  // two Z buffers; S of the tile is read
+  uint64_t* const vt_full = bars + 11;  // the two halves of V^T
+  uint64_t* const vt_empty = bars + 13;
+  uint64_t* const o_done = bars + 15;  // all of O
+  uint64_t* const k_full = bars + 16;
   uint64_t* const k_empty = k_full + kAStages;
   uint64_t* const v_full = k_empty + kAStages;
   uint64_t* const v_empty = v_full + kAStages;
-  uint64_t* const meet = v_empty + kAStages;  // the softmax warps among themselves
-  uint32_t* const tslot = reinterpret_cast<uint32_t*>(meet + 1);
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(v_empty + kAStages);
   volatile int* const nan_any = reinterpret_cast<volatile int*>(tslot + 1);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 4);
+    mbar_init(meet, 4);
+    mbar_init(o_ready, 4);
+    mbar_init(o_done, 1);
+    mbar_init(nan_full, 4);
+    mbar_init(nan_read, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&a_full[i], 4);
+      mbar_init(&z_full[i], 4);
+      mbar_init(&vt_full[i], 4);
+      mbar_init(&vt_empty[i], 1);
     }
-    mbar_init(meet, 4);
     for (int i = 0; i < kAStages; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 4);
     }
-    *nan_any = 0;
+    nan_any[0] = nan_any[1] = 0;
     mbar_fence_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(tslot, kAttnQTmem);
     tmem_relinquish();
   }
@@ -489,6 +533,12 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   pdl_trigger();
   const uint32_t tmem = *tslot;
   const int first_page = k_begin / kPageSlots;
+  // rows of the CTA that a launch can use, in the granularity of an MMA's N
+  const int rows16 = (min(p.block, POS) * p.G + 15) & ~15;
+  // slots from here on are not seen by every row of the CTA
+  const int mask_from = p.mask == DFLASH_MASK_NONE     ? k_stop
+                        : p.mask == DFLASH_MASK_CAUSAL ? min(k_stop, ctx + j0 + 1)
+                                                       : min(k_stop, ctx);
 
   if (n_tiles == 0) {
     // no slot at all: rows without anything seen get zeros (an unused split of a
@@ -498,107 +548,217 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       for (int i = 0; i < 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse && h == 0) p.lse[grow * p.H + hr] = -INFINITY;
     }
-  } else if (warp == 4) {
-    // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
-    // softmax does not see its slots).  Whole warps wait, one lane issues: the
-    // addresses and descriptors stay in uniform registers.
-    const bool leader = elect_one();
-    if (leader) {
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-    }
-    int k_issued = 0, v_issued = 0;
-    auto load = [&](int t, bool is_v, int pg) -> bool {
-      const int st = t % kAStages, ph = (t / kAStages) & 1;
-      uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st];
-      uint64_t* full = is_v ? &v_full[st] : &k_full[st];
-      if (t >= kAStages && !__all_sync(0xffffffffu, warp_wait(empty, ph ^ 1, status))) return false;
+  } else if (warp >= 8) {
+    regs_dec<kIssueRegs>();
+    if (warp == 8) {
+      // ---- producer: K one tile ahead of V; an unmapped page loads page 0 (the
+      // softmax does not see its slots).  Whole warps wait, one lane issues: the
+      // addresses and descriptors stay in uniform registers.
+      const bool leader = elect_one();
       if (leader) {
-        mbar_arrive_expect_tx(full, kTileBytes);
-        tma_load_2d(sm + (is_v ? kAOffV : kAOffK) + st * kTileBytes, is_v ? &maps.v : &maps.k, 0,
-                    (max(pg, 0) * p.c.Hkv + kvh) * kPageSlots, full);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+      }
+      int k_issued = 0, v_issued = 0;
+      auto load = [&](int t, bool is_v, int pg) -> bool {
+        const int st = t % kAStages, ph = (t / kAStages) & 1;
+        uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st];
+        uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+        if (t >= kAStages && !__all_sync(0xffffffffu, warp_wait(empty, ph ^ 1, status))) return false;
+        if (leader) {
+          mbar_arrive_expect_tx(full, kTileBytes);
+          tma_load_2d(sm + (is_v ? kAOffV : kAOffK) + st * kTileBytes, is_v ? &maps.v : &maps.k, 0,
+                      (max(pg, 0) * p.c.Hkv + kvh) * kPageSlots, full);
+        }
+        __syncwarp();
+        return true;
+      };
+      int raw_k = kvq_page_load(p.c, seq, first_page), pg_v = 0;
+#pragma unroll 1
+      for (int t = 0; t <= n_tiles; ++t) {
+        const int pg_k = kvq_page_check(p.c, raw_k);
+        raw_k = t + 1 < n_tiles ? kvq_page_load(p.c, seq, first_page + t + 1) : 0;
+        if (t < n_tiles) {
+          if (pg_k < 0) set_dev_status(status, kDevCapacity);
+          if (!load(t, false, pg_k)) break;
+          k_issued = t + 1;
+        }
+        if (t >= 1) {
+          if (!load(t - 1, true, pg_v)) break;
+          v_issued = t;
+        }
+        pg_v = pg_k;
+      }
+      // every issued copy has landed before this warp leaves
+#pragma unroll 1
+      for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
+        warp_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
+#pragma unroll 1
+      for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
+        warp_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---- MMA issuer: S two tiles ahead of O^T.  A commit covers all that was issued before: that
+      // S(t) is done says that O^T(t - 2) is, and that Z(t) is full that S(t) is read.
+      constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
+      const uint32_t id_o = idesc_f16_f32(128, 0) | ((uint32_t)(rows16 >> 3) << 17);
+      const uint64_t q_desc = sw128_desc(smem_u32(sm)), z_desc = sw128_desc(smem_u32(sm + kAOffZ));
+      const uint64_t k_desc = sw128_desc(smem_u32(sm + kAOffK));
+      // (a descriptor's address field counts 16 bytes)
+      const bool leader = elect_one();
+      bool ok = __all_sync(0xffffffffu, warp_wait(q_full, 0, status));
+      auto scores = [&](int t) {
+        const int st = t % kAStages;
+        ok = warp_wait(&k_full[st], (t / kAStages) & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t kd = k_desc + st * (kTileBytes >> 4);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f8(tmem + (t & 1) * kSOdd, q_desc + part * (kQPart >> 4) + kk * 2, kd + kk * 2,
+                        id_s, part + kk > 0 ? 1u : 0u);
+          tc_commit(&s_full[t & 1]);
+          tc_commit(&k_empty[st]);
+        }
+        __syncwarp();
+      };
+      if (ok) scores(0);
+      if (ok && n_tiles > 1) scores(1);
+#pragma unroll 1
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        ok = warp_wait(o_ready, t & 1, status);
+        if (ok) ok = warp_wait(&z_full[t & 1], (t >> 1) & 1, status);
+        const uint64_t zd = z_desc + (t & 1) * (2 * kZBlock >> 4);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // 64 slots each
+          if (ok) ok = warp_wait(&vt_full[u], t & 1, status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 slots
+              tc_mma_f16_ta(tmem + kTmemOCol, tmem + kTmemVCol + 32 * u + 8 * kk,
+                            zd + u * (kZBlock >> 4) + kk * 2, id_o, t + u + kk > 0 ? 1u : 0u);
+            tc_commit(&vt_empty[u]);
+            if (u == 1 && t + 1 == n_tiles) tc_commit(o_done);
+          }
+          __syncwarp();
+        }
+        if (ok && t + 2 < n_tiles) scores(t + 2);
       }
       __syncwarp();
-      return true;
-    };
-    int raw_k = kvq_page_load(p.c, seq, first_page), pg_v = 0;
-#pragma unroll 1
-    for (int t = 0; t <= n_tiles; ++t) {
-      const int pg_k = kvq_page_check(p.c, raw_k);
-      raw_k = t + 1 < n_tiles ? kvq_page_load(p.c, seq, first_page + t + 1) : 0;
-      if (t < n_tiles) {
-        if (pg_k < 0) set_dev_status(status, kDevCapacity);
-        if (!load(t, false, pg_k)) break;
-        k_issued = t + 1;
-      }
-      if (t >= 1) {
-        if (!load(t - 1, true, pg_v)) break;
-        v_issued = t;
-      }
-      pg_v = pg_k;
     }
-    // every issued copy has landed before this warp leaves
+  } else if (warp >= 4) {
+    regs_dec<kConvertRegs>();
+    // ---- V to fp16 in tensor memory, exactly (NaN stays NaN), and O's rescaling.  This warp has
+    // the dims 32 cw .. + 31, its lane quarter.  A transposing load gives a lane four
+    // slots 4 (lane % 4) .. of dim lane / 4 (and + 8) of 16 x 16 codes; in fp16 they are
+    // the two words that the 16x256b store takes from it.
+    // V rows that are not seen must not hold NaN (0 * NaN): those behind the split's slots, or
+    // on no page, are zeroed first; in rows that some query rows see and others do not,
+    // NaN codes are zeroed and noted for the rows that see them: a bit for each of the warp's dims,
+    // left over the slot's own codes, which are used by then.
+    const int cw = warp - 4;
+    const uint32_t lane_base = tmem + ((uint32_t)(cw * 32) << 16);
+    // this lane's rows of the transposing loads: slots lane + 32 g, 16 dims
+    const uint32_t v_at0 = smem_u32(sm + kAOffV) + lane * 128 + ((2 * cw ^ (lane & 7)) << 4);
+    const uint32_t v_at1 = smem_u32(sm + kAOffV) + lane * 128 + (((2 * cw + 1) ^ (lane & 7)) << 4);
+    bool ok = true;
+    int marked = 0;  // tiles so far that not every row sees whole
+    int raw = kvq_page_load(p.c, seq, first_page);
 #pragma unroll 1
-    for (int t = max(0, k_issued - kAStages); t < k_issued; ++t)
-      warp_wait(&k_full[t % kAStages], (t / kAStages) & 1, status);
-#pragma unroll 1
-    for (int t = max(0, v_issued - kAStages); t < v_issued; ++t)
-      warp_wait(&v_full[t % kAStages], (t / kAStages) & 1, status);
-    __syncwarp();
-  } else if (warp == 5) {
-    // ---- MMA issuer: S two tiles ahead of P V
-    constexpr uint32_t id_s = idesc_e4m3_f32(64, kTile);
-    constexpr uint32_t id_o = idesc_e4m3_f32(128, kKvqHd) | kIdescBMajorMN;
-    const uint64_t q_desc = sw128_desc(smem_u32(sm)), p_desc = sw128_desc(smem_u32(ps));
-    const uint64_t k_desc = sw128_desc(smem_u32(sm + kAOffK));
-    const uint64_t v_desc = sw128_desc_mn(smem_u32(sm + kAOffV), kTileBytes);
-    // (a descriptor's address field counts 16 bytes)
-    const bool leader = elect_one();
-    bool ok = __all_sync(0xffffffffu, warp_wait(q_full, 0, status));
-    auto scores = [&](int t) {
-      const int st = t % kAStages;
-      ok = warp_wait(&k_full[st], (t / kAStages) & 1, status);
-      if (ok && t >= 2) ok = warp_wait(&s_free[t & 1], ((t >> 1) - 1) & 1, status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t kd = k_desc + st * (kTileBytes >> 4);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f8(tmem + (t & 1) * kSOdd, q_desc + part * (kQPart >> 4) + kk * 2, kd + kk * 2, id_s,
-                      part + kk > 0 ? 1u : 0u);
-        tc_commit(&s_full[t & 1]);
-        tc_commit(&k_empty[st]);
-      }
-      __syncwarp();
-    };
-    if (ok) scores(0);
-    if (ok && n_tiles > 1) scores(1);
-#pragma unroll 1
-    for (int t = 0; ok && t < n_tiles; ++t) {
-      const int st = t % kAStages;
-      ok = warp_wait(&v_full[st], (t / kAStages) & 1, status);
-      if (ok) ok = warp_wait(&p_full[t & 1], (t >> 1) & 1, status);
-      ok = __all_sync(0xffffffffu, ok);
+    for (int t = 0; t < n_tiles; ++t) {
+      const int tile0 = k_begin + t * kTile, st = t % kAStages;
+      const int stop = kvq_page_check(p.c, raw) < 0 ? tile0 : k_stop;
+      if (t + 1 < n_tiles) raw = kvq_page_load(p.c, seq, first_page + t + 1);
+      const bool partly = tile0 + kTile > min(stop, mask_from);
+      ok = __all_sync(0xffffffffu, warp_wait(&v_full[st], (t / kAStages) & 1, status));
       if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t vd = v_desc + st * (kTileBytes >> 4), pd = p_desc + (t & 1) * (kTileBytes >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f8(tmem + kTmemOCol, pd + kk * 2, vd + kk * (32 * kKvqHd >> 4), id_o,
-                    t + kk > 0 ? 1u : 0u);
-        tc_commit(&pv_done[t & 1]);
-        tc_commit(&v_empty[st]);
+      uint32_t found[4] = {0u, 0u, 0u, 0u};
+      if (partly) {
+        clean_v(sm, st, cw, lane, stop - tile0, mask_from - tile0, found);
+        if (found[0] | found[1] | found[2] | found[3]) nan_any[marked & 1] = 1;
+        __syncwarp();
       }
-      __syncwarp();
-      if (t + 2 < n_tiles) scores(t + 2);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // 64 slots each
+        // this half of O^T(t - 1) is done: its place is free
+        if (ok && t > 0) ok = warp_wait(&vt_empty[u], (t - 1) & 1, status);
+        if (u == 1) {
+          // O holds tiles 0 .. t - 1 now: its columns (rows of q) times the factors by which the
+          // maximum of this tile shrinks them, 16 columns for each softmax warp that has any
+          if (ok) ok = warp_wait(&a_full[t & 1], (t >> 1) & 1, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          const float* const factor = reinterpret_cast<const float*>(sm + kAOffAlpha) + (t & 1) * 64;
+          const int* const any = reinterpret_cast<const int*>(sm + kAOffGrown) + (t & 1) * 4;
+          if (t > 0) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {
+              if (!any[w]) continue;
+              float o[16];
+              tmem_ld16(lane_base + kTmemOCol + 16 * w, o);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(factor + 16 * w + i);
+                o[i] *= f.x;
+                o[i + 1] *= f.y;
+                o[i + 2] *= f.z;
+                o[i + 3] *= f.w;
+              }
+              tmem_st16(lane_base + kTmemOCol + 16 * w, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_ready);
+        }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        uint32_t w[2][8];  // 16 dims each
+        const uint32_t off = st * kTileBytes + u * (64 * 128);
+        ldmatrix_b8_trans(v_at0 + off, &w[0][0]);
+        ldmatrix_b8_trans(v_at0 + off + 32 * 128, &w[0][4]);
+        ldmatrix_b8_trans(v_at1 + off, &w[1][0]);
+        ldmatrix_b8_trans(v_at1 + off + 32 * 128, &w[1][4]);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t vt[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) codes_to_half(w[hh][i], vt[2 * i], vt[2 * i + 1]);
+          tmem_st_16x256b_x4(lane_base + ((uint32_t)(16 * hh) << 16) + kTmemVCol + 32 * u, vt);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vt_full[u]);
+      }
+      if (!ok) break;
+      if (partly) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint32_t*>(nan_bits(sm, st, lane + 32 * k, cw)) = found[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(nan_full);
+        ok = __all_sync(0xffffffffu, warp_wait(nan_read, marked & 1, status));
+        if (!ok) break;
+        // (two flags, in turn: another of these warps may be a tile ahead, but not two)
+        if (threadIdx.x == 128) nan_any[marked & 1] = 0;
+        ++marked;
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(&v_empty[st]);
     }
     __syncwarp();
   } else {
+    regs_inc<kSoftmaxRegs>();
     // ---- softmax warps: half h of row t16's thread pair holds slots
     // 64 h .. 64 h + 63 of every tile (blocks 4 h .. 4 h + 3)
     const bool warp_live = __any_sync(0xffffffffu, live);
@@ -612,12 +772,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
     if (lane == 0) mbar_arrive(q_full);
     const float q_signed = warp_live ? q_scales[t16] : 0.f;
     const float q_scale = fabsf(q_signed);
+    __syncwarp();  // (the scales' place takes the factors of even tiles)
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    // slots from here on are not seen by every row of the CTA
-    const int mask_from = p.mask == DFLASH_MASK_NONE     ? k_stop
-                          : p.mask == DFLASH_MASK_CAUSAL ? min(k_stop, ctx + j0 + 1)
-                                                         : min(k_stop, ctx);
-    const int partial_from = p.mask == DFLASH_MASK_NONE ? k_stop : mask_from;
     float m_used = -INFINITY, l = 0.f;
     uint32_t bad[4] = {0u, 0u, 0u, 0u};  // dims in which the row saw a NaN of V
     bool ok = true;
@@ -632,19 +788,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       return make_uint2(*reinterpret_cast<const uint32_t*>(k_ex + at),
                         *reinterpret_cast<const uint32_t*>(v_ex + at));
     };
-    const uint32_t b_s_full = smem_u32(s_full), b_s_free = smem_u32(s_free);
-    const uint32_t b_p_full = smem_u32(p_full), b_pv = smem_u32(pv_done);
+    const uint32_t b_s_full = smem_u32(s_full), b_z_full = smem_u32(z_full);
     auto wait_for = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, warp_wait(bar, parity, status));
     };
-    // a barrier of the four warps whose wait is bounded like every other
-    uint32_t met = 0;
-    auto warps_meet = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(meet);
-      ok = wait_for(smem_u32(meet), met++ & 1);
-      return ok;
-    };
+    // this lane's 64 weights of a tile: a row of its block of Z
+    uint8_t* const z_row = sm + kAOffZ + h * kZBlock + row * 128;
+    int marked = 0;  // tiles so far that not every row sees whole
     int pg = kvq_page_check(p.c, *next_id++);
     int raw_next = n_tiles > 1 ? *next_id++ : -1;
     uint2 ex = exps_of(pg);
@@ -671,9 +821,8 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         tmem_wait_ld();
         tc_fence_before();
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(b_s_free + odd8);
       float ck[4], ev[4], mx = -INFINITY;
+      bool any_grown = false;
       if (warp_live) {
         if (masked) {
           // Blocks from `stop` on may never have been written, and an unmapped page has page
@@ -700,100 +849,52 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           mx = fmaxf(mx, fmaf(bm, ck[i], ev[i]));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      }
-      // P V(t - 2) done: this P buffer is free (a warp without rows waits too: its
-      // arrival below must not count for an earlier tile)
-      if (t >= 2 && !(ok = wait_for(b_pv + odd8, phase ^ 1))) break;
-      if (warp_live) {
-        const bool grow_m = mx > m_used + kLazyLog2;
-        if (__any_sync(0xffffffffu, grow_m)) {
-          const float alpha = grow_m ? ex2(m_used - mx) : 1.f;
-          if (t > 0) {
-            // O holds tiles 0 .. t - 1 once P V(t - 1) is done
-            if (!(ok = wait_for(b_pv + (odd8 ^ 8), ((t - 1) >> 1) & 1))) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(lane_base + kTmemOCol + 32 * c, o);
-            }
-            tmem_wait_st();
-          }
-          if (grow_m) {
-            l *= alpha;
-            m_used = mx;
-          }
+        const bool grown = mx > m_used + (kTopLog2 + kLazyLog2);
+        any_grown = __any_sync(0xffffffffu, grown);
+        if (any_grown) {
+          const float m_new = mx - kTopLog2;
+          const float alpha = grown ? ex2(m_used - m_new) : 1.f;
+          if (h == 0) reinterpret_cast<float*>(sm + kAOffAlpha)[(t & 1) * 64 + row] = alpha;
+          l *= alpha;
+          if (grown) m_used = m_new;
         }
+      }
+      // (the factors of two tiles ago are used: S of this tile was issued after their O^T)
+      if (lane == 0) reinterpret_cast<int*>(sm + kAOffGrown)[(t & 1) * 4 + warp] = any_grown;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[t & 1]);
+      // (O^T(t - 2) is done, see the MMA issuer: this Z buffer is free)
+      if (warp_live) {
         const float base = m_used == -INFINITY ? 0.f : -m_used;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float add = ev[i] + base;
           float2 sum = make_float2(0.f, 0.f);
-          uint32_t c1[4], c2[4];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            float z[4];
+          for (int w = 0; w < 2; ++w) {
+            uint32_t zh[4];
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float2 x = fma2(make_float2(s[16 * i + 4 * w + k], s[16 * i + 4 * w + k + 1]),
-                                    ck[i], add);
-              z[k] = ex2(x.x);
-              z[k + 1] = ex2(x.y);
-              sum = add2(sum, make_float2(z[k], z[k + 1]));
+            for (int k = 0; k < 4; ++k) {
+              const int at = 16 * i + 8 * w + 2 * k;
+              const float2 x = fma2(make_float2(s[at], s[at + 1]), ck[i], add);
+              const float2 z = make_float2(ex2(x.x), ex2(x.y));
+              sum = add2(sum, z);
+              const __half2 z16 = __floats2half2_rn(z.x, z.y);
+              zh[k] = *reinterpret_cast<const uint32_t*>(&z16);
             }
-            split_weights(z, 4 * w, p.two, c1[w], c2[w]);
+            *reinterpret_cast<uint4*>(z_row + (t & 1) * (2 * kZBlock) + (((2 * i + w) ^ (t16 & 7)) << 4)) =
+                make_uint4(zh[0], zh[1], zh[2], zh[3]);
           }
           l = fmaf(sum.x + sum.y, pow2i(-(int)ev[i]), l);
-          const uint32_t off = (t & 1) * kTileBytes + (uint32_t)(32 * warp + t16) * 128 +
-                               ((uint32_t)((4 * h + i) ^ (t16 & 7)) << 4);
-          *reinterpret_cast<uint4*>(ps + off) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
-          *reinterpret_cast<uint4*>(ps + off + 16 * 128) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
         }
       }
-      // V rows that are not seen must not hold NaN codes (0 * NaN): those behind
-      // the split's slots, or on no page, are zeroed; in rows that some query
-      // rows see and others do not, NaN codes are zeroed and noted for the rows
-      // that see them (in a table [128 slots][4] of dims' bits, over the other P
-      // buffer)
-      if (tile0 + kTile > min(stop, partial_from)) {
-        const int st = t % kAStages;
-        ok = wait_for(smem_u32(&v_full[st]), (t / kAStages) & 1);
-        if (ok && t > 0) ok = wait_for(b_pv + (odd8 ^ 8), ((t - 1) >> 1) & 1);
-        if (!ok) break;
-        uint32_t* const nan_bits = reinterpret_cast<uint32_t*>(ps + (~t & 1) * kTileBytes);
-        *reinterpret_cast<uint4*>(nan_bits + threadIdx.x * 4) = make_uint4(0u, 0u, 0u, 0u);
-        if (!warps_meet()) break;
-        uint8_t* const vs = sm + kAOffV + st * kTileBytes;
-        const int v_end = max(stop - tile0, 0), v_from = max(0, min(v_end, partial_from - tile0));
-#pragma unroll 1
-        for (int i = v_from * 8 + (int)threadIdx.x; i < kTile * 8; i += 128) {
-          const int vr = i >> 3, ch = i & 7;
-          uint4* const at = reinterpret_cast<uint4*>(vs + vr * 128 + ((ch ^ (vr & 7)) << 4));
-          if (vr >= v_end) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-            continue;
-          }
-          const uint4 v4 = *at;
-          uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
-          uint32_t found = 0;  // bit per byte
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t m = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            w[k] &= ~(m | (m - (m >> 7)));
-            found |= ((m >> 7) * 0x10204080u >> 28) << (4 * k);
-          }
-          if (found) {
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
-            atomicOr(&nan_bits[vr * 4 + (ch >> 1)], found << (16 * (ch & 1)));
-            *nan_any = 1;
-          }
-        }
-        if (!warps_meet()) break;
-        if (*nan_any) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(b_z_full + odd8);
+      // a tile that some rows see and others do not: NaN of V, noted by the warps that convert it
+      if (masked) {
+        if (!(ok = wait_for(smem_u32(nan_full), marked & 1))) break;
+        if (nan_any[marked++ & 1]) {
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t vis = visible32(p, tile0 + 64 * h + 32 * c, stop, ctx, jr, anc);
@@ -801,41 +902,41 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
             while (vis) {
               const int at = 64 * h + 32 * c + __ffs(vis) - 1;
               vis &= vis - 1;
-              for (int k = 0; k < 4; ++k) bad[k] |= nan_bits[at * 4 + k];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                bad[k] |= *reinterpret_cast<const uint32_t*>(nan_bits(sm, t % kAStages, at, k));
             }
           }
-          if (!warps_meet()) break;
-          if (threadIdx.x == 0) *nan_any = 0;
-          if (!warps_meet()) break;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(nan_read);
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(b_p_full + odd8);
     }
-    // ---- epilogue: lanes t and t + 16 hold the P1 and the P2 part of row t's O
+    // ---- epilogue: lane d of warp w has dim 32 w + d of every row's O
     l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k) bad[k] |= __shfl_xor_sync(0xffffffffu, bad[k], 16);
-    if (ok) ok = wait_for(b_pv + ((n_tiles - 1) & 1) * 8, ((n_tiles - 1) >> 1) & 1);
-    if (ok && warp_live) {
+    if (ok) ok = wait_for(smem_u32(o_done), 0);
+    if (ok) {
       tc_fence_after();
+      // Through shared memory (Q and Z are done with): rows of dims, padded
+#pragma unroll 1
+      for (int c = 0; c < rows16; c += 16) {
+        float o[16];
+        tmem_ld16(lane_base + kTmemOCol + c, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float*>(sm + (c + i) * kORow + (32 * warp + lane) * 4) = o[i];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      ok = wait_for(smem_u32(meet), 0);
+    }
+    if (ok && warp_live) {
       const bool none = l == 0.f;
       if (q_signed < 0.f && !none) l = __int_as_float(0x7fffffff);
       const bool whole = span.used == 1;
-      // Through shared memory (Q, P, K and V are done with), so that the stores are
-      // whole rows: lane i's 128 columns (row i % 16, part i / 16) as a padded row
-      uint8_t* const stage = sm + warp * 32 * kORow;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32_nowait(lane_base + kTmemOCol + 32 * c, o);
-        tmem_wait_ld();
-        uint4* const at = reinterpret_cast<uint4*>(stage + lane * kORow + 128 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) at[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
+      const uint8_t* const stage = sm + warp * 16 * kORow;
       const long long rh = grow * p.H + hr;
       const long long part_row = (long long)split * p.batch * p.block * p.H + rh;
       const long long out_at = (whole ? rh : part_row) * kKvqHd;
@@ -843,22 +944,18 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(m_used, l);
         else if (p.lse)
-          p.lse[rh] = none ? -INFINITY : (m_used + __log2f(l)) * kLn2;
+          p.lse[rh] = none ? -INFINITY : lse_of(m_used, l);
       }
       const float scale = none ? 0.f : (whole ? rcp(l) : 1.f);
       const bool any_bad = __any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u);
       const int n_live = __popc(__ballot_sync(0xffffffffu, live) & 0xffffu);  // rows 0 .. n_live - 1
-      __syncwarp();
 #pragma unroll 2
       for (int i = 0; i < n_live; ++i) {
         const float4 x = *reinterpret_cast<const float4*>(stage + i * kORow + 16 * lane);
-        const float4 y = *reinterpret_cast<const float4*>(stage + (16 + i) * kORow + 16 * lane);
         const float sc = __shfl_sync(0xffffffffu, scale, i);
         const long long at = __shfl_sync(0xffffffffu, out_at, i) + 4 * lane;
-        const float s1 = sc * (1.f / 16), s2 = sc * (1.f / 256);
         // (a row that saw nothing has sc = 0: zeros, not 0 * NaN)
-        float4 v = make_float4(x.x * s1 + y.x * s2, x.y * s1 + y.y * s2, x.z * s1 + y.z * s2,
-                               x.w * s1 + y.w * s2);
+        float4 v = make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
         if (sc == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (any_bad) {
           uint32_t nan = 0;
@@ -886,7 +983,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) tmem_dealloc(tmem, kAttnQTmem);
+  if (warp == 8) tmem_dealloc(tmem, kAttnQTmem);
 }
 
 // Merge of the splits of a row: one warp per (row, head), lane l holding dims
@@ -957,7 +1054,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
   pk.x = *reinterpret_cast<const uint32_t*>(&a);
   pk.y = *reinterpret_cast<const uint32_t*>(&c);
   *reinterpret_cast<uint2*>(p.out + (int64_t)rh * kKvqHd + lane * 4) = pk;
-  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+  if (p.lse && lane == 0) p.lse[rh] = l == 0.f ? -INFINITY : lse_of(m, l);
 }
 
 // Splits of a launch of `ctas` CTAs over max_keys slots: the count, as many as the
@@ -965,8 +1062,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kvq_merge_kernel(const KvqAt
 // two CTAs share the SM.  Such a pair takes 2 units a tile of each, a CTA alone 1.4; a CTA's
 // set-up and output cost 6 beside its tiles; merging costs a unit for every 7200
 // (row, head) outputs of a split.  (Measured at a batch of 8, 16,400 slots, 16 rows, 32 heads
-// over 8: 1 to 9 splits 150, 86, 78, 64, 84, 81, 74, 76, 67 us, 4 taken; 1000 rows over about
-// 4000 slots: 226 us unsplit, 265 with 2 splits.)
+// over 8: 1 to 9 splits 126, 73, 68, 57, 77, 77, 70, 67, 63 us, 4 taken; 1000 rows over about
+// 4000 slots: 213 us unsplit, 261 with 2 splits; 32 sequences of one row over 32,769 slots: 304 to
+// 326 us at 1 to 10 splits, 307 at 7, taken.)
 constexpr int kKvqMaxSplits = 256;
 static int kvq_plan_splits(int sm_count, int64_t ctas, int64_t max_keys, int64_t max_splits,
                            int64_t merge_rows) {
@@ -1017,8 +1115,9 @@ constexpr uint32_t kSOffBar = kSOffSlot + kSGroup * kTile * 8;
 constexpr int kScoreSmem = (int)kSOffBar + 256 + 1024;
 constexpr uint32_t kSOffMute = kSOffBar + 192;  // [3][64] bits: rows with lse -inf
 constexpr uint32_t kScoreTmem = 256;
+constexpr int kScoreThreads = 192;
 
-__global__ void __launch_bounds__(kAttnQThreads, 2)
+__global__ void __launch_bounds__(kScoreThreads, 2)
     kvq_score_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
   pdl_wait();
   extern __shared__ uint8_t smem_raw[];
@@ -1403,7 +1502,6 @@ static dflash_status kvq_attn_args(KvqAttnK* p, const dflash_kvq_cache* cache, i
   p->H = H;
   p->G = H / cache->n_kv_heads;
   p->pos = 64 / p->G;
-  p->two = 2;
   p->q_tiles = (int)kvq_q_tiles(block, p->G);
   p->g_inv = (65536 + p->G - 1) / p->G;
   p->q = static_cast<const bf16*>(q);
@@ -1496,7 +1594,7 @@ dflash_status dflash_kvq_score(const dflash_kvq_cache* cache, int32_t batch, int
   static std::atomic<bool> smem_done[kMaxDevices];
   if (ensure_smem_attr(smem_done, kvq_score_kernel, kScoreSmem) != cudaSuccess) return DFLASH_E_CUDA;
   const dim3 grid(splits, cache->n_kv_heads, batch);
-  if (launch_k(true, kvq_score_kernel, grid, dim3(kAttnQThreads), kScoreSmem, (cudaStream_t)stream,
+  if (launch_k(true, kvq_score_kernel, grid, dim3(kScoreThreads), kScoreSmem, (cudaStream_t)stream,
                maps, p) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;

@@ -521,6 +521,11 @@ DFLASH_API dflash_status dflash_kvq_read(const dflash_kvq_cache *cache, int32_t 
  * (status DFLASH_E_CAPACITY).  Rows past q_lens[b] are left as they were.  What
  * a row does not see (other rows' slots, whatever lies behind slot n) does not
  * enter its result, NaN included.
+ * Scores and sums are in fp32 from bf16 q and the cache's exact values, but for elements of q
+ * below 2^-10 of their row's largest, which are held to 2^-18 of that; a row of q with a
+ * NaN, an infinity or a magnitude above 448 * 2^118 gets NaN.  A weight is held in fp16: off
+ * by at most 2^-11 of itself or, in units of the largest p_s * 2^(exponent of slot s's block of
+ * V) of the row, by 2^-36.  The result is rounded to bf16.
  *   q_dev    [batch][block] rows of n_heads * 128 bf16, q_row_stride elements
  *            apart (>= n_heads * 128, a multiple of 8), 16-byte aligned
  *   out_dev  [batch][block][n_heads][128] bf16, 16-byte aligned
@@ -552,7 +557,7 @@ DFLASH_API int64_t dflash_kvq_attention_workspace(int32_t batch, int32_t n_heads
  *                          exp(q_jh . k_s / sqrt(128) - lse_jh)   (s seen by j)
  * for the slots s < n of the batch's sequences q; the rest is left as it was.
  * Arguments as in dflash_kvq_attention, whose lse is read (a row with lse -inf
- * adds nothing).  For a drafted block call it after acceptance, with the
+ * adds nothing; q is held as there, the weights are in fp32).  For a drafted block call it after acceptance, with the
  * committed length and q_lens = the rows kept.
  *   score_in_dev, score_out_dev [n_seqs][n_kv_heads][pages_per_seq * 128] float;
  *   may be the same array; score_in NULL reads as zero.  4-byte aligned. */

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from kvq_util import HD, PAGE, Cache, bf16
+from kvq_util import HD, PAGE, Cache, ancestors, bf16
 from test_gpu_kvq import check_rows, i32, run_attention
 from oracle import kvq as ok
 
@@ -164,3 +164,36 @@ def test_evict_updates_lengths_in_place(heads, lens, budget, window):
     for run in runs[1:]:
         for a, z in zip(run, runs[0]):
             assert torch.equal(a, z)
+
+
+@pytest.mark.parametrize("mask,n,block,g", [("causal", 700, 300, 1), ("causal", 520, 140, 3), ("tree", 640, 130, 2),
+                                            ("tree", 300, 200, 1)])
+def test_attention_nan_of_v_over_several_partly_seen_pages(mask, n, block, g):
+    """Rows see the NaN of V of the slots they see, dim by dim, and no other's."""
+    rng = np.random.default_rng(n)
+    c = Cache(1, 1, (n + PAGE - 1) // PAGE, seed=n)
+    k, v = rng.normal(size=(1, n, 1, HD)), rng.normal(size=(1, n, 1, HD))
+    slots = np.sort(rng.choice(np.arange(n - block, n), 12, replace=False))
+    dims = rng.choice(HD, 12)
+    v[0, slots, 0, dims] = np.nan
+    v[0, 5, 0, 77] = np.nan  # seen by every row
+    v[0, slots[3], 0, :] = np.nan
+    c.append([0], k, v)
+    anc = sets = None
+    if mask == "tree":
+        parents = [-1] + [int(rng.integers(max(0, i - 9), i)) for i in range(1, block)]
+        sets, bits = ancestors(parents, (block + 63) // 64)
+        anc = bits[None].copy()
+    q = rng.normal(size=(1, block, g, HD))
+    vis = ok.visible(mask, n, block, sets)
+    held = c.val["v"][0, :n]
+    nan = (vis.astype(float) @ np.isnan(held[:, 0])) > 0  # [block][128]
+    c.val["v"][0, :n] = np.nan_to_num(held)
+    for ws in (True, False):
+        got, lse, qe = run_attention(c, q, mask, [n], anc=anc, ws=ws)
+        assert (np.isnan(got[0]) == nan[:, None]).all()
+        ref, ref_lse, mag = ok.attend(qe[0], c.val["k"][0, :n], c.val["v"][0, :n], vis)
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * mag + 1e-30
+        ok_at = np.broadcast_to(~nan[:, None], ref.shape)
+        assert (np.abs(got[0] - ref) <= tol)[ok_at].all()
+        assert np.isfinite(lse).all()
