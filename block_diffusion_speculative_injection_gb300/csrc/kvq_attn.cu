@@ -79,15 +79,16 @@ __device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, in
 //   two MMAs (M = 64) into one accumulator.
 //
 //   The weights carry V's exponents: with u_k = log2(e) s_k + eV_k (eV_k the exponent of
-//   slot k's block of V), z_k = 2^(u_k - m) is the weight of the CODES of V, and the
+//   slot k's block of V), z_k = 2^(u_k - m + 11) is the weight of the CODES of V, and the
 //   softmax sum is sum z_k 2^-eV_k.  So neither K's exponents (a factor of S) nor V's (an
 //   addend of the exponent) cost a multiplication an element.
 //
-//   z is held in fp16, with m so that the largest z of a row lies in [2^11, 2^15]: off by at most
-//   2^-11 of itself down to 2^-14, by 2^-25 below, which is 2^-36 of the largest.  So the
-//   thin tail beside a slot that draws nearly all of the weight keeps its 11 bits, and
-//   131,072 slots below that floor sum to less than 2^-18 of the largest.  (Two e4m3 parts of z
-//   lose the tail: their codes end some 17 binades below the largest.)
+//   z is held in fp16, with m (a maximum met so far) so that a row's largest is in
+//   [2^11, 2^15]: off by at most 2^-11 of itself down to 2^-14, by 2^-25 below, which is 2^-36
+//   of the largest.  So the thin tail beside a slot that draws nearly all of the weight
+//   keeps its 11 bits, and 131,072 slots below that floor sum to less than 2^-18 of the
+//   largest.  (Two e4m3 parts of z lose the tail: their codes end some 17 binades below the
+//   largest.)
 //   V's codes are exact in fp16.  Four warps convert each tile once, transposed, into tensor memory:
 //   O^T = V^T Z^T is an M = 128 MMA (full rate) with A = V^T there and B = Z in shared memory.
 //   Through shared memory the fp16 V would be written and read again at twice the bytes of its
@@ -148,6 +149,9 @@ constexpr uint32_t kSOdd = 16u << 16;  // lane offset of the S buffer of odd til
 // (Rescaling at a factor of 2, 58 % of the warps' tiles rescaled O on 33-page splits, at 16
 // one in ten does.)
 constexpr float kTopLog2 = 11.f, kLazyLog2 = 4.f;
+// Maxima (in units of log2) up to which their own rounding, that of kTopLog2 - m and that of its
+// sum with an exponent, 2^-4 each at most, keep z below 2^15.2.
+constexpr float kFarLog2 = 1048576.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -161,10 +165,10 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// log of a softmax sum l held relative to 2^m; l of a short tail is about 2^kTopLog2, where
-// log2 would lose bits that m has room for
+// log of a softmax sum l of z (l 2^-11 is at most the row's slots, and 1 where one has all the
+// weight: log2 is most exact there)
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return ((m + kTopLog2) + __log2f(l * (1.f / 2048))) * kLn2;
+  return (m + __log2f(l * (1.f / 2048))) * kLn2;
 }
 static_assert(kTopLog2 == 11.f, "2^kTopLog2 = 2048");
 // the values of four e4m3 codes, two a word
@@ -849,14 +853,13 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
           mx = fmaxf(mx, fmaf(bm, ck[i], ev[i]));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const bool grown = mx > m_used + (kTopLog2 + kLazyLog2);
+        const bool grown = mx > m_used + kLazyLog2;
         any_grown = __any_sync(0xffffffffu, grown);
         if (any_grown) {
-          const float m_new = mx - kTopLog2;
-          const float alpha = grown ? ex2(m_used - m_new) : 1.f;
+          const float alpha = grown ? ex2(m_used - mx) : 1.f;
           if (h == 0) reinterpret_cast<float*>(sm + kAOffAlpha)[(t & 1) * 64 + row] = alpha;
           l *= alpha;
-          if (grown) m_used = m_new;
+          if (grown) m_used = mx;
         }
       }
       // (the factors of two tiles ago are used: S of this tile was issued after their O^T)
@@ -865,10 +868,23 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
       if (lane == 0) mbar_arrive(&a_full[t & 1]);
       // (O^T(t - 2) is done, see the MMA issuer: this Z buffer is free)
       if (warp_live) {
-        const float base = m_used == -INFINITY ? 0.f : -m_used;
+        const float m = m_used == -INFINITY ? 0.f : m_used;
+        float add[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add[i] = ev[i] + (kTopLog2 - m);
+        if (__any_sync(0xffffffffu, fabsf(m) > kFarLog2)) {
+          // such an addend is off by more than z has room for: u (rounded as in the maximum, so
+          // that the largest is the maximum) less the maximum, which is exact, first
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s[16 * i + k] = fmaf(s[16 * i + k], ck[i], ev[i]) - m;
+            ck[i] = 1.f;
+            add[i] = kTopLog2;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float add = ev[i] + base;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
@@ -876,7 +892,7 @@ __global__ void __launch_bounds__(kAttnQThreads, 2)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int at = 16 * i + 8 * w + 2 * k;
-              const float2 x = fma2(make_float2(s[at], s[at + 1]), ck[i], add);
+              const float2 x = fma2(make_float2(s[at], s[at + 1]), ck[i], add[i]);
               const float2 z = make_float2(ex2(x.x), ex2(x.y));
               sum = add2(sum, z);
               const __half2 z16 = __floats2half2_rn(z.x, z.y);
