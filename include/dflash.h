@@ -454,7 +454,7 @@ DFLASH_API dflash_status dflash_block_attention_noalloc(int32_t batch, int32_t n
  *                 (dflash_kvq_check reads and clears it)
  * All pointers are device memory of the device that is current at the call
  * (any other pointer: DFLASH_E_INVALID_ARG): k8 and v8 16-byte aligned, k_exp
- * and v_exp 8-byte aligned, n_pages * n_kv_heads * 128 < 2^31. Codes and
+ * and v_exp 8-byte aligned, n_pages * n_kv_heads * 128 < 2^31.  Codes and
  * exponents of slots that nothing was written to may hold any bytes.
  * The exponent of a block of 16 slots is the smallest e in [-40, 40] with
  * max |x| <= 448 * 2^e over its rows, codes are rounded to nearest even.  A
@@ -521,11 +521,12 @@ DFLASH_API dflash_status dflash_kvq_read(const dflash_kvq_cache *cache, int32_t 
  * (status DFLASH_E_CAPACITY).  Rows past q_lens[b] are left as they were.  What
  * a row does not see (other rows' slots, whatever lies behind slot n) does not
  * enter its result, NaN included.
- * Scores and sums are in fp32 from bf16 q and the cache's exact values, but for elements of q
- * below 2^-10 of their row's largest, which are held to 2^-18 of that; a row of q with a
- * NaN, an infinity or a magnitude above 448 * 2^118 gets NaN.  A weight is held in fp16: off
- * by at most 2^-11 of itself or, in units of the largest p_s * 2^(exponent of slot s's block of
- * V) of the row, by 2^-36.  The result is rounded to bf16.
+ * Scores and sums are in fp32 from bf16 q and the cache's exact values, but for
+ * elements of q below 2^-10 of their row's largest, which are held to 2^-18 of
+ * that; a row of q with a NaN, an infinity or a magnitude above 448 * 2^118 gets
+ * NaN.  A weight is held in fp16: off by at most 2^-11 of itself or, in units of
+ * the row's largest p_s * 2^(exponent of slot s's block of V), by 2^-36.  The
+ * result is rounded to bf16.
  *   q_dev    [batch][block] rows of n_heads * 128 bf16, q_row_stride elements
  *            apart (>= n_heads * 128, a multiple of 8), 16-byte aligned
  *   out_dev  [batch][block][n_heads][128] bf16, 16-byte aligned
@@ -557,8 +558,9 @@ DFLASH_API int64_t dflash_kvq_attention_workspace(int32_t batch, int32_t n_heads
  *                          exp(q_jh . k_s / sqrt(128) - lse_jh)   (s seen by j)
  * for the slots s < n of the batch's sequences q; the rest is left as it was.
  * Arguments as in dflash_kvq_attention, whose lse is read (a row with lse -inf
- * adds nothing; q is held as there, the weights are in fp32).  For a drafted block call it after acceptance, with the
- * committed length and q_lens = the rows kept.
+ * adds nothing; q is held as there, the weights are in fp32).  For a drafted
+ * block call it after acceptance, with the committed length and q_lens = the
+ * rows kept.
  *   score_in_dev, score_out_dev [n_seqs][n_kv_heads][pages_per_seq * 128] float;
  *   may be the same array; score_in NULL reads as zero.  4-byte aligned. */
 DFLASH_API dflash_status dflash_kvq_score(
@@ -577,8 +579,8 @@ DFLASH_API dflash_status dflash_kvq_score(
  * released after).  Blocks take their exponents anew.  Sources are only read.  An
  * entry with dst_ids[b] == src_ids[b] is refused on the device
  * (DFLASH_E_DEVICE_CHECK, entry skipped); a destination that is another entry's source
- * or destination gives unspecified rows, scores and entries of kept in both (entries may stay
- * as they were); rows for unmapped destination pages are
+ * or destination gives unspecified rows, scores and entries of kept in both
+ * (entries may stay as they were); rows for unmapped destination pages are
  * dropped, source slots on unmapped pages read as zero (DFLASH_E_CAPACITY).
  *   score_dev    [n_seqs][n_kv_heads][pages_per_seq * 128]: row src_ids[b] is read,
  *                row dst_ids[b] gets the kept slots' scores, then zeros
@@ -586,8 +588,8 @@ DFLASH_API dflash_status dflash_kvq_score(
  *                row, -1 past min(n, budget)
  *   new_lens_dev [batch] int32 out: min(n, budget); may be kv_lens_dev, whose lengths are
  *                then updated in place
- * Apart from that the arrays written must not overlap one another, the ids, the lengths or
- * the page table (DFLASH_E_INVALID_ARG).
+ * Apart from that the arrays written must not overlap one another, the ids, the
+ * lengths or the page table (DFLASH_E_INVALID_ARG).
  *   max_keys     host bound on the lengths, for planning only (1..2^29)
  * budget 1..pages_per_seq * 128, window 0..budget. */
 DFLASH_API dflash_status dflash_kvq_evict(const dflash_kvq_cache *cache, int32_t batch,
