@@ -109,9 +109,9 @@ __device__ __forceinline__ bool kvq_entry(const KvqAttnK& p, int b, int& seq, in
 // tiles ahead of O^T.  (Warps 10 and 11 only complete a warpgroup, whose registers the softmax takes
 // over.)  A softmax warp none of whose rows is in use only takes part in the barriers.
 //
-// Measured: 32 sequences of one row over 24,000 to 32,769 slots (1.89 GB) 307 us, 6.2 TB/s; 8
+// Measured: 32 sequences of one row over 24,000 to 32,769 slots (1.89 GB) 309 us, 6.1 TB/s; 8
 // sequences of 16 rows over 16,400 slots (271 MB) 57 us, 4.8 TB/s; 1000 rows of 2 sequences
-// over 2500 to 5097 slots 214 us.
+// over 2500 to 5097 slots 216 us.
 // Tried and slower (8 sequences of 8 KV heads over 16,384 slots, 1 and 16 rows a sequence; kept form
 // 50 and 56 us): the conversion in rolled loops (81, 85), on eight warps instead of four (66, 76),
 // with the header's 16-bit operands instead of both halves of a register at once (56, 64); V in
