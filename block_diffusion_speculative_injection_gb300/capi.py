@@ -55,6 +55,14 @@ class DTree(ctypes.Structure):
     ]
 
 
+class _PagesStruct(ctypes.Structure):
+    _fields_ = [
+        ("page_table", ctypes.c_void_p), ("n_mapped", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+    ]
+
+
 class _KvqCacheStruct(ctypes.Structure):
     _fields_ = [
         ("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
@@ -114,6 +122,12 @@ _SIGS = {
                           _P, _P], _I),
     "dflash_kvq_evict": ([_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P], _I),
     "dflash_kvq_check": ([_P, _P], _I),
+    "dflash_pages_map": ([_P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "dflash_pages_release": ([_P, _I, _P, _P, _P], _I),
+    "dflash_status_check": ([_P, _P], _I),
+    "dflash_kvq_append_packed": ([_P, _I, _I, _P, _P, _P, _P, _P, _L, _L, _P], _I),
+    "dflash_prompt_attention": ([_I, _I, _I, _I, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P], _I),
+    "dflash_token_logprobs": ([_I, _I, _I, _P, _L, _P, _I, _P, _P, _P, _P, _P], _I),
     "dflash_plan_gemm": ([_I, _I, _I, _I, _I, _I, _P], _I),
     "dflash_plan_attention": ([_I, _I, _I, _I, _I, ctypes.c_int64, _I, _P], _I),
     "dflash_profile": ([_P, _I], _I),
@@ -614,6 +628,122 @@ def dflash_kvq_evict(cache: KvqCache, batch, src_ids, dst_ids, kv_lens, max_keys
 def dflash_kvq_check(cache: KvqCache, stream=None) -> None:
     """Waits for the stream, clears the cache's status word and raises if it was set."""
     _kvq_check(load().dflash_kvq_check(cache.ref, _kvq_stream(stream)), "dflash_kvq_check")
+
+
+# ---------------------------------------------------------------------------
+# packed batches of prompts
+# ---------------------------------------------------------------------------
+class Pages:
+    """Pages of a cache mapped on the GPU, over tensors the caller owns (and this
+    keeps alive): page_table [n_seqs][pages_per_seq], n_mapped [n_seqs], free_pages
+    [n_pages], n_free [1], status [1], all int32."""
+
+    def __init__(self, page_table, n_mapped, free_pages, n_free, status):
+        if page_table.dim() != 2 or free_pages.dim() != 1:
+            _kvq_refuse("page_table: need [n_seqs][pages], free_pages: [n_pages]")
+        _kvq_dense(page_table, "page_table", "i32", tuple(page_table.shape))
+        _kvq_dense(n_mapped, "n_mapped", "i32", (page_table.shape[0],))
+        _kvq_dense(free_pages, "free_pages", "i32", tuple(free_pages.shape))
+        _kvq_dense(n_free, "n_free", "i32", (1,))
+        _kvq_dense(status, "status", "i32", (1,))
+        self.tensors = (page_table, n_mapped, free_pages, n_free, status)
+        self.n_seqs, self.pages_per_seq = page_table.shape
+        self._struct = _PagesStruct(*[_ptr(t) for t in self.tensors], free_pages.shape[0],
+                                    self.n_seqs, self.pages_per_seq)
+        self.ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, n_pages, n_seqs, pages_per_seq, device="cuda", status=None):
+        """A pool of n_pages free pages, the lowest ids first, nothing mapped."""
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((n_seqs, pages_per_seq), -1, **i32), torch.zeros(n_seqs, **i32),
+                   torch.arange(n_pages - 1, -1, -1, **i32), torch.full((1,), n_pages, **i32),
+                   torch.zeros(1, **i32) if status is None else status)
+
+
+def dflash_pages_map(pages: Pages, batch, n_rows, seq_ids, start, counts, offsets, kv_lens,
+                     row_seq=None, row_pos=None, row_slot=None, stream=None) -> None:
+    """Maps pages for counts[b] rows behind start[b] slots of each sequence and
+    lays out the packed batch: offsets, lengths, and the rows' maps."""
+    one, row = (batch,), (n_rows,)
+    _kvq_check(load().dflash_pages_map(
+        pages.ref, batch, n_rows, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(start, "start", "i32", one), _kvq_dense(counts, "counts", "i32", one),
+        _kvq_dense(offsets, "offsets", "i32", (batch + 1,)),
+        _kvq_dense(kv_lens, "kv_lens", "i32", one), _kvq_dense(row_seq, "row_seq", "i32", row),
+        _kvq_dense(row_pos, "row_pos", "i32", row), _kvq_dense(row_slot, "row_slot", "i32", row),
+        _kvq_stream(stream)), "dflash_pages_map")
+
+
+def dflash_pages_release(pages: Pages, batch, seq_ids=None, keep=None, stream=None) -> None:
+    """Gives back the pages behind the first keep[b] slots (None: all pages)."""
+    one = (batch,)
+    _kvq_check(load().dflash_pages_release(
+        pages.ref, batch, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(keep, "keep", "i32", one), _kvq_stream(stream)), "dflash_pages_release")
+
+
+def dflash_status_check(status, stream=None) -> None:
+    """Waits for the stream, clears the status word and raises if it was set."""
+    _kvq_check(load().dflash_status_check(_kvq_dense(status, "status", "i32", (1,)),
+                                          _kvq_stream(stream)), "dflash_status_check")
+
+
+def _packed_rows(t, name: str, n_rows: int, heads: int) -> int:
+    """Elements between the rows of a bf16 [n_rows][heads][128] tensor whose rows
+    may be slices of wider ones."""
+    if t.dim() != 3:
+        _kvq_refuse(f"{name}: need bfloat16 of shape {(n_rows, heads, 128)}")
+    return _kvq_rows(t[None], name, 1, n_rows, heads)
+
+
+def dflash_kvq_append_packed(cache: KvqCache, batch, seq_ids, start, offsets, k, v,
+                             stream=None) -> None:
+    """Writes the packed bf16 rows k, v [n_rows][n_kv_heads][128] of each sequence to
+    slots start[b] on."""
+    one, heads, n_rows = (batch,), cache.n_kv_heads, k.shape[0]
+    _kvq_check(load().dflash_kvq_append_packed(
+        cache.ref, batch, n_rows, _kvq_dense(seq_ids, "seq_ids", "i32", one),
+        _kvq_dense(start, "start", "i32", one), _kvq_dense(offsets, "offsets", "i32", (batch + 1,)),
+        k.data_ptr(), v.data_ptr(), _packed_rows(k, "k", n_rows, heads),
+        _packed_rows(v, "v", n_rows, heads), _kvq_stream(stream)), "dflash_kvq_append_packed")
+
+
+def dflash_prompt_attention(batch, causal, offsets, q, k, v, out, lse=None, status=None,
+                            stream=None) -> None:
+    """Attention of a packed batch of prompts over themselves: q [n_rows][n_heads][128],
+    k, v [n_rows][n_kv_heads][128] (rows may be slices of wider ones), out of
+    q's shape, lse [n_rows][n_heads], status [1] int32 (zero at the start)."""
+    if q.dim() != 3 or k.dim() != 3:
+        _kvq_refuse("q, k: need [n_rows][heads][128]")
+    n_rows, heads, kv_heads = q.shape[0], q.shape[1], k.shape[1]
+    _kvq_check(load().dflash_prompt_attention(
+        batch, n_rows, heads, kv_heads, int(causal), _kvq_dense(offsets, "offsets", "i32", (batch + 1,)),
+        q.data_ptr(), _packed_rows(q, "q", n_rows, heads), k.data_ptr(),
+        _packed_rows(k, "k", n_rows, kv_heads), v.data_ptr(),
+        _packed_rows(v, "v", n_rows, kv_heads), _kvq_dense(out, "out", "bf16", (n_rows, heads, 128)),
+        _kvq_dense(lse, "lse", "f32", (n_rows, heads)), _kvq_dense(status, "status", "i32", (1,)),
+        _kvq_stream(stream)), "dflash_prompt_attention")
+
+
+def dflash_token_logprobs(logits, tokens, top=0, logp=None, entropy=None, top_ids=None,
+                          top_logp=None, stream=None) -> None:
+    """Log probabilities of tokens [rows] under logits [rows][vocab] (fp32 or bf16, rows
+    may be slices of wider ones), entropies [rows], and the `top` best ids with theirs."""
+    d = _KVQ_DTYPES or _kvq_dtypes()
+    if logits.dim() != 2 or logits.dtype not in d["f32"] + d["bf16"] or (
+            logits.shape[1] > 1 and logits.stride(1) != 1):
+        _kvq_refuse("logits: need float32 or bfloat16 [rows][vocab], each row contiguous")
+    rows, vocab = logits.shape
+    dtype = DFLASH_F32 if logits.dtype in d["f32"] else DFLASH_BF16
+    _kvq_check(load().dflash_token_logprobs(
+        rows, vocab, dtype, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+        _kvq_dense(tokens, "tokens", "i32", (rows,)), top, _kvq_dense(logp, "logp", "f32", (rows,)),
+        _kvq_dense(entropy, "entropy", "f32", (rows,)),
+        _kvq_dense(top_ids, "top_ids", "i32", (rows, top)),
+        _kvq_dense(top_logp, "top_logp", "f32", (rows, top)), _kvq_stream(stream)),
+        "dflash_token_logprobs")
 
 
 def dflash_debug_trace(ctx, dst=None) -> None:

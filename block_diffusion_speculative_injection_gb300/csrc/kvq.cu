@@ -7,6 +7,7 @@
 // codes by whole binades (lossless above the subnormal codes), and attention can
 // fold the exponents into its scores.
 #include "kvq.cuh"
+#include "packed.cuh"
 
 namespace dflash {
 
@@ -42,30 +43,54 @@ __device__ __forceinline__ uint2 code_row(const float* x, float s) {
 // its block's committed codes and new rows whole before it writes, so a block
 // has one writer.  Bound by memory: 2 B in and 1 B out per new element; 15,000 rows of
 // 8 heads (92 MB) take 21 us, 4.3 TB/s.
+//
+// Packed rows: `rows` in all, and n_blk units of 16 of them; the r rows of a sequence touch up
+// to floor(r / 16) + 2 blocks.
 // ---------------------------------------------------------------------------
 struct AppendK {
   KvqK c;
-  const int32_t *seq_ids, *start, *counts;
+  const int32_t *seq_ids, *start, *counts, *offsets;
   const bf16* in[2];
   long long stride[2];  // elements between rows
-  int batch, rows, n_blk;
+  int batch, rows;
+  long long n_blk;
 };
 
+template <bool kPacked>
 __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int kv = (int)(w & 1);
-  w >>= 1;
-  const int head = (int)(w % p.c.Hkv);
-  w /= p.c.Hkv;
-  const int blk = (int)(w % p.n_blk);
-  w /= p.n_blk;
-  if (w >= p.batch) return;
-  const int b = (int)w;
+  int b, blk, cnt;
+  long long row0;  // the sequence's first row
+  int head;
+  if (kPacked) {
+    packed_check(p.offsets, p.batch, p.rows, (long long)blockIdx.x * 128 + threadIdx.x,
+                 (long long)gridDim.x * 128, p.c.status);
+    w >>= 1;
+    head = (int)(w % p.c.Hkv);
+    w /= p.c.Hkv;
+    if (w >= p.n_blk) return;
+    b = packed_find(p.offsets, p.batch, kKvqSub, 2, w);
+    int first = 0;
+    if (b < 0 || !packed_rows(p.offsets, b, p.rows, first, cnt)) return;
+    blk = (int)(w - packed_base(p.offsets, b, kKvqSub, 2));
+    row0 = first;
+  } else {
+    w >>= 1;
+    head = (int)(w % p.c.Hkv);
+    w /= p.c.Hkv;
+    blk = (int)(w % p.n_blk);
+    w /= p.n_blk;
+    if (w >= p.batch) return;
+    b = (int)w;
+    cnt = p.counts ? p.counts[b] : p.rows;
+    row0 = (long long)b * p.rows;
+  }
   const int seq = kvq_seq(p.c, p.seq_ids, b);
-  const int s0 = p.start[b], cnt = p.counts ? p.counts[b] : p.rows;
+  const int s0 = p.start[b];
   if (seq < 0) return;
   if (s0 < 0 || cnt < 0 || cnt > p.rows) {
     set_dev_status(p.c.status, kDevCheck);
@@ -99,7 +124,7 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
       raw[i].x = c.x;
       raw[i].y = c.y;
     } else if (r < n_live) {
-      const long long row = (long long)b * p.rows + (slot0 + r - s0);
+      const long long row = row0 + (slot0 + r - s0);
       raw[i] = *reinterpret_cast<const uint4*>(in + row * stride + head * kKvqHd + col);
     }
   }
@@ -662,6 +687,20 @@ static bool kvq_overlap(const KvqRange& a, const KvqRange& b) {
   return x < y ? y - x < (uint64_t)a.n * 4 : x - y < (uint64_t)b.n * 4;
 }
 
+static void append_fill(AppendK* p, const dflash_kvq_cache* cache, int batch, int rows,
+                        const int32_t* seq_ids, const int32_t* start, const void* k, const void* v,
+                        int64_t k_stride, int64_t v_stride) {
+  p->c = kvq_device_view(cache);
+  p->seq_ids = seq_ids;
+  p->start = start;
+  p->in[0] = static_cast<const bf16*>(k);
+  p->in[1] = static_cast<const bf16*>(v);
+  p->stride[0] = k_stride;
+  p->stride[1] = v_stride;
+  p->batch = batch;
+  p->rows = rows;
+}
+
 static bool row_stride_ok(int64_t stride, int heads) {
   return stride >= (int64_t)heads * kKvqHd && stride % 8 == 0 && stride < ((int64_t)1 << 31);
 }
@@ -689,17 +728,36 @@ dflash_status dflash_kvq_append(const dflash_kvq_cache* cache, int32_t batch, in
   const void* const ptrs[] = {seq_ids, start, counts, k, v};
   DF_TRY(kvq_cache_ptrs_ok(cache));
   DF_TRY(kvq_ptrs_ok(ptrs, 5));
-  p.c = kvq_device_view(cache);
-  p.seq_ids = seq_ids;
-  p.start = start;
+  append_fill(&p, cache, batch, rows, seq_ids, start, k, v, k_row_stride, v_row_stride);
   p.counts = counts;
-  p.in[0] = static_cast<const bf16*>(k);
-  p.in[1] = static_cast<const bf16*>(v);
-  p.stride[0] = k_row_stride;
-  p.stride[1] = v_row_stride;
-  p.batch = batch;
-  p.rows = rows;
-  if (launch_k(true, kvq_append_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0,
+  p.offsets = nullptr;
+  if (launch_k(true, kvq_append_kernel<false>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0,
+               (cudaStream_t)stream, p) != cudaSuccess)
+    return DFLASH_E_CUDA;
+  return DFLASH_OK;
+}
+
+dflash_status dflash_kvq_append_packed(const dflash_kvq_cache* cache, int32_t batch, int32_t n_rows,
+                                       const int32_t* seq_ids, const int32_t* start,
+                                       const int32_t* offsets, const void* k, const void* v,
+                                       int64_t k_row_stride, int64_t v_row_stride,
+                                       dflash_stream_t stream) {
+  if (!kvq_cache_ok(cache) || batch < 1 || n_rows < 1 || !start || !offsets || !k || !v ||
+      !kvq_aligned(k, 16) || !kvq_aligned(v, 16) || !row_stride_ok(k_row_stride, cache->n_kv_heads) ||
+      !row_stride_ok(v_row_stride, cache->n_kv_heads) || n_rows >= (1 << 30) || batch >= (1 << 26) ||
+      !kvq_ints_aligned({seq_ids, start, offsets}))
+    return DFLASH_E_INVALID_ARG;
+  AppendK p;
+  p.n_blk = packed_units(n_rows, batch, kKvqSub, 2);
+  const int64_t warps = p.n_blk * cache->n_kv_heads * 2;
+  if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
+  const void* const ptrs[] = {seq_ids, start, offsets, k, v};
+  DF_TRY(kvq_cache_ptrs_ok(cache));
+  DF_TRY(kvq_ptrs_ok(ptrs, 5));
+  append_fill(&p, cache, batch, n_rows, seq_ids, start, k, v, k_row_stride, v_row_stride);
+  p.counts = nullptr;
+  p.offsets = offsets;
+  if (launch_k(true, kvq_append_kernel<true>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0,
                (cudaStream_t)stream, p) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;
@@ -794,15 +852,16 @@ dflash_status dflash_kvq_evict(const dflash_kvq_cache* cache, int32_t batch, con
   return DFLASH_OK;
 }
 
-dflash_status dflash_kvq_check(const dflash_kvq_cache* cache, dflash_stream_t stream) {
-  if (!kvq_cache_ok(cache)) return DFLASH_E_INVALID_ARG;
-  DF_TRY(kvq_cache_ptrs_ok(cache));
+dflash_status dflash_status_check(int32_t* status_dev, dflash_stream_t stream) {
+  if (!status_dev || !kvq_aligned(status_dev, 4)) return DFLASH_E_INVALID_ARG;
+  const void* const ptrs[] = {status_dev};
+  DF_TRY(kvq_ptrs_ok(ptrs, 1));
   cudaStream_t st = (cudaStream_t)stream;
   int32_t s = 0;
-  if (cudaMemcpyAsync(&s, cache->status_dev, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+  if (cudaMemcpyAsync(&s, status_dev, 4, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
       cudaStreamSynchronize(st) != cudaSuccess)
     return DFLASH_E_CUDA;
-  if (s != 0 && (cudaMemsetAsync(cache->status_dev, 0, 4, st) != cudaSuccess ||
+  if (s != 0 && (cudaMemsetAsync(status_dev, 0, 4, st) != cudaSuccess ||
                  cudaStreamSynchronize(st) != cudaSuccess))
     return DFLASH_E_CUDA;
   switch (s) {
@@ -811,6 +870,12 @@ dflash_status dflash_kvq_check(const dflash_kvq_cache* cache, dflash_stream_t st
     case kDevTimeout: return DFLASH_E_TIMEOUT;
     default: return DFLASH_E_DEVICE_CHECK;
   }
+}
+
+dflash_status dflash_kvq_check(const dflash_kvq_cache* cache, dflash_stream_t stream) {
+  if (!kvq_cache_ok(cache)) return DFLASH_E_INVALID_ARG;
+  DF_TRY(kvq_cache_ptrs_ok(cache));
+  return dflash_status_check(cache->status_dev, stream);
 }
 
 }  // extern "C"

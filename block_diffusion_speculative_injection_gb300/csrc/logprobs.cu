@@ -1,0 +1,399 @@
+// Log probabilities of given tokens, with the entropy of their distributions and the best
+// alternatives (dflash_token_logprobs), from one read of the logits.
+//
+// With m the row's maximum and d_i = x_i - m,
+//   S = sum e^d_i,  T = sum d_i e^d_i,
+//   log p_t = d_t - log S,  entropy = -sum p_i log p_i = log S - T / S.
+// S and T of parts of a row with maxima m1 <= m join as
+//   S += f S1,  T += f (T1 + (m1 - m) S1),  f = e^(m1 - m).
+#include <cmath>
+
+#include "kvq.cuh"
+
+namespace dflash {
+
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpVals = 16;                       // values a thread reads at once
+constexpr int kLpStep = kLpThreads * kLpVals;     // ids of an iteration of a CTA
+constexpr int kLpTop = 32;                        // most alternatives
+constexpr int kLpKeys = kLpStep + kLpStep / 4;    // candidates a CTA holds
+constexpr int kLpCluster = 8;                     // most CTAs a row
+static_assert(kLpKeys / kLpThreads < 32, "a thread's count in five bits");
+constexpr float kLpLog2e = 1.4426950408889634f;
+// d_i are cut off here, where e^d_i is zero in fp32, so that a logit of -inf adds 0 and not
+// 0 * inf to T
+constexpr float kLpFloor = -200.f;
+
+struct LogpK {
+  const void* logits;
+  long long stride;  // elements between rows
+  const int32_t* tokens;
+  float *logp, *entropy, *top_logp;
+  int32_t* top_ids;
+  int vocab, top;
+};
+
+// Sums of a part of a row: maximum, S, T.
+struct RowSum {
+  float m, s, t;
+};
+// max that passes NaN on
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lp_exp(float d) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * kLpLog2e));
+  return y;
+}
+__device__ __forceinline__ void raise(RowSum& a, float m) {
+  // (from -inf nothing has been added yet; the floor also keeps inf - inf out)
+  const float d = fmaxf(a.m - m, kLpFloor), f = lp_exp(d);
+  a.t = f * (a.t + d * a.s);
+  a.s *= f;
+  a.m = m;
+}
+__device__ __forceinline__ RowSum join(RowSum a, RowSum b) {
+  const float m = max_nan(a.m, b.m);
+  raise(a, m);
+  raise(b, m);
+  a.s += b.s;
+  a.t += b.t;
+  return a;
+}
+
+// Candidates as numbers that order like them: the larger value first, then the lower id.  0 is
+// below every logit but -inf and NaN, which are no alternatives.
+__device__ __forceinline__ uint64_t lp_key(float x, int id) {
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 equals 0
+  const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return ((uint64_t)o << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ float lp_key_value(uint64_t k) {
+  const uint32_t o = (uint32_t)(k >> 32);
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+// the values of 16 bytes
+template <typename T>
+struct LpVec;
+template <>
+struct LpVec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void get(uint4 r, float* x) {
+    x[0] = __uint_as_float(r.x);
+    x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z);
+    x[3] = __uint_as_float(r.w);
+  }
+};
+template <>
+struct LpVec<bf16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void get(uint4 r, float* x) { bf16x8_to_f(r, x); }
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+struct LpShared {
+  uint64_t keys[kLpKeys];
+  uint64_t best[kLpTop];     // the part's alternatives in order, 0 behind the last
+  uint64_t all[kLpCluster * kLpTop];
+  RowSum part[kLpWarps];
+  RowSum sum;                // the part's sums
+  float group[kLpThreads / 8];
+  float floor;               // values up to here are no candidates any more
+  int count;
+};
+
+// The n best of c keys (all different but for zeros), in order, to out[0 .. n), zeros behind the last;
+// whole CTA.  Up to a few hundred each is ranked by counting; of more, first the n-th best is
+// found by its bits.
+__device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out) {
+  const int tid = threadIdx.x;
+  uint64_t least = 1;
+  if (c > 2 * kLpThreads) {
+    uint64_t t = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const uint64_t next = t | (1ull << bit);
+      int mine = 0;
+      for (int i = tid; i < c; i += kLpThreads) mine += keys[i] >= next;
+      int sum = 0;
+      for (int half = 1; half <= 16; half <<= 1)  // (a thread counts 20 at most)
+        sum += half * __syncthreads_count((mine / half) & 1);
+      if (sum >= n) t = next;
+    }
+    least = max(t, (uint64_t)1);
+  }
+  if (tid < n) out[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < c; i += kLpThreads) {
+    const uint64_t k = keys[i];
+    if (k < least) continue;
+    int rank = 0;
+    for (int j = 0; j < c; ++j) rank += keys[j] > k;
+    if (rank < n) out[rank] = k;
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK p, const int C) {
+  pdl_wait();
+  constexpr int E = LpVec<T>::kN, U = kLpVals / E;
+  extern __shared__ __align__(16) uint8_t lp_smem[];
+  LpShared& sh = *reinterpret_cast<LpShared*>(lp_smem);
+  const int row = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int tok = p.tokens ? p.tokens[row] : 0;
+  if (tok < 0) return;  // (the whole cluster) a row that is not in use
+  const T* const x = static_cast<const T*>(p.logits) + (long long)row * p.stride;
+  // the row: up to E - 1 ids before the first 16-byte boundary, whole vectors, up to E - 1 behind
+  const int head = min(p.vocab, (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+  const int vecs = (p.vocab - head) / E, tail0 = head + vecs * E;
+  const int v0 = (int)((long long)vecs * rank / C), v1 = (int)((long long)vecs * (rank + 1) / C);
+  const uint4* const vec = reinterpret_cast<const uint4*>(x + head);
+  float x_tok = 0.f;
+  if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
+  if (tid == 0) {
+    sh.count = 0;
+    sh.floor = -INFINITY;
+  }
+  RowSum a = {-INFINITY, 0.f, 0.f};
+  auto add = [&](float v) {
+    if (v == -INFINITY) return;
+    const float m = max_nan(a.m, v);
+    if (!(m == a.m)) raise(a, m);
+    const float d = fmaxf(v - a.m, kLpFloor), e = lp_exp(d);
+    a.s += e;
+    a.t += e * d;
+  };
+  auto keep = [&](float v, int id) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kLpKeys) sh.keys[at] = lp_key(v, id);
+  };
+  __syncthreads();
+  // the ids before the vectors: candidates with the first ones
+  if (rank == 0 && tid < head) {
+    const float v = ld_f(x + tid);
+    add(v);
+    if (p.top && v > -INFINITY) keep(v, tid);
+  }
+  bool open = p.top > 0;  // fewer than `top` candidates so far
+  float floor = INFINITY;
+  int next_cut = 0;
+  int it = 0;
+  for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
+    uint4 raw[U];
+    float val[kLpVals];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kLpThreads + tid;
+      if (i < v1) {
+        raw[u] = ld_stream(vec + i);
+        LpVec<T>::get(raw[u], val + u * E);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) val[u * E + e] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kLpVals; ++e) mx = max_nan(mx, val[e]);
+    const float m = max_nan(a.m, mx);
+    if (!(m == a.m)) raise(a, m);
+    if (m != -INFINITY) {
+#pragma unroll
+      for (int e = 0; e < kLpVals; ++e) {
+        const float d = fmaxf(val[e] - m, kLpFloor), w = lp_exp(d);
+        a.s += w;
+        a.t += w * d;
+      }
+    }
+    if (open) {
+      // While there are fewer than `top` candidates: 32 groups' maxima are 32 different values,
+      // so the least of them is no more than the 32nd best of this iteration.
+      float g = mx != mx ? INFINITY : mx;  // (a row with a NaN has no alternatives' values anyway)
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if ((lane & 7) == 0) sh.group[tid >> 3] = g;
+      __syncthreads();
+      float low = sh.group[lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      if (low == INFINITY) low = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kLpVals; ++e)
+        if (val[e] > -INFINITY && val[e] >= low)
+          keep(val[e], head + (i0 + e / E * kLpThreads + tid) * E + e % E);
+    } else if (mx > floor) {
+      // ids rise with the iterations: what only equals the floor comes behind those that made it
+#pragma unroll
+      for (int e = 0; e < kLpVals; ++e)
+        if (val[e] > floor) keep(val[e], head + (i0 + e / E * kLpThreads + tid) * E + e % E);
+    }
+    if (p.top && it >= next_cut) {  // after the iterations 0, 1, 3, 7, ..
+      next_cut = open ? it + 1 : 2 * it + 1;
+      __syncthreads();
+      const int c = min(sh.count, kLpKeys);
+      lp_select(sh.keys, c, p.top, sh.best);
+      const bool over = sh.count > kLpKeys;
+      __syncthreads();
+      if (!over) {
+        if (tid < p.top) sh.keys[tid] = sh.best[tid];
+        if (tid == 0) {
+          int n = 0;
+          while (n < p.top && sh.best[n]) ++n;
+          sh.count = n;
+        }
+        open = sh.best[p.top - 1] == 0;
+        if (!open) floor = lp_key_value(sh.best[p.top - 1]);
+      }
+      __syncthreads();
+    }
+  }
+  // the ids behind the vectors
+  if (rank == C - 1 && tail0 + tid < p.vocab) {
+    const float v = ld_f(x + tail0 + tid);
+    add(v);
+    if (p.top && v > -INFINITY && (open || v > floor)) keep(v, tail0 + tid);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    RowSum b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+    a = join(a, b);
+  }
+  if (lane == 0) sh.part[warp] = a;
+  __syncthreads();
+  if (p.top) {
+    if (sh.count <= kLpKeys) {
+      lp_select(sh.keys, sh.count, p.top, sh.best);
+    } else {
+      // More candidates than there is room for (logits that rise with the id): `top` times the
+      // best one below the last, over the whole part.
+      const int f0 = rank == 0 ? 0 : head + v0 * E, f1 = rank == C - 1 ? p.vocab : head + v1 * E;
+      uint64_t last = ~0ull;
+      for (int k = 0; k < p.top; ++k) {
+        uint64_t b = 0;
+        for (int i = f0 + tid; i < f1; i += kLpThreads) {
+          const float v = ld_f(x + i);
+          const uint64_t key = v > -INFINITY ? lp_key(v, i) : 0;
+          if (key < last && key > b) b = key;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+        if (lane == 0) sh.all[warp] = b;
+        __syncthreads();
+        b = 0;
+        for (int w = 0; w < kLpWarps; ++w) b = max(b, sh.all[w]);
+        if (tid == 0) sh.best[k] = b;
+        last = b;
+        __syncthreads();
+      }
+    }
+  }
+  if (tid == 0) {
+    RowSum r = sh.part[0];
+    for (int w = 1; w < kLpWarps; ++w) r = join(r, sh.part[w]);
+    sh.sum = r;
+  }
+  RowSum r;
+  const uint64_t* best = sh.best;
+  if (C > 1) {
+    cluster_sync();
+    if (rank == 0) {
+      for (int i = tid; i < C * p.top; i += kLpThreads) {
+        const uint32_t at = map_peer(smem_u32(&sh.best[i % p.top]), i / p.top);
+        uint64_t k;
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(at) : "memory");
+        sh.all[i] = k;
+      }
+      if (tid == 0) {
+        r = sh.sum;
+        for (int c = 1; c < C; ++c) {
+          const uint32_t at = map_peer(smem_u32(&sh.sum), c);
+          RowSum b;
+          b.m = ld_peer_f32(at);
+          b.s = ld_peer_f32(at + 4);
+          b.t = ld_peer_f32(at + 8);
+          r = join(r, b);
+        }
+        sh.part[0] = r;
+      }
+    }
+    cluster_sync();  // the others' shared memory has been read
+    if (rank != 0) return;
+    r = sh.part[0];
+    if (p.top) {
+      lp_select(sh.all, C * p.top, p.top, sh.keys);
+      best = sh.keys;
+    }
+  } else {
+    __syncthreads();
+    r = sh.sum;
+  }
+  const bool mass = r.m != -INFINITY;
+  const float log_s = logf(r.s);
+  if (tid == 0) {
+    if (p.logp && p.tokens)
+      p.logp[row] = tok >= p.vocab || !mass ? -INFINITY : (x_tok - r.m) - log_s;
+    if (p.entropy) p.entropy[row] = mass ? log_s - r.t / r.s : 0.f;
+  }
+  if (tid < p.top) {
+    const uint64_t k = best[tid];
+    const long long at = (long long)row * p.top + tid;
+    p.top_ids[at] = k ? (int)~(uint32_t)k : -1;
+    p.top_logp[at] = k ? (lp_key_value(k) - r.m) - log_s : -INFINITY;
+  }
+}
+
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, const void* logits,
+                                    int64_t row_stride, const int32_t* tokens, int32_t top,
+                                    float* logp, float* entropy, int32_t* top_ids, float* top_logp,
+                                    dflash_stream_t stream) {
+  if (rows < 1 || rows >= (1 << 27) || vocab < 1 || vocab >= (1 << 30) ||
+      (dtype != DFLASH_F32 && dtype != DFLASH_BF16) || !logits || row_stride < vocab ||
+      row_stride >= ((int64_t)1 << 40) || top < 0 || top > kLpTop || (logp && !tokens) ||
+      (top > 0 && (!top_ids || !top_logp)) || (!logp && !entropy && top == 0) ||
+      !kvq_aligned(logits, dtype == DFLASH_F32 ? 4 : 2) || !kvq_aligned(logp, 4) ||
+      !kvq_aligned(entropy, 4) || !kvq_aligned(top_logp, 4) || !kvq_ints_aligned({tokens, top_ids}))
+    return DFLASH_E_INVALID_ARG;
+  const void* const ptrs[] = {logits, tokens, logp, entropy, top_ids, top_logp};
+  DF_TRY(kvq_ptrs_ok(ptrs, 6));
+  LogpK p;
+  p.logits = logits;
+  p.stride = row_stride;
+  p.tokens = tokens;
+  p.logp = logp;
+  p.entropy = entropy;
+  p.top_ids = top_ids;
+  p.top_logp = top_logp;
+  p.vocab = vocab;
+  p.top = top;
+  int C = 1;
+  while (C < kLpCluster && (int64_t)rows * C * 2 <= 2 * kvq_sms() && vocab > C * kLpStep) C *= 2;
+  const auto kernel = dtype == DFLASH_F32 ? token_logprobs_kernel<float> : token_logprobs_kernel<bf16>;
+  if (launch_k_cluster(true, dim3(C, 1, 1), kernel, dim3((unsigned)(rows * C)), dim3(kLpThreads),
+                       sizeof(LpShared), (cudaStream_t)stream, p, C) != cudaSuccess)
+    return DFLASH_E_CUDA;
+  return DFLASH_OK;
+}
+
+}  // extern "C"

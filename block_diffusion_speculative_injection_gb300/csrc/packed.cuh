@@ -1,0 +1,59 @@
+// Packed batches: sequence b's rows are offsets[b] .. offsets[b + 1] - 1 of one run of n_rows
+// rows.  The lengths are known on the device only, so launches are sized from n_rows and
+// batch, and a CTA or warp finds the sequence its work lies in.
+#pragma once
+
+#include "internal.cuh"
+
+namespace dflash {
+
+// Work units of `unit` rows: sequence b has the units from offsets[b] / unit + extra * b on, up
+// to the next sequence's.  floor(x + y) >= floor(x) + floor(y), so that leaves it
+// floor(rows / unit) + extra or more, and all of them lie below n_rows / unit + extra * batch.
+inline int64_t packed_units(int64_t n_rows, int64_t batch, int unit, int extra) {
+  return n_rows / unit + extra * batch;
+}
+
+// First unit of sequence b
+__device__ __forceinline__ long long packed_base(const int32_t* offsets, int b, int unit, int extra) {
+  return offsets[b] / unit + (long long)extra * b;
+}
+
+// The sequence that unit u lies in (the last b with base <= u), or -1 before the first: a whole
+// warp searches, 32 probes at a time, so a batch of up to 32 takes one load.
+__device__ __forceinline__ int packed_find(const int32_t* offsets, int batch, int unit, int extra,
+                                           long long u) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, end = batch;
+  while (true) {
+    const int step = (end - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < end && packed_base(offsets, at, unit, extra) <= u;
+    const int n = __popc(__ballot_sync(0xffffffffu, below));
+    if (n == 0) return -1;
+    lo += (n - 1) * step;
+    if (step == 1) return lo;
+    end = min(end, lo + step);
+  }
+}
+
+// Whether sequence b's rows lie in [0, n_rows) in order; its first row and count.
+__device__ __forceinline__ bool packed_rows(const int32_t* offsets, int b, int n_rows, int& first,
+                                            int& count) {
+  first = offsets[b];
+  const int end = offsets[b + 1];
+  count = end - first;
+  return first >= 0 && first <= end && end <= n_rows;
+}
+
+// Every thread of the launch looks at the entries i, i + all, ...: a list that is not in order,
+// or leaves [0, n_rows], sets the status even where no unit falls into the bad entry.
+__device__ __forceinline__ void packed_check(const int32_t* offsets, int batch, int n_rows,
+                                             long long i, long long all, int32_t* status) {
+  for (; i < batch; i += all) {
+    int first, count;
+    if (!packed_rows(offsets, (int)i, n_rows, first, count)) set_dev_status(status, kDevCheck);
+  }
+}
+
+}  // namespace dflash
