@@ -8,6 +8,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "attn_util.cuh"
 #include "kvq.cuh"
 
 namespace dflash {
@@ -153,20 +154,8 @@ constexpr float kTopLog2 = 11.f, kLazyLog2 = 4.f;
 // sum with an exponent, 2^-4 each at most, keep z below 2^15.2.
 constexpr float kFarLog2 = 1048576.f;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 1 / l to one or two units in the last place (l is a sum of weights, or NaN), and
-// log2 within 2^-22
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // log of a softmax sum l of z (l 2^-11 is at most the row's slots, and 1 where one has all the
-// weight: log2 is most exact there)
+// weight: log2, within 2^-22, is most exact there)
 __device__ __forceinline__ float lse_of(float m, float l) {
   return (m + __log2f(l * (1.f / 2048))) * kLn2;
 }
@@ -214,38 +203,9 @@ __device__ __forceinline__ void clean_v(uint8_t* sm, int st, int cw, int lane, i
     }
   }
 }
-// Registers a thread of this warpgroup gives back or takes over (all its warps together).
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 // bits below n set (n clamped to 0..32)
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u));
-}
-
-// (a0, a1) * b + c and (a0, a1) + (b0, b1) in one instruction each
-__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
 }
 
 // block position (within the CTA's) of one of its 64 rows
@@ -374,16 +334,6 @@ __device__ __forceinline__ void convert_q(uint4* q_raw, int warp, int lane, uint
   }
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b));
-  return r;
-}
-
 // Rows of the q tile from block position j0 on that see block slot i (r rows in the
 // sequence), a bit each.
 __device__ __forceinline__ uint64_t score_rows_seeing(const KvqAttnK& p, int b, int i, int j0, int r) {
@@ -404,47 +354,6 @@ __device__ __forceinline__ uint64_t score_rows_seeing(const KvqAttnK& p, int b, 
 struct KvqMaps {
   CUtensorMap k, v;
 };
-
-// Bounded wait of a whole warp (every lane polls, so every lane has the
-// barrier's ordering): gives up after about 2 s, like mbar_wait.  A poll may suspend
-// the warp for up to 20 us (a hint), so a waiting warp leaves its issue slots to
-// the others, and the clock is read only after such a poll has failed.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if ((i & 15u) == 0) {
-      const uint64_t now = global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > 2000000000ull) break;
-    }
-  }
-  set_dev_status(status, kDevTimeout);
-  return false;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return warp_wait(smem_u32(bar), parity, status);
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// one lane of a converged warp, the same one every time
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 
 __global__ void __launch_bounds__(kAttnQThreads, 2)
     kvq_attn_kernel(const __grid_constant__ KvqMaps maps, const KvqAttnK p) {
