@@ -107,11 +107,11 @@ def logprobs(x, token, top):
     if alive.size == 0:
         return -np.inf, 0.0, [-1] * top, [-np.inf] * top
     m = x[alive].max()
-    lse = m + math.log(np.exp(x[alive] - m).sum())
-    lp = x[alive] - lse
+    log_s = math.log(np.exp(x[alive] - m).sum())
+    lp = (x[alive] - m) - log_s  # (m + log_s would round log_s away beside a huge m)
     entropy = float(-(np.exp(lp) * lp).sum())
     order = alive[np.lexsort((alive, -x[alive]))][:top]
     ids = [int(i) for i in order] + [-1] * (top - order.size)
-    vals = [float(x[i] - lse) for i in order] + [-np.inf] * (top - order.size)
-    mine = x[token] - lse if 0 <= token < x.size else -np.inf
+    vals = [float((x[i] - m) - log_s) for i in order] + [-np.inf] * (top - order.size)
+    mine = (x[token] - m) - log_s if 0 <= token < x.size else -np.inf
     return mine, entropy, ids, vals
