@@ -32,7 +32,8 @@ template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// (a0, a1) * b + c, (a0, a1) + (b0, b1) and (a0, a1) * b in one instruction each
+// (a0, a1) * b + c (b, c scalars or pairs), (a0, a1) + (b0, b1) and (a0, a1) * b in one instruction
+// each
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
   float2 r;
   asm("{\n\t.reg .b64 x, y, z;\n\t"
@@ -40,6 +41,15 @@ __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
       "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

@@ -8,17 +8,17 @@
 //   S += f S1,  T += f (T1 + (m1 - m) S1),  f = e^(m1 - m).
 #include <cmath>
 
+#include "attn_util.cuh"
 #include "kvq.cuh"
 
 namespace dflash {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpVals = 16;                       // values a thread reads at once
-constexpr int kLpStep = kLpThreads * kLpVals;     // ids of an iteration of a CTA
+constexpr int kLpStep = kLpThreads * 16;          // ids of an iteration of a CTA
 constexpr int kLpTop = 32;                        // most alternatives
-constexpr int kLpKeys = kLpStep + kLpStep / 4;    // candidates a CTA holds
+constexpr int kLpKeys = 768;                      // candidates a CTA holds
 constexpr int kLpCluster = 8;                     // most CTAs a row
-static_assert(kLpKeys / kLpThreads < 32, "a thread's count in five bits");
+static_assert(kLpKeys / kLpThreads < 4, "a thread's count in two bits");
 constexpr float kLpLog2e = 1.4426950408889634f;
 // d_i are cut off here, where e^d_i is zero in fp32, so that a logit of -inf adds 0 and not
 // 0 * inf to T
@@ -43,11 +43,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float lp_exp(float d) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * kLpLog2e));
-  return y;
-}
+__device__ __forceinline__ float lp_exp(float d) { return ex2(d * kLpLog2e); }
 __device__ __forceinline__ void raise(RowSum& a, float m) {
   // (from -inf nothing has been added yet; the floor also keeps inf - inf out)
   const float d = fmaxf(a.m - m, kLpFloor), f = lp_exp(d);
@@ -76,23 +72,37 @@ __device__ __forceinline__ float lp_key_value(uint64_t k) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// the values of 16 bytes
+// 16 bytes of logits: the values, the largest (NaN passes), and a word of -inf
 template <typename T>
 struct LpVec;
 template <>
 struct LpVec<float> {
-  static constexpr int kN = 4;
+  static constexpr int kN = 4, kAtOnce = 4, kCtas = 4;  // values; vectors a thread reads at once
+  static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void get(uint4 r, float* x) {
     x[0] = __uint_as_float(r.x);
     x[1] = __uint_as_float(r.y);
     x[2] = __uint_as_float(r.z);
     x[3] = __uint_as_float(r.w);
   }
+  static __device__ __forceinline__ float top(uint4 r) {
+    return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
+                   max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+  }
 };
 template <>
 struct LpVec<bf16> {
-  static constexpr int kN = 8;
+  static constexpr int kN = 8, kAtOnce = 2, kCtas = 5;
+  static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ __forceinline__ void get(uint4 r, float* x) { bf16x8_to_f(r, x); }
+  static __device__ __forceinline__ __nv_bfloat162 pair(const uint32_t& w) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+  }
+  static __device__ __forceinline__ float top(uint4 r) {
+    const __nv_bfloat162 m =
+        __hmax2_nan(__hmax2_nan(pair(r.x), pair(r.y)), __hmax2_nan(pair(r.z), pair(r.w)));
+    return max_nan(__low2float(m), __high2float(m));
+  }
 };
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
@@ -107,10 +117,10 @@ struct LpShared {
   uint64_t keys[kLpKeys];
   uint64_t best[kLpTop];     // the part's alternatives in order, 0 behind the last
   uint64_t all[kLpCluster * kLpTop];
+  uint64_t warp_best[2][kLpWarps];
   RowSum part[kLpWarps];
   RowSum sum;                // the part's sums
   float group[kLpThreads / 8];
-  float floor;               // values up to here are no candidates any more
   int count;
 };
 
@@ -120,15 +130,14 @@ struct LpShared {
 __device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out) {
   const int tid = threadIdx.x;
   uint64_t least = 1;
-  if (c > 2 * kLpThreads) {
+  if (c > kLpThreads) {
     uint64_t t = 0;
+#pragma unroll 1
     for (int bit = 63; bit >= 0; --bit) {
       const uint64_t next = t | (1ull << bit);
       int mine = 0;
       for (int i = tid; i < c; i += kLpThreads) mine += keys[i] >= next;
-      int sum = 0;
-      for (int half = 1; half <= 16; half <<= 1)  // (a thread counts 20 at most)
-        sum += half * __syncthreads_count((mine / half) & 1);
+      const int sum = __syncthreads_count(mine & 1) + 2 * __syncthreads_count(mine >> 1);
       if (sum >= n) t = next;
     }
     least = max(t, (uint64_t)1);
@@ -139,16 +148,29 @@ __device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out) {
     const uint64_t k = keys[i];
     if (k < least) continue;
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < c; ++j) rank += keys[j] > k;
     if (rank < n) out[rank] = k;
   }
   __syncthreads();
 }
 
+// largest of the threads' keys, in every thread; two calls in a row use different buffers
+__device__ __forceinline__ uint64_t lp_block_max(uint64_t b, uint64_t* buffer) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+  if ((threadIdx.x & 31) == 0) buffer[threadIdx.x >> 5] = b;
+  __syncthreads();
+  b = buffer[0];
+#pragma unroll
+  for (int w = 1; w < kLpWarps; ++w) b = max(b, buffer[w]);
+  return b;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK p, const int C) {
+__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_kernel(const LogpK p, const int C) {
   pdl_wait();
-  constexpr int E = LpVec<T>::kN, U = kLpVals / E;
+  constexpr int E = LpVec<T>::kN, U = LpVec<T>::kAtOnce;
   extern __shared__ __align__(16) uint8_t lp_smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(lp_smem);
   const int row = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
@@ -163,10 +185,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK 
   const uint4* const vec = reinterpret_cast<const uint4*>(x + head);
   float x_tok = 0.f;
   if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
-  if (tid == 0) {
-    sh.count = 0;
-    sh.floor = -INFINITY;
-  }
+  if (tid == 0) sh.count = 0;
   RowSum a = {-INFINITY, 0.f, 0.f};
   auto add = [&](float v) {
     if (v == -INFINITY) return;
@@ -188,72 +207,120 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK 
     if (p.top && v > -INFINITY) keep(v, tid);
   }
   bool open = p.top > 0;  // fewer than `top` candidates so far
+  bool lost = false;      // more candidates than there was room for
   float floor = INFINITY;
   int next_cut = 0;
   int it = 0;
-  for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
-    uint4 raw[U];
-    float val[kLpVals];
-    float mx = -INFINITY;
+  uint4 next[U];
+  auto fetch = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * kLpThreads + tid;
-      if (i < v1) {
-        raw[u] = ld_stream(vec + i);
-        LpVec<T>::get(raw[u], val + u * E);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) val[u * E + e] = -INFINITY;
-      }
+      next[u] = i < v1 ? ld_stream(vec + i)
+                       : make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
     }
+  };
+  fetch(v0);
+#pragma unroll 1
+  for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
+    uint4 now[U];
 #pragma unroll
-    for (int e = 0; e < kLpVals; ++e) mx = max_nan(mx, val[e]);
+    for (int u = 0; u < U; ++u) now[u] = next[u];
+    if (i0 + kLpThreads * U < v1) fetch(i0 + kLpThreads * U);
+    // calls f(value, id) for each of this thread's values
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float v[E];
+        LpVec<T>::get(now[u], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f(v[e], head + (i0 + u * kLpThreads + tid) * E + e);
+      }
+    };
+    float mx = LpVec<T>::top(now[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) mx = max_nan(mx, LpVec<T>::top(now[u]));
     const float m = max_nan(a.m, mx);
     if (!(m == a.m)) raise(a, m);
     if (m != -INFINITY) {
+      float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
+      const float2 minus_m = make_float2(-m, -m);
 #pragma unroll
-      for (int e = 0; e < kLpVals; ++e) {
-        const float d = fmaxf(val[e] - m, kLpFloor), w = lp_exp(d);
-        a.s += w;
-        a.t += w * d;
+      for (int u = 0; u < U; ++u) {
+        float v[E];
+        LpVec<T>::get(now[u], v);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          float2 d = add2(make_float2(v[e], v[e + 1]), minus_m);
+          d.x = fmaxf(d.x, kLpFloor);
+          d.y = fmaxf(d.y, kLpFloor);
+          float2 w = mul2(d, kLpLog2e);
+          w.x = ex2(w.x);
+          w.y = ex2(w.y);
+          s2 = add2(s2, w);
+          t2 = fma2(w, d, t2);
+        }
       }
+      a.s += s2.x + s2.y;
+      a.t += t2.x + t2.y;
     }
+    // (the values are unpacked anew for what follows, not held in registers)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      asm volatile("" : "+r"(now[u].x), "+r"(now[u].y), "+r"(now[u].z), "+r"(now[u].w));
     if (open) {
-      // While there are fewer than `top` candidates: 32 groups' maxima are 32 different values,
-      // so the least of them is no more than the 32nd best of this iteration.
+      // While there are fewer than `top` candidates: the maxima of 32 groups are 32 different
+      // values, so the top-th largest of them is no more than the top-th best of this iteration.
       float g = mx != mx ? INFINITY : mx;  // (a row with a NaN has no alternatives' values anyway)
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
       if ((lane & 7) == 0) sh.group[tid >> 3] = g;
       __syncthreads();
-      float low = sh.group[lane];
+      const int before = sh.count;
+      g = sh.group[lane];
+      int above = 0;  // groups before this one
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+      for (int j = 0; j < 32; ++j) {
+        const float o = __shfl_sync(0xffffffffu, g, j);
+        above += o > g || (o == g && j < lane);
+      }
+      float low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == p.top - 1)) - 1);
       if (low == INFINITY) low = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < kLpVals; ++e)
-        if (val[e] > -INFINITY && val[e] >= low)
-          keep(val[e], head + (i0 + e / E * kLpThreads + tid) * E + e % E);
+      __syncthreads();
+      if (mx >= low)
+        each([&](float v, int id) {
+          if (v > -INFINITY && v >= low) keep(v, id);
+        });
+      __syncthreads();
+      if (sh.count > kLpKeys) {  // (many equal ones): `top` times the best below the last
+        uint64_t last = ~0ull;
+#pragma unroll 1
+        for (int k = 0; k < p.top; ++k) {
+          uint64_t b = 0;
+          each([&](float v, int id) {
+            const uint64_t key = v > -INFINITY ? lp_key(v, id) : 0;
+            if (key < last) b = max(b, key);
+          });
+          last = lp_block_max(b, sh.warp_best[k & 1]);
+          if (tid == 0) sh.keys[before + k] = last;
+        }
+        if (tid == 0) sh.count = before + p.top;  // (zeros among them are no candidates)
+      }
     } else if (mx > floor) {
       // ids rise with the iterations: what only equals the floor comes behind those that made it
-#pragma unroll
-      for (int e = 0; e < kLpVals; ++e)
-        if (val[e] > floor) keep(val[e], head + (i0 + e / E * kLpThreads + tid) * E + e % E);
+      each([&](float v, int id) {
+        if (v > floor) keep(v, id);
+      });
     }
-    if (p.top && it >= next_cut) {  // after the iterations 0, 1, 3, 7, ..
-      next_cut = open ? it + 1 : 2 * it + 1;
+    if (p.top && it >= next_cut) {  // after the iterations 0, 3, 15, ..
+      next_cut = open ? it + 1 : 4 * it + 3;
       __syncthreads();
-      const int c = min(sh.count, kLpKeys);
-      lp_select(sh.keys, c, p.top, sh.best);
-      const bool over = sh.count > kLpKeys;
-      __syncthreads();
-      if (!over) {
+      const int c = sh.count;
+      lost = lost || c > kLpKeys;
+      if (!lost) {
+        lp_select(sh.keys, c, p.top, sh.best);
         if (tid < p.top) sh.keys[tid] = sh.best[tid];
-        if (tid == 0) {
-          int n = 0;
-          while (n < p.top && sh.best[n]) ++n;
-          sh.count = n;
-        }
+        if (tid == 0) sh.count = p.top;
         open = sh.best[p.top - 1] == 0;
         if (!open) floor = lp_key_value(sh.best[p.top - 1]);
       }
@@ -277,7 +344,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK 
   if (lane == 0) sh.part[warp] = a;
   __syncthreads();
   if (p.top) {
-    if (sh.count <= kLpKeys) {
+    lost = lost || sh.count > kLpKeys;
+    if (!lost) {
       lp_select(sh.keys, sh.count, p.top, sh.best);
     } else {
       // More candidates than there is room for (logits that rise with the id): `top` times the
@@ -291,16 +359,10 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogpK 
           const uint64_t key = v > -INFINITY ? lp_key(v, i) : 0;
           if (key < last && key > b) b = key;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-        if (lane == 0) sh.all[warp] = b;
-        __syncthreads();
-        b = 0;
-        for (int w = 0; w < kLpWarps; ++w) b = max(b, sh.all[w]);
-        if (tid == 0) sh.best[k] = b;
-        last = b;
-        __syncthreads();
+        last = lp_block_max(b, sh.warp_best[k & 1]);
+        if (tid == 0) sh.best[k] = last;
       }
+      __syncthreads();
     }
   }
   if (tid == 0) {

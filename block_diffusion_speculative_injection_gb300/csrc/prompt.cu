@@ -45,14 +45,14 @@ struct PromptMaps {
 //
 // Keys behind a row's own position, or the prompt's end, have weight 0, which keeps finite values
 // of V out, not NaN or infinities (0 * NaN): in the tiles that not every row of the CTA sees
-// whole, two warps replace those by zeros in shared memory.  If there were any, the rows that do see
+// whole, a warp replaces those by zeros in shared memory.  If there were any, the rows that do see
 // them add them to their results at the end.
 //
 // Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle): Q 2 x 32 KB, a ring of five
 // stages of 32 KB for K and V in the order K0 K1 V0 K2 V1 ..  Tensor memory: S and O of both tiles, all
 // 512 columns.
-// Warps 0-3, 4-7: softmax of tile 0 and 1.  Warp 8: TMA.  Warp 9: MMAs, for each tile O(j) and
-// then S(j + 1), so that S(j + 1) follows the last read of P(j), which it overwrites.  Warps 10, 11: V.
+// Warps 0-3, 4-7: softmax of tile 0 and 1.  Warp 8: TMA.  Warps 9, 10: the tiles' MMAs, O(j) and
+// then S(j + 1), so that S(j + 1) follows the last read of P(j), which it overwrites.  Warp 11: V.
 // ---------------------------------------------------------------------------
 constexpr int kPT = 128;                       // rows of a query tile, keys of a step
 constexpr uint32_t kPBox = kPT * 128;          // 128 rows of 64 dims
@@ -132,14 +132,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* const s_full = bars + 2;    // [2]
   uint64_t* const p_full = bars + 4;    // [2][2] halves of P
   uint64_t* const o_full = bars + 8;    // [2]
-  uint64_t* const drained = bars + 10;
-  uint64_t* const clean = bars + 11;    // [kPClean] tiles it.clean ..
+  uint64_t* const drained = bars + 10;  // [2]
+  uint64_t* const clean = bars + 12;    // [kPClean] tiles it.clean ..
   uint64_t* const raw_full = clean + kPClean;  // [kPClean] the same before they are cleaned
   uint64_t* const kv_full = raw_full + kPClean;  // [stages]
   uint64_t* const kv_empty = kv_full + kPStages;
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(kv_empty + kPStages);
   volatile int* const v_bad = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert((11 + 2 * kPClean + 2 * kPStages) * 8 + 8 <= 256, "barriers fit");
+  static_assert((12 + 2 * kPClean + 2 * kPStages) * 8 + 8 <= 256, "barriers fit");
 
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
@@ -148,15 +148,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&p_full[2 * x], 4);
       mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&o_full[x], 1);
+      mbar_init(&drained[x], 1);
     }
     for (int i = 0; i < kPClean; ++i) {
-      mbar_init(&clean[i], 2);
+      mbar_init(&clean[i], 1);
       mbar_init(&raw_full[i], 1);
     }
-    mbar_init(drained, 1);
     for (int i = 0; i < kPStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], it.steps_b > 0 ? 2 : 1);
     }
     *v_bad = 0;
     mbar_fence_init();
@@ -231,88 +231,90 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
       for (int j = it.clean; j < v_issued; ++j) warp_wait(&raw_full[j - it.clean], 0, status);
       __syncwarp();
-    } else if (warp == 9) {
-      // ---- MMA issuer
+    } else if (warp <= 10) {
+      // ---- MMA issuers, one for each query tile, so that one's waits pass beside the other's
+      // products.  Whole warps wait, one lane issues: the descriptors stay in uniform registers.
+      const int x = warp - 9, steps = x == 0 ? it.steps_a : it.steps_b;
       constexpr uint32_t id_s = idesc_bf16_f32(kPT, kPT);
       constexpr uint32_t id_o = idesc_bf16_f32(kPT, kPromptHd) | kIdescBMajorMN;
-      const uint64_t q_desc = sw128_desc(smem_u32(sm));
+      const uint64_t q_desc = sw128_desc(smem_u32(sm + x * kPStage));
       const uint64_t k_desc = sw128_desc(smem_u32(sm + kPOffKV));
       const uint64_t v_desc = sw128_desc_mn(smem_u32(sm + kPOffKV), kPBox);
+      const uint32_t t_s = tmem + kPTmemS + x * kPT, t_o = tmem + kPTmemO + x * kPromptHd;
       bool ok = true;
       auto wait_for = [&](uint64_t* bar, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, warp_wait(bar, parity, status));
         return ok;
       };
-      auto scores = [&](int x, int j) {
-        const int at = prompt_load_k(j), st = at % kPStages;
-        if (!wait_for(&kv_full[st], (at / kPStages) & 1)) return;
+      auto wait_kv = [&](int at) { wait_for(&kv_full[at % kPStages], (at / kPStages) & 1); };
+      auto scores = [&](int j) {  // and K is free when they are done
+        const int st = prompt_load_k(j) % kPStages;
         tc_fence_after();
         if (leader) {
-          const uint64_t qd = q_desc + x * (kPStage >> 4), kd = k_desc + st * (kPStage >> 4);
+          const uint64_t kd = k_desc + st * (kPStage >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = ((kk >> 2) * kPBox + (kk & 3) * 32) >> 4;
-            tc_mma_bf16(tmem + kPTmemS + x * kPT, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+            tc_mma_bf16(t_s, q_desc + off, kd + off, id_s, kk > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[x]);
+          tc_commit(&kv_empty[st]);
         }
         __syncwarp();
       };
-      auto release = [&](int at) {  // (once all issued so far is done)
-        if (leader) tc_commit(&kv_empty[at % kPStages]);
-        __syncwarp();
-      };
-      if (wait_for(&q_full[0], 0)) scores(0, 0);
-      if (it.steps_b > 0 && wait_for(&q_full[1], 0)) scores(1, 0);
-      if (ok) release(0);
+      if (steps > 0) {
+        wait_kv(0);
+        if (wait_for(&q_full[x], 0)) scores(0);
+      }
 #pragma unroll 1
-      for (int j = 0; ok && j < n_steps; ++j) {
+      for (int j = 0; ok && j < steps; ++j) {
         const int at = prompt_load_v(j, n_steps), st = at % kPStages;
-#pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int steps = x == 0 ? it.steps_a : it.steps_b;
-          if (j >= steps) continue;
-          if (j >= it.clean)
-            wait_for(&clean[j - it.clean], 0);
-          else
-            wait_for(&kv_full[st], (at / kPStages) & 1);
+        // the step's loads first (they are early), then only the softmax is waited for
+        if (j + 1 < steps) wait_kv(prompt_load_k(j + 1));
+        if (j >= it.clean)
+          wait_for(&clean[j - it.clean], 0);
+        else
+          wait_kv(at);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!wait_for(&p_full[2 * x + half], j & 1)) break;
-            tc_fence_after();
-            if (leader) {
-              const uint64_t vd = v_desc + st * (kPStage >> 4);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait_for(&p_full[2 * x + half], j & 1)) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t vd = v_desc + st * (kPStage >> 4);
 #pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                tc_mma_f16_ta(tmem + kPTmemO + x * kPromptHd, tmem + kPTmemS + x * kPT + 8 * kk,
-                              vd + kk * (16 * 128 >> 4), id_o, j + kk > 0 ? 1u : 0u);
-              if (half == 1 && j + 1 == steps) tc_commit(&o_full[x]);
-            }
-            __syncwarp();
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              tc_mma_f16_ta(t_o, t_s + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, j + kk > 0 ? 1u : 0u);
+            if (half == 1) tc_commit(&kv_empty[st]);
+            if (half == 1 && j + 1 == steps) tc_commit(&o_full[x]);
           }
-          if (ok && j + 1 < steps) scores(x, j + 1);
+          __syncwarp();
         }
-        if (ok) {
-          release(at);
-          if (j + 1 < n_steps) release(prompt_load_k(j + 1));
-        }
+        if (ok && j + 1 < steps) scores(j + 1);
+      }
+      // What this tile does not use is free as far as it is concerned, once it is loaded: an
+      // arrival before that would count for the stage's load before.
+#pragma unroll 1
+      for (int i = 2 * steps; ok && steps > 0 && i < 2 * n_steps; ++i) {
+        const int at = i & 1 ? prompt_load_v(i >> 1, n_steps) : prompt_load_k(i >> 1);
+        wait_kv(at);
+        if (ok && leader) mbar_arrive(&kv_empty[at % kPStages]);
+        __syncwarp();
       }
       // nothing of this warp is in flight when it leaves
-      if (leader) tc_commit(drained);
+      if (leader) tc_commit(&drained[x]);
       __syncwarp();
-      warp_wait(drained, 0, status);
+      warp_wait(&drained[x], 0, status);
       __syncwarp();
     } else {
       // ---- V without NaN and infinities where not every row sees all keys
-      const int t = threadIdx.x - 10 * 32;
-      bool bad = false;
+            bool bad = false;
 #pragma unroll 1
       for (int j = it.clean; j < n_steps; ++j) {
         const int at = prompt_load_v(j, n_steps), st = at % kPStages;
         if (!__all_sync(0xffffffffu, warp_wait(&raw_full[j - it.clean], 0, status))) break;
         uint4* const tile = reinterpret_cast<uint4*>(sm + kPOffKV + st * kPStage);
 #pragma unroll 4
-        for (int i = t; i < (int)(kPStage / 16); i += 64) {
+        for (int i = lane; i < (int)(kPStage / 16); i += 32) {
           const uint4 v = tile[i];
           uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0;
 #pragma unroll
