@@ -60,7 +60,7 @@ constexpr uint32_t kPStage = 2 * kPBox;        // a K, V or Q tile
 constexpr int kPStages = 5;
 constexpr uint32_t kPOffKV = 2 * kPStage;
 constexpr uint32_t kPOffBar = kPOffKV + kPStages * kPStage;
-constexpr int kPromptSmem = (int)kPOffBar + 256 + 1024;  // barriers, alignment slack
+constexpr int kPromptSmem = (int)kPOffBar + 768 + 1024;  // barriers, alignment slack
 static_assert(kPromptSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kPromptThreads = 384;
 constexpr int kPromptRegs = 168, kPSoftRegs = 216, kPIssueRegs = 72;
@@ -75,18 +75,35 @@ constexpr float kPLazy = 8.f / kPScaleLog2;
 // the product with log2(e) / sqrt(128) would be a factor in the weights, 2^-4 binades here.
 constexpr float kPFar = 1048576.f / kPScaleLog2;
 
+// An item: two query tiles of a prompt and KV head, `index` of units * Hkv.
 struct PromptItem {
-  int first, n;     // the prompt's rows
-  int p0a, p0b;     // first position of each query tile
+  int first, n;          // the prompt's rows
+  int p0a, p0b;          // first position of each query tile
   int steps_a, steps_b;  // key tiles each sees (0: no row)
-  int clean;        // first key tile that not every row sees whole
+  int clean;             // first key tile that not every row sees whole
   int kvh;
 };
+constexpr int kPParts = 2;   // of P: a part's products begin while the next is computed
+constexpr int kPSlots = 2;   // items known ahead
+constexpr int kPAskLate = 1; // steps
+constexpr int kPClean = 4;   // barriers of the cleaned tiles, used in turn
+struct PromptShared {
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kPParts], o_full[2], o_empty[2], drained[2];
+  uint64_t raw_full[kPClean], clean[kPClean];
+  uint64_t kv_full[kPStages], kv_empty[kPStages];
+  uint64_t item_full[kPSlots], item_empty[kPSlots], next_full;
+  PromptItem item[kPSlots];  // n = 0: no more
+  int bad[kPSlots];          // whether V held a NaN or infinity in the tiles cleaned
+  uint32_t tmem;
+  alignas(16) uint8_t next[2][16];  // what a request for the next item answered
+};
+static_assert(sizeof(PromptShared) <= 768, "barriers fit");
 
-__device__ __forceinline__ bool prompt_item(const PromptK& p, PromptItem& it) {
-  it.kvh = blockIdx.x % p.Hkv;
-  // the last positions first: their CTAs take longest
-  const long long u = p.units - 1 - (long long)(blockIdx.x / p.Hkv);
+// whole warp
+__device__ __forceinline__ bool prompt_item(const PromptK& p, int index, PromptItem& it) {
+  it.kvh = index % p.Hkv;
+  // the last positions first: they take longest
+  const long long u = p.units - 1 - (long long)(index / p.Hkv);
   const int per = p.tiles * p.pos;
   const int b = packed_find(p.offsets, p.batch, per, 1, u);
   if (b < 0 || !packed_rows(p.offsets, b, p.n_rows, it.first, it.n)) return false;
@@ -100,15 +117,50 @@ __device__ __forceinline__ bool prompt_item(const PromptK& p, PromptItem& it) {
   };
   it.steps_a = steps(it.p0a);
   it.steps_b = p.tiles > 1 && it.p0b < it.n ? steps(it.p0b) : 0;
-  it.clean = mask_from / kPT;
+  it.clean = min(mask_from / kPT, max(it.steps_a, it.steps_b));
   return true;
 }
-// (at most 2 * 128 positions a CTA: their own keys lie in three tiles at most)
-constexpr int kPClean = 3;
 
-// which of the loads in ring order is K or V of step j of n
+// which of an item's loads in ring order is K or V of step j of n
 __device__ __forceinline__ int prompt_load_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int prompt_load_v(int j, int n) { return min(2 * j + 2, 2 * n - 1); }
+
+// Asks for a CTA of this launch that has not started, to do its work here; the answer (16
+// bytes) arrives on the barrier.
+__device__ __forceinline__ void request_cta(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// its blockIdx.x, or -1: none is left (or the GPU wants them to start by themselves)
+__device__ __forceinline__ int requested_cta(const void* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+// What every role but the producer keeps of the items it has passed.
+struct PromptPast {
+  int items;    // so far
+  int loads;    // of the ring
+  int cleaned;  // tiles of V
+  __device__ __forceinline__ void pass(const PromptItem& it) {
+    const int n = max(it.steps_a, it.steps_b);
+    ++items;
+    loads += 2 * n;
+    cleaned += n - it.clean;
+  }
+};
 
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptMaps maps, const PromptK p) {
@@ -116,85 +168,83 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  PromptShared& sh = *reinterpret_cast<PromptShared*>(sm + kPOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  packed_check(p.offsets, p.batch, p.n_rows, (long long)blockIdx.x * kPromptThreads + threadIdx.x,
-               (long long)gridDim.x * kPromptThreads, p.status);
-  PromptItem it;
-  if (!prompt_item(p, it)) {  // the whole CTA
-    pdl_trigger();
-    return;
-  }
   int32_t* const status = p.status;
-  const int n_steps = max(it.steps_a, it.steps_b);
-
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + kPOffBar);
-  uint64_t* const q_full = bars;        // [2]
-  uint64_t* const s_full = bars + 2;    // [2]
-  uint64_t* const p_full = bars + 4;    // [2][2] halves of P
-  uint64_t* const o_full = bars + 8;    // [2]
-  uint64_t* const drained = bars + 10;  // [2]
-  uint64_t* const clean = bars + 12;    // [kPClean] tiles it.clean ..
-  uint64_t* const raw_full = clean + kPClean;  // [kPClean] the same before they are cleaned
-  uint64_t* const kv_full = raw_full + kPClean;  // [stages]
-  uint64_t* const kv_empty = kv_full + kPStages;
-  uint32_t* const tslot = reinterpret_cast<uint32_t*>(kv_empty + kPStages);
-  volatile int* const v_bad = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert((12 + 2 * kPClean + 2 * kPStages) * 8 + 8 <= 256, "barriers fit");
-
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[2 * x], 4);
-      mbar_init(&p_full[2 * x + 1], 4);
-      mbar_init(&o_full[x], 1);
-      mbar_init(&drained[x], 1);
+      mbar_init(&sh.q_full[x], 1);
+      mbar_init(&sh.q_empty[x], 1);
+      mbar_init(&sh.s_full[x], 1);
+      for (int i = 0; i < kPParts; ++i) mbar_init(&sh.p_full[x][i], 4);
+      mbar_init(&sh.o_full[x], 1);
+      mbar_init(&sh.o_empty[x], 4);
+      mbar_init(&sh.drained[x], 1);
     }
     for (int i = 0; i < kPClean; ++i) {
-      mbar_init(&clean[i], 1);
-      mbar_init(&raw_full[i], 1);
+      mbar_init(&sh.clean[i], 1);
+      mbar_init(&sh.raw_full[i], 1);
     }
     for (int i = 0; i < kPStages; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], it.steps_b > 0 ? 2 : 1);
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 2);
     }
-    *v_bad = 0;
+    for (int i = 0; i < kPSlots; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_empty[i], 11);  // every warp but the producer
+    }
+    mbar_init(&sh.next_full, 1);
     mbar_fence_init();
   }
   if (warp == 8) {
-    tmem_alloc(tslot, 512);
+    tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = sh.tmem;
+  auto wait = [&](uint64_t* bar, int phase) -> bool {
+    return __all_sync(0xffffffffu, warp_wait(bar, phase & 1, status));
+  };
+  // the next item (false: none, or a wait that ran out), and that this warp is done with it
+  auto next_item = [&](const PromptPast& past, PromptItem& it) -> bool {
+    const int slot = past.items % kPSlots;
+    if (!wait(&sh.item_full[slot], past.items / kPSlots)) return false;
+    it = sh.item[slot];
+    return it.n > 0;
+  };
+  auto item_done = [&](const PromptPast& past) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_empty[past.items % kPSlots]);
+  };
 
   if (warp >= 8) {
     regs_dec<kPIssueRegs>();
     const bool leader = elect_one();
     if (warp == 8) {
-      // ---- producer
+      // ---- producer: finds the items and loads them
       if (leader) {
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
       }
-      int issued = 0, v_issued = 0;
-      auto load = [&](bool is_v, int j) -> bool {
+      int issued = 0, cleaned = 0, items = 0, q_loads[2] = {0, 0};
+      bool ok = true;
+      auto load = [&](const PromptItem& it, bool is_v, int j) -> bool {
         const int st = issued % kPStages, round = issued / kPStages;
-        if (round > 0 && !__all_sync(0xffffffffu, warp_wait(&kv_empty[st], (round - 1) & 1, status)))
-          return false;
+        if (round > 0 && !wait(&sh.kv_empty[st], round - 1)) return ok = false;
+        // The tiles of V that are cleaned have barriers of their own: that warp does not
+        // follow the ring, whose barriers have one bit for the round.
+        const bool raw = is_v && j >= it.clean;
         if (leader) {
           uint8_t* const dst = sm + kPOffKV + st * kPStage;
           const CUtensorMap* const map = is_v ? &maps.v : &maps.k;
-          // The tiles of V that are cleaned have barriers of their own: those warps do not
-          // follow the ring, whose barriers have one bit for the round.
-          uint64_t* full = &kv_full[st];
-          if (is_v && j >= it.clean) {
+          uint64_t* full = &sh.kv_full[st];
+          if (raw) {
             mbar_arrive(full);
-            full = &raw_full[j - it.clean];
+            full = &sh.raw_full[cleaned % kPClean];
           }
           mbar_arrive_expect_tx(full, kPStage);
           tma_load_3d(dst, map, 0, it.kvh, it.first + j * kPT, full);
@@ -202,39 +252,82 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
         ++issued;
-        if (is_v) v_issued = j + 1;
+        if (raw) ++cleaned;
         return true;
       };
-      auto load_q = [&](int x, int p0, int steps) {
-        if (leader && steps > 0) {
+      auto load_q = [&](const PromptItem& it, int x, int p0, int steps, int& loads) -> bool {
+        if (steps == 0) return true;
+        if (loads > 0 && !wait(&sh.q_empty[x], loads - 1)) return ok = false;
+        if (leader) {
           uint8_t* const dst = sm + x * kPStage;
-          mbar_arrive_expect_tx(&q_full[x], (uint32_t)(2 * 128 * p.G * p.pos));
-          tma_load_3d(dst, &maps.q, 0, it.kvh * p.G, it.first + p0, &q_full[x]);
-          tma_load_3d(dst + kPBox, &maps.q, 64, it.kvh * p.G, it.first + p0, &q_full[x]);
+          mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(2 * 128 * p.G * p.pos));
+          tma_load_3d(dst, &maps.q, 0, it.kvh * p.G, it.first + p0, &sh.q_full[x]);
+          tma_load_3d(dst + kPBox, &maps.q, 64, it.kvh * p.G, it.first + p0, &sh.q_full[x]);
         }
         __syncwarp();
+        ++loads;
+        return true;
       };
-      load_q(0, it.p0a, it.steps_a);
-      load(false, 0);
-      load_q(1, it.p0b, it.steps_b);
+      // makes an item known (n = 0: there are no more)
+      auto publish = [&](const PromptItem& it) -> bool {
+        const int slot = items % kPSlots, round = items / kPSlots;
+        if (round > 0 && !wait(&sh.item_empty[slot], round - 1)) return ok = false;
+        if (lane == 0) {
+          sh.item[slot] = it;
+          sh.bad[slot] = 0;
+          mbar_arrive(&sh.item_full[slot]);
+        }
+        __syncwarp();
+        ++items;
+        return true;
+      };
+      int index = blockIdx.x;
 #pragma unroll 1
-      for (int j = 0; j < n_steps; ++j) {
-        if (j + 1 < n_steps && !load(false, j + 1)) break;
-        if (!load(true, j)) break;
+      for (int asked = 0; ok && index >= 0; ++asked) {
+        auto ask = [&]() {
+          if (leader) {  // (the answer before was read: order that before the next one's writing)
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&sh.next_full, 16);
+            request_cta(sh.next[asked & 1], &sh.next_full);
+          }
+          __syncwarp();
+        };
+        packed_check(p.offsets, p.batch, p.n_rows, 32ll * index + lane, 1ll << 40, status);
+        PromptItem it;
+        const bool any = prompt_item(p, index, it) && publish(it);
+        const int n = any ? max(it.steps_a, it.steps_b) : 0;
+        // The next item is asked for while the last steps' loads are under way; with few steps
+        // there is no time for that, and little to share out better.
+        if (n <= kPAskLate) ask();
+        if (n > 0) {
+          load(it, false, 0) && load_q(it, 0, it.p0a, it.steps_a, q_loads[0]) &&
+              load_q(it, 1, it.p0b, it.steps_b, q_loads[1]);
+#pragma unroll 1
+          for (int j = 0; ok && j < n; ++j)
+            if (j + 1 == n || load(it, false, j + 1)) load(it, true, j);
+        }
+        if (n > kPAskLate) ask();
+        // (also after a failure: nothing may arrive here later)
+        if (!wait(&sh.next_full, asked)) ok = false;
+        index = requested_cta(sh.next[asked & 1]);
       }
+      PromptItem none;
+      memset(&none, 0, sizeof(none));
+      if (ok) publish(none);
       // every issued copy has landed before this warp leaves
-      warp_wait(&q_full[0], 0, status);
-      if (it.steps_b > 0) warp_wait(&q_full[1], 0, status);
 #pragma unroll 1
-      for (int i = max(0, issued - kPStages); i < issued; ++i)
-        warp_wait(&kv_full[i % kPStages], (i / kPStages) & 1, status);
+      for (int x = 0; x < 2; ++x) {
+        const int n = x == 0 ? q_loads[0] : q_loads[1];
+        if (n > 0) wait(&sh.q_full[x], n - 1);
+      }
 #pragma unroll 1
-      for (int j = it.clean; j < v_issued; ++j) warp_wait(&raw_full[j - it.clean], 0, status);
-      __syncwarp();
+      for (int i = max(0, issued - kPStages); i < issued; ++i) wait(&sh.kv_full[i % kPStages], i / kPStages);
+#pragma unroll 1
+      for (int i = max(0, cleaned - kPClean); i < cleaned; ++i) wait(&sh.raw_full[i % kPClean], i / kPClean);
     } else if (warp <= 10) {
       // ---- MMA issuers, one for each query tile, so that one's waits pass beside the other's
       // products.  Whole warps wait, one lane issues: the descriptors stay in uniform registers.
-      const int x = warp - 9, steps = x == 0 ? it.steps_a : it.steps_b;
+      const int x = warp - 9;
       constexpr uint32_t id_s = idesc_bf16_f32(kPT, kPT);
       constexpr uint32_t id_o = idesc_bf16_f32(kPT, kPromptHd) | kIdescBMajorMN;
       const uint64_t q_desc = sw128_desc(smem_u32(sm + x * kPStage));
@@ -242,203 +335,251 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const uint64_t v_desc = sw128_desc_mn(smem_u32(sm + kPOffKV), kPBox);
       const uint32_t t_s = tmem + kPTmemS + x * kPT, t_o = tmem + kPTmemO + x * kPromptHd;
       bool ok = true;
-      auto wait_for = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, warp_wait(bar, parity, status));
+      auto wait_for = [&](uint64_t* bar, int phase) {
+        if (ok) ok = wait(bar, phase);
         return ok;
       };
-      auto wait_kv = [&](int at) { wait_for(&kv_full[at % kPStages], (at / kPStages) & 1); };
-      auto scores = [&](int j) {  // and K is free when they are done
-        const int st = prompt_load_k(j) % kPStages;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t kd = k_desc + st * (kPStage >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = ((kk >> 2) * kPBox + (kk & 3) * 32) >> 4;
-            tc_mma_bf16(t_s, q_desc + off, kd + off, id_s, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&s_full[x]);
-          tc_commit(&kv_empty[st]);
-        }
-        __syncwarp();
-      };
-      if (steps > 0) {
-        wait_kv(0);
-        if (wait_for(&q_full[x], 0)) scores(0);
-      }
+      auto wait_kv = [&](int at) { wait_for(&sh.kv_full[at % kPStages], at / kPStages); };
+      PromptPast past = {0, 0, 0};
+      int mine = 0, done = 0;  // items with rows in this tile, and their steps
+      PromptItem it;
 #pragma unroll 1
-      for (int j = 0; ok && j < steps; ++j) {
-        const int at = prompt_load_v(j, n_steps), st = at % kPStages;
-        // the step's loads first (they are early), then only the softmax is waited for
-        if (j + 1 < steps) wait_kv(prompt_load_k(j + 1));
-        if (j >= it.clean)
-          wait_for(&clean[j - it.clean], 0);
-        else
-          wait_kv(at);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait_for(&p_full[2 * x + half], j & 1)) break;
+      for (; ok && next_item(past, it); item_done(past), past.pass(it)) {
+        const int steps = x == 0 ? it.steps_a : it.steps_b;
+        const int n_steps = max(it.steps_a, it.steps_b);
+        auto scores = [&](int j) {  // and K, after the last step Q, is free when they are done
+          const int st = (past.loads + prompt_load_k(j)) % kPStages;
           tc_fence_after();
           if (leader) {
-            const uint64_t vd = v_desc + st * (kPStage >> 4);
+            const uint64_t kd = k_desc + st * (kPStage >> 4);
 #pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              tc_mma_f16_ta(t_o, t_s + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, j + kk > 0 ? 1u : 0u);
-            if (half == 1) tc_commit(&kv_empty[st]);
-            if (half == 1 && j + 1 == steps) tc_commit(&o_full[x]);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = ((kk >> 2) * kPBox + (kk & 3) * 32) >> 4;
+              tc_mma_bf16(t_s, q_desc + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&sh.s_full[x]);
+            tc_commit(&sh.kv_empty[st]);
+            if (j + 1 == steps) tc_commit(&sh.q_empty[x]);
           }
           __syncwarp();
+        };
+        if (steps > 0) {
+          wait_kv(past.loads);
+          if (wait_for(&sh.q_full[x], mine)) scores(0);
         }
-        if (ok && j + 1 < steps) scores(j + 1);
-      }
-      // What this tile does not use is free as far as it is concerned, once it is loaded: an
-      // arrival before that would count for the stage's load before.
 #pragma unroll 1
-      for (int i = 2 * steps; ok && steps > 0 && i < 2 * n_steps; ++i) {
-        const int at = i & 1 ? prompt_load_v(i >> 1, n_steps) : prompt_load_k(i >> 1);
-        wait_kv(at);
-        if (ok && leader) mbar_arrive(&kv_empty[at % kPStages]);
-        __syncwarp();
+        for (int j = 0; ok && j < steps; ++j) {
+          const int at = past.loads + prompt_load_v(j, n_steps), st = at % kPStages;
+          // the step's loads first (they are early), then only the softmax is waited for
+          if (j + 1 < steps) wait_kv(past.loads + prompt_load_k(j + 1));
+          const int c = past.cleaned + j - it.clean;
+          if (j >= it.clean)
+            wait_for(&sh.clean[c % kPClean], c / kPClean);
+          else
+            wait_kv(at);
+          // O of the item before has been read
+          if (j == 0 && mine > 0) wait_for(&sh.o_empty[x], mine - 1);
+#pragma unroll
+          for (int part = 0; part < kPParts; ++part) {
+            if (!wait_for(&sh.p_full[x][part], done + j)) break;
+            tc_fence_after();
+            if (leader) {
+              const uint64_t vd = v_desc + st * (kPStage >> 4);
+              constexpr int kSteps = kPT / 16 / kPParts;  // of 16 keys
+#pragma unroll
+              for (int kk = kSteps * part; kk < kSteps * (part + 1); ++kk)
+                tc_mma_f16_ta(t_o, t_s + 8 * kk, vd + kk * (16 * 128 >> 4), id_o, j + kk > 0 ? 1u : 0u);
+              if (part == kPParts - 1) tc_commit(&sh.kv_empty[st]);
+              if (part == kPParts - 1 && j + 1 == steps) tc_commit(&sh.o_full[x]);
+            }
+            __syncwarp();
+          }
+          if (ok && j + 1 < steps) scores(j + 1);
+        }
+        // What this tile does not use is free as far as it is concerned, once it is loaded: an
+        // arrival before that would count for the stage's load before.
+#pragma unroll 1
+        for (int i = 2 * steps; ok && i < 2 * n_steps; ++i) {
+          const int at = past.loads + (i & 1 ? prompt_load_v(i >> 1, n_steps) : prompt_load_k(i >> 1));
+          wait_kv(at);
+          if (ok && leader) mbar_arrive(&sh.kv_empty[at % kPStages]);
+          __syncwarp();
+        }
+        if (steps > 0) ++mine;
+        done += steps;
       }
       // nothing of this warp is in flight when it leaves
-      if (leader) tc_commit(&drained[x]);
+      if (leader) tc_commit(&sh.drained[x]);
       __syncwarp();
-      warp_wait(&drained[x], 0, status);
-      __syncwarp();
+      wait(&sh.drained[x], 0);
     } else {
       // ---- V without NaN and infinities where not every row sees all keys
-            bool bad = false;
+      bool ok = true;
+      PromptPast past = {0, 0, 0};
+      PromptItem it;
 #pragma unroll 1
-      for (int j = it.clean; j < n_steps; ++j) {
-        const int at = prompt_load_v(j, n_steps), st = at % kPStages;
-        if (!__all_sync(0xffffffffu, warp_wait(&raw_full[j - it.clean], 0, status))) break;
-        uint4* const tile = reinterpret_cast<uint4*>(sm + kPOffKV + st * kPStage);
-#pragma unroll 4
-        for (int i = lane; i < (int)(kPStage / 16); i += 32) {
-          const uint4 v = tile[i];
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // a half whose exponent is all ones carries into its top bit
-            const uint32_t b = ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-            any |= b;
-            w[e] &= ~((b - (b >> 15)) | b);
+      for (; ok && next_item(past, it); item_done(past), past.pass(it)) {
+        const int n_steps = max(it.steps_a, it.steps_b);
+        bool bad = false;
+#pragma unroll 1
+        for (int j = it.clean; j < n_steps; ++j) {
+          const int st = (past.loads + prompt_load_v(j, n_steps)) % kPStages;
+          const int c = past.cleaned + j - it.clean;
+          if (!(ok = wait(&sh.raw_full[c % kPClean], c / kPClean))) break;
+          uint4* const tile = reinterpret_cast<uint4*>(sm + kPOffKV + st * kPStage);
+          // the largest exponent first: all ones is rare
+          uint32_t top = 0;
+#pragma unroll 8
+          for (int i = lane; i < (int)(kPStage / 16); i += 32) {
+            const uint4 v = tile[i];
+            constexpr uint32_t ones = 0x7f807f80u;
+            top = __vimax3_u16x2(top, v.x & ones, v.y & ones);
+            top = __vimax3_u16x2(top, v.z & ones, v.w & ones);
           }
-          if (any) {
-            tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((top & 0xffffu) == 0x7f80u || (top >> 16) == 0x7f80u) {
             bad = true;
+#pragma unroll 1
+            for (int i = lane; i < (int)(kPStage / 16); i += 32) {
+              const uint4 v = tile[i];
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // a half whose exponent is all ones carries into its top bit
+                const uint32_t b = ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                w[e] &= ~((b - (b >> 15)) | b);
+              }
+              tile[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
+          if (bad) *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.clean[c % kPClean]);
         }
-        if (bad) *v_bad = 1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&clean[j - it.clean]);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else {
     regs_inc<kPSoftRegs>();
     // ---- softmax: this thread's row of tile x
     const int x = warp >> 2, row = threadIdx.x & 127;
     const int g_pos = row * p.g_inv >> 16;
-    const int p0 = x == 0 ? it.p0a : it.p0b, pos = p0 + g_pos;
-    const int n_mine = x == 0 ? it.steps_a : it.steps_b;
-    const int limit = p.causal ? min(pos + 1, it.n) : it.n;  // its keys
-    const int mask_from = p.causal ? p0 + 1 : it.n;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + kPTmemS + x * kPT, t_o = lanes + kPTmemO + x * kPromptHd;
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
+    PromptPast past = {0, 0, 0};
+    int mine = 0, done = 0;  // items with rows in this tile, and their steps
+    PromptItem it;
 #pragma unroll 1
-    for (int j = 0; j < n_mine; ++j) {
-      if (!(ok = __all_sync(0xffffffffu, warp_wait(&s_full[x], j & 1, status)))) break;
-      tc_fence_after();
-      uint32_t s[kPT];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + 32 * c, s + 32 * c);
-      tmem_wait_ld();
-      if ((j + 1) * kPT > mask_from) {
-        const int end = limit - j * kPT;
-#pragma unroll
-        for (int i = 0; i < kPT; ++i)
-          if (i >= end) s[i] = __float_as_uint(-INFINITY);
-      }
-      float mx = -INFINITY, mx2 = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kPT; i += 4) {
-        mx = max3(mx, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-        mx2 = max3(mx2, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-      }
-      mx = fmaxf(mx, mx2);
-      const bool grown = mx > m + kPLazy || (m == -INFINITY && mx > m);
-      if (__any_sync(0xffffffffu, grown)) {
-        const float alpha = grown ? ex2((m - mx) * kPScaleLog2) : 1.f;
-        if (j > 0) {  // O holds the steps before: S(j) is complete, so they are
+    for (; ok && next_item(past, it); item_done(past), past.pass(it)) {
+      const int n_mine = x == 0 ? it.steps_a : it.steps_b;
+      if (n_mine == 0) continue;
+      const int p0 = x == 0 ? it.p0a : it.p0b, pos = p0 + g_pos;
+      const int limit = p.causal ? min(pos + 1, it.n) : it.n;  // its keys
+      const int mask_from = p.causal ? p0 + 1 : it.n;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32_nowait(t_o + 32 * c, o);
-            tmem_wait_ld();
+      for (int j = 0; j < n_mine; ++j) {
+        if (!(ok = wait(&sh.s_full[x], done + j))) break;
+        tc_fence_after();
+        uint32_t s[kPT];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(t_o + 32 * c, o);
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+        if ((j + 1) * kPT > mask_from) {
+          const int end = limit - j * kPT;
+#pragma unroll
+          for (int i = 0; i < kPT; ++i)
+            if (i >= end) s[i] = __float_as_uint(-INFINITY);
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx[c] = max3(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]), -INFINITY);
+#pragma unroll
+        for (int i = 8; i < kPT; i += 2) {
+          float& t = mx[(i >> 1) & 3];
+          t = max3(t, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        }
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const bool grown = top > m + kPLazy || (m == -INFINITY && top > m);
+        const float m_next = grown ? top : m;
+        float base = m_next == -INFINITY ? 0.f : -m_next * kPScaleLog2;
+        const bool far = fabsf(m_next) > kPFar && m_next != -INFINITY;
+        if (__any_sync(0xffffffffu, grown || far)) {
+          if (j > 0 && __any_sync(0xffffffffu, grown)) {
+            // O holds the steps before: S(j) is complete, so they are
+            const float alpha = grown ? ex2((m - top) * kPScaleLog2) : 1.f;
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32_nowait(t_o + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(t_o + 32 * c, o);
+            }
+          }
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < kPT; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - m_next);
+            base = 0.f;
           }
         }
-        if (grown) {
-          l *= alpha;
-          m = mx;
-        }
-      }
-      float base = m == -INFINITY ? 0.f : -m * kPScaleLog2;
-      if (__any_sync(0xffffffffu, fabsf(m) > kPFar && m != -INFINITY)) {
-        if (m != -INFINITY) {
+        m = m_next;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto stored = [&](int part) {  // P of this part is in tensor memory
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[x][part]);
+        };
+        constexpr int kWords = kPT / 2 / kPParts;
 #pragma unroll
-          for (int i = 0; i < kPT; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - m);
-          base = 0.f;
-        }
-      }
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int part = 0; part < kPParts; ++part) {
+          float pk[kWords];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+          for (int i = 0; i < kWords; ++i) {
+            const int e = 2 * (kWords * part + i);
+            float2 z = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kPScaleLog2,
+                            base);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum[i & 1] = add2(sum[i & 1], z);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(z.x, z.y);
+            pk[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+          }
+          if (part > 0) stored(part - 1);  // (the store passes while this part is computed)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int e = 64 * half + 2 * i;
-          float2 z = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kPScaleLog2,
-                          base);
-          z.x = ex2(z.x);
-          z.y = ex2(z.y);
-          sum[i & 1] = add2(sum[i & 1], z);
-          const __nv_bfloat162 h = __floats2bfloat162_rn(z.x, z.y);
-          pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int i = 0; i < kWords; i += 16) tmem_st16(t_s + kWords * part + i, pk + i);
         }
-        tmem_st32(t_s + 32 * half, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
+        stored(kPParts - 1);
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
       }
-      sum[0] = add2(sum[0], sum[1]);
-      l += sum[0].x + sum[0].y;
-    }
-    // ---- the rows' results
-    if (n_mine > 0 && ok) ok = __all_sync(0xffffffffu, warp_wait(&o_full[x], 0, status));
-    if (n_mine > 0 && ok) {
+      // ---- the rows' results
+      if (ok) ok = wait(&sh.o_full[x], mine);
+      if (!ok) break;
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int head0 = it.kvh * p.G;
+      const int head = it.kvh * p.G + row - g_pos * p.G;
       const bool live = g_pos < p.pos && pos < it.n;
       if (live && p.lse)
-        p.lse[(long long)(it.first + pos) * p.H + head0 + row - g_pos * p.G] =
+        p.lse[(long long)(it.first + pos) * p.H + head] =
             l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
-      const bool bad = *v_bad != 0;
-      // through shared memory (this warp's rows of Q, which is used up), 16 bytes at chunk c ^ row
-      uint8_t* const stage = sm + x * kPStage + (warp & 3) * (32 * 256);
+      const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
+      bf16* const out = p.out + ((long long)(it.first + pos) * p.H + head) * kPromptHd;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         tmem_ld32_nowait(t_o + 32 * c, o);
         tmem_wait_ld();
+        if (c == 3) {  // O may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_empty[x]);
+        }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         if (bad && live) {
@@ -452,32 +593,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
         }
+        if (live) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                           __uint_as_float(o[8 * k + 2 * e + 1]));
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                             __uint_as_float(o[8 * k + 2 * e + 1]));
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + k) ^ (lane & 15)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int r = 2 * i + (lane >> 4), chunk = lane & 15;
-        const int rr = (warp & 3) * 32 + r, g = rr * p.g_inv >> 16;
-        if (g < p.pos && p0 + g < it.n) {
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 256 + ((chunk ^ (r & 15)) << 4));
-          *reinterpret_cast<uint4*>(p.out +
-                                    ((long long)(it.first + p0 + g) * p.H + head0 + rr - g * p.G) *
-                                        kPromptHd +
-                                    8 * chunk) = v;
-        }
-      }
+      ++mine;
+      done += n_mine;
     }
   }
   tc_fence_before();
