@@ -60,6 +60,8 @@ constexpr uint32_t kPStage = 2 * kPBox;        // a K, V or Q tile
 constexpr int kPStages = 5;
 constexpr uint32_t kPOffKV = 2 * kPStage;
 constexpr uint32_t kPOffBar = kPOffKV + kPStages * kPStage;
+constexpr uint32_t kPOutBytes = 32 * 128;      // a warp's 32 rows of 64 dims on their way out
+static_assert(8 * kPOutBytes <= kPStage, "the results of both tiles fit into a stage");
 constexpr int kPromptSmem = (int)kPOffBar + 768 + 1024;  // barriers, alignment slack
 static_assert(kPromptSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kPromptThreads = 384;
@@ -88,7 +90,7 @@ constexpr int kPSlots = 2;   // items known ahead
 constexpr int kPAskLate = 1; // steps
 constexpr int kPClean = 4;   // barriers of the cleaned tiles, used in turn
 struct PromptShared {
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kPParts], o_full[2], o_empty[2], drained[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kPParts], o_full[2], o_empty[2], issued[2], drained[2];
   uint64_t raw_full[kPClean], clean[kPClean];
   uint64_t kv_full[kPStages], kv_empty[kPStages];
   uint64_t item_full[kPSlots], item_empty[kPSlots], next_full;
@@ -152,12 +154,12 @@ __device__ __forceinline__ int requested_cta(const void* answer) {
 // What every role but the producer keeps of the items it has passed.
 struct PromptPast {
   int items;    // so far
-  int loads;    // of the ring
+  int loads;    // of the ring, and the stage that an item's results pass through
   int cleaned;  // tiles of V
   __device__ __forceinline__ void pass(const PromptItem& it) {
     const int n = max(it.steps_a, it.steps_b);
     ++items;
-    loads += 2 * n;
+    loads += 2 * n + 1;
     cleaned += n - it.clean;
   }
 };
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int i = 0; i < kPParts; ++i) mbar_init(&sh.p_full[x][i], 4);
       mbar_init(&sh.o_full[x], 1);
       mbar_init(&sh.o_empty[x], 4);
+      mbar_init(&sh.issued[x], 1);
       mbar_init(&sh.drained[x], 1);
     }
     for (int i = 0; i < kPClean; ++i) {
@@ -305,6 +308,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
           for (int j = 0; ok && j < n; ++j)
             if (j + 1 == n || load(it, false, j + 1)) load(it, true, j);
+          // a stage for the results on their way out
+          const int st = issued % kPStages, round = issued / kPStages;
+          if (ok && round > 0) ok = wait(&sh.kv_empty[st], round - 1);
+          if (ok && lane == 0) mbar_arrive(&sh.kv_full[st]);
+          __syncwarp();
+          if (ok) ++issued;
         }
         if (n > kPAskLate) ask();
         // (also after a failure: nothing may arrive here later)
@@ -342,11 +351,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto wait_kv = [&](int at) { wait_for(&sh.kv_full[at % kPStages], at / kPStages); };
       PromptPast past = {0, 0, 0};
       int mine = 0, done = 0;  // items with rows in this tile, and their steps
+      int turns = 0;           // steps that both tiles had
       PromptItem it;
 #pragma unroll 1
       for (; ok && next_item(past, it); item_done(past), past.pass(it)) {
         const int steps = x == 0 ? it.steps_a : it.steps_b;
-        const int n_steps = max(it.steps_a, it.steps_b);
+        const int n_steps = max(it.steps_a, it.steps_b), n_both = min(it.steps_a, it.steps_b);
         auto scores = [&](int j) {  // and K, after the last step Q, is free when they are done
           const int st = (past.loads + prompt_load_k(j)) % kPStages;
           tc_fence_after();
@@ -379,6 +389,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             wait_kv(at);
           // O of the item before has been read
           if (j == 0 && mine > 0) wait_for(&sh.o_empty[x], mine - 1);
+          // The tiles take turns, the first before the second.  Left to themselves both come at
+          // once, their products pass in alternation and end together, and so do the softmaxes:
+          // in step for good, with the tensor cores idle meanwhile (2.0 us a step instead of 1.4).
+          const int turn = turns + j - (x == 0 ? 1 : 0);
+          if (j < n_both && turn >= 0) wait_for(&sh.issued[1 - x], turn);
 #pragma unroll
           for (int part = 0; part < kPParts; ++part) {
             if (!wait_for(&sh.p_full[x][part], done + j)) break;
@@ -395,12 +410,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             __syncwarp();
           }
           if (ok && j + 1 < steps) scores(j + 1);
+          if (ok && leader && j < n_both) mbar_arrive(&sh.issued[x]);
         }
+        turns += n_both;
         // What this tile does not use is free as far as it is concerned, once it is loaded: an
         // arrival before that would count for the stage's load before.
 #pragma unroll 1
-        for (int i = 2 * steps; ok && i < 2 * n_steps; ++i) {
-          const int at = past.loads + (i & 1 ? prompt_load_v(i >> 1, n_steps) : prompt_load_k(i >> 1));
+        for (int i = 2 * steps; ok && i < 2 * n_steps + (steps == 0 ? 1 : 0); ++i) {
+          const int at = past.loads + (i == 2 * n_steps ? i
+                                       : i & 1          ? prompt_load_v(i >> 1, n_steps)
+                                                        : prompt_load_k(i >> 1));
           wait_kv(at);
           if (ok && leader) mbar_arrive(&sh.kv_empty[at % kPStages]);
           __syncwarp();
@@ -569,44 +588,54 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         p.lse[(long long)(it.first + pos) * p.H + head] =
             l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
       const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
-      bf16* const out = p.out + ((long long)(it.first + pos) * p.H + head) * kPromptHd;
+      float o[kPromptHd];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_o + 32 * c, reinterpret_cast<uint32_t*>(o) + 32 * c);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_empty[x]);  // O may be overwritten
+#pragma unroll
+      for (int i = 0; i < kPromptHd; ++i) o[i] *= inv;
+      if (bad && live) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32_nowait(t_o + 32 * c, o);
-        tmem_wait_ld();
-        if (c == 3) {  // O may be overwritten
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.o_empty[x]);
-        }
+        for (int key = it.clean * kPT; key < limit; ++key) {
+          const bf16* const v = p.v + (long long)(it.first + key) * p.vs + it.kvh * kPromptHd;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (bad && live) {
-#pragma unroll 1
-          for (int key = it.clean * kPT; key < limit; ++key) {
-            const bf16* const v = p.v + (long long)(it.first + key) * p.vs + it.kvh * kPromptHd + 32 * c;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float f = ld_f(v + i);
-              if (!(fabsf(f) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + f);
-            }
-          }
-        }
-        if (live) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                             __uint_as_float(o[8 * k + 2 * e + 1]));
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < kPromptHd; ++i) {
+            const float f = ld_f(v + i);
+            if (!(fabsf(f) < INFINITY)) o[i] += f;
           }
         }
       }
+      // Through shared memory, 64 dims at a time (16 bytes at chunk c ^ row): a row a lane would
+      // touch 32 lines an instruction, so 32 turns of the memory pipe instead of 4.
+      const int slot = past.loads + 2 * max(it.steps_a, it.steps_b);
+      if (!(ok = wait(&sh.kv_full[slot % kPStages], slot / kPStages))) break;
+      uint8_t* const stage = sm + kPOffKV + slot % kPStages * kPStage + warp * kPOutBytes;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              f_to_bf16x8(o + 64 * half + 8 * c);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), c = lane & 7;
+          const int rr = (warp & 3) * 32 + r, g = rr * p.g_inv >> 16;
+          if (g < p.pos && p0 + g < it.n) {
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+            *reinterpret_cast<uint4*>(
+                p.out + ((long long)(it.first + p0 + g) * p.H + it.kvh * p.G + rr - g * p.G) * kPromptHd +
+                64 * half + 8 * c) = v;
+          }
+        }
+        __syncwarp();
+      }
+      fence_proxy_async_smem();  // (a load may overwrite it)
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+      if (row == 0) mbar_arrive(&sh.kv_empty[slot % kPStages]);
       ++mine;
       done += n_mine;
     }
