@@ -409,8 +409,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             __syncwarp();
           }
-          if (ok && j + 1 < steps) scores(j + 1);
           if (ok && leader && j < n_both) mbar_arrive(&sh.issued[x]);
+          if (ok && j + 1 < steps) scores(j + 1);
         }
         turns += n_both;
         // What this tile does not use is free as far as it is concerned, once it is loaded: an
