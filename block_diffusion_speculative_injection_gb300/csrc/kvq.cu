@@ -54,6 +54,7 @@ struct AppendK {
   long long stride[2];  // elements between rows
   int batch, rows;
   long long n_blk;
+  PackedUnits units;
 };
 
 template <bool kPacked>
@@ -73,10 +74,10 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
     head = (int)(w % p.c.Hkv);
     w /= p.c.Hkv;
     if (w >= p.n_blk) return;
-    b = packed_find(p.offsets, p.batch, kKvqSub, 2, w);
+    b = packed_find(p.offsets, p.batch, p.units, w);
     int first = 0;
     if (b < 0 || !packed_rows(p.offsets, b, p.rows, first, cnt)) return;
-    blk = (int)(w - packed_base(p.offsets, b, kKvqSub, 2));
+    blk = (int)(w - packed_base(p.offsets, b, p.units));
     row0 = first;
   } else {
     w >>= 1;
@@ -749,6 +750,7 @@ dflash_status dflash_kvq_append_packed(const dflash_kvq_cache* cache, int32_t ba
     return DFLASH_E_INVALID_ARG;
   AppendK p;
   p.n_blk = packed_units(n_rows, batch, kKvqSub, 2);
+  p.units = packed_units_of(kKvqSub, 2);
   const int64_t warps = p.n_blk * cache->n_kv_heads * 2;
   if (warps >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
   const void* const ptrs[] = {seq_ids, start, offsets, k, v};

@@ -7,28 +7,36 @@
 
 namespace dflash {
 
-// Work units of `unit` rows: sequence b has the units from offsets[b] / unit + extra * b on, up
-// to the next sequence's.  floor(x + y) >= floor(x) + floor(y), so that leaves it
+// Work units of `unit` rows (1..256): sequence b has the units from offsets[b] / unit + extra * b
+// on, up to the next sequence's.  floor(x + y) >= floor(x) + floor(y), so that leaves it
 // floor(rows / unit) + extra or more, and all of them lie below n_rows / unit + extra * batch.
+struct PackedUnits {
+  uint64_t magic;  // ceil(2^38 / unit): n * magic >> 38 is n / unit where n * magic < 2^64 (n up
+                   // to 2^26 * unit), as n * (magic * unit - 2^38) < 2^38 then
+  int extra;
+};
+inline PackedUnits packed_units_of(int unit, int extra) {
+  return PackedUnits{((1ull << 38) + unit - 1) / unit, extra};
+}
 inline int64_t packed_units(int64_t n_rows, int64_t batch, int unit, int extra) {
   return n_rows / unit + extra * batch;
 }
 
-// First unit of sequence b
-__device__ __forceinline__ long long packed_base(const int32_t* offsets, int b, int unit, int extra) {
-  return offsets[b] / unit + (long long)extra * b;
+// First unit of sequence b (offsets out of range: any number)
+__device__ __forceinline__ long long packed_base(const int32_t* offsets, int b, const PackedUnits& u) {
+  return (long long)((uint64_t)(uint32_t)offsets[b] * u.magic >> 38) + (long long)u.extra * b;
 }
 
-// The sequence that unit u lies in (the last b with base <= u), or -1 before the first: a whole
+// The sequence that unit `at` lies in (the last b with base <= at), or -1 before the first: a whole
 // warp searches, 32 probes at a time, so a batch of up to 32 takes one load.
-__device__ __forceinline__ int packed_find(const int32_t* offsets, int batch, int unit, int extra,
-                                           long long u) {
+__device__ __forceinline__ int packed_find(const int32_t* offsets, int batch, const PackedUnits& u,
+                                           long long at) {
   const int lane = threadIdx.x & 31;
   int lo = 0, end = batch;
   while (true) {
     const int step = (end - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool below = at < end && packed_base(offsets, at, unit, extra) <= u;
+    const int probe = lo + lane * step;
+    const bool below = probe < end && packed_base(offsets, probe, u) <= at;
     const int n = __popc(__ballot_sync(0xffffffffu, below));
     if (n == 0) return -1;
     lo += (n - 1) * step;

@@ -23,7 +23,8 @@ struct PromptK {
   int batch, n_rows, H, Hkv, G, causal;
   int pos, g_inv;  // positions of a tile's 128 rows; row / G = row * g_inv >> 16 (row < 128)
   int tiles;       // query tiles of a CTA: 1 or 2
-  int units;       // of tiles * pos positions, over all sequences
+  int n_units;     // of tiles * pos positions, over all sequences
+  PackedUnits units;
 };
 
 struct PromptMaps {
@@ -57,11 +58,11 @@ struct PromptMaps {
 constexpr int kPT = 128;                       // rows of a query tile, keys of a step
 constexpr uint32_t kPBox = kPT * 128;          // 128 rows of 64 dims
 constexpr uint32_t kPStage = 2 * kPBox;        // a K, V or Q tile
-constexpr int kPStages = 5;
+constexpr int kPStages = 4;
 constexpr uint32_t kPOffKV = 2 * kPStage;
-constexpr uint32_t kPOffBar = kPOffKV + kPStages * kPStage;
-constexpr uint32_t kPOutBytes = 32 * 128;      // a warp's 32 rows of 64 dims on their way out
-static_assert(8 * kPOutBytes <= kPStage, "the results of both tiles fit into a stage");
+constexpr uint32_t kPOffOut = kPOffKV + kPStages * kPStage;
+constexpr uint32_t kPOutBytes = 32 * 128;      // a softmax warp's 32 rows of 64 dims on their way out
+constexpr uint32_t kPOffBar = kPOffOut + 8 * kPOutBytes;
 constexpr int kPromptSmem = (int)kPOffBar + 768 + 1024;  // barriers, alignment slack
 static_assert(kPromptSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr int kPromptThreads = 384;
@@ -103,13 +104,13 @@ static_assert(sizeof(PromptShared) <= 768, "barriers fit");
 
 // whole warp
 __device__ __forceinline__ bool prompt_item(const PromptK& p, int index, PromptItem& it) {
-  it.kvh = index % p.Hkv;
+  const int from_end = (int)((uint32_t)index / (uint32_t)p.Hkv);
+  it.kvh = index - from_end * p.Hkv;
   // the last positions first: they take longest
-  const long long u = p.units - 1 - (long long)(index / p.Hkv);
-  const int per = p.tiles * p.pos;
-  const int b = packed_find(p.offsets, p.batch, per, 1, u);
+  const int u = p.n_units - 1 - from_end;
+  const int b = packed_find(p.offsets, p.batch, p.units, u);
   if (b < 0 || !packed_rows(p.offsets, b, p.n_rows, it.first, it.n)) return false;
-  const long long at = (u - packed_base(p.offsets, b, per, 1)) * per;
+  const long long at = (u - packed_base(p.offsets, b, p.units)) * (p.tiles * p.pos);
   if (at >= it.n) return false;
   const int mask_from = p.causal ? (int)at + 1 : it.n;
   it.p0a = (int)at;
@@ -154,12 +155,12 @@ __device__ __forceinline__ int requested_cta(const void* answer) {
 // What every role but the producer keeps of the items it has passed.
 struct PromptPast {
   int items;    // so far
-  int loads;    // of the ring, and the stage that an item's results pass through
+  int loads;    // of the ring
   int cleaned;  // tiles of V
   __device__ __forceinline__ void pass(const PromptItem& it) {
     const int n = max(it.steps_a, it.steps_b);
     ++items;
-    loads += 2 * n + 1;
+    loads += 2 * n;
     cleaned += n - it.clean;
   }
 };
@@ -308,12 +309,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
           for (int j = 0; ok && j < n; ++j)
             if (j + 1 == n || load(it, false, j + 1)) load(it, true, j);
-          // a stage for the results on their way out
-          const int st = issued % kPStages, round = issued / kPStages;
-          if (ok && round > 0) ok = wait(&sh.kv_empty[st], round - 1);
-          if (ok && lane == 0) mbar_arrive(&sh.kv_full[st]);
-          __syncwarp();
-          if (ok) ++issued;
         }
         if (n > kPAskLate) ask();
         // (also after a failure: nothing may arrive here later)
@@ -416,10 +411,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // What this tile does not use is free as far as it is concerned, once it is loaded: an
         // arrival before that would count for the stage's load before.
 #pragma unroll 1
-        for (int i = 2 * steps; ok && i < 2 * n_steps + (steps == 0 ? 1 : 0); ++i) {
-          const int at = past.loads + (i == 2 * n_steps ? i
-                                       : i & 1          ? prompt_load_v(i >> 1, n_steps)
-                                                        : prompt_load_k(i >> 1));
+        for (int i = 2 * steps; ok && i < 2 * n_steps; ++i) {
+          const int at = past.loads + (i & 1 ? prompt_load_v(i >> 1, n_steps) : prompt_load_k(i >> 1));
           wait_kv(at);
           if (ok && leader) mbar_arrive(&sh.kv_empty[at % kPStages]);
           __syncwarp();
@@ -485,6 +478,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int g_pos = row * p.g_inv >> 16;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + kPTmemS + x * kPT, t_o = lanes + kPTmemO + x * kPromptHd;
+    // rows that this thread writes, from the tile's first: the heads of other KV heads lie between
+    // positions
+    int out_row[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int rr = (warp & 3) * 32 + 4 * i + (lane >> 3);
+      out_row[i] = (rr * p.g_inv >> 16) * (p.H - p.G) + rr;
+    }
     bool ok = true;
     PromptPast past = {0, 0, 0};
     int mine = 0, done = 0;  // items with rows in this tile, and their steps
@@ -581,61 +582,63 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (ok) ok = wait(&sh.o_full[x], mine);
       if (!ok) break;
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int head = it.kvh * p.G + row - g_pos * p.G;
-      const bool live = g_pos < p.pos && pos < it.n;
-      if (live && p.lse)
-        p.lse[(long long)(it.first + pos) * p.H + head] =
-            l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
-      const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
       float o[kPromptHd];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_o + 32 * c, reinterpret_cast<uint32_t*>(o) + 32 * c);
+      const float inv = l == 0.f ? 0.f : rcp(l);
+      const int n_live = min(p.pos, it.n - p0) * p.G;  // rows of the prompt
+      // first of the tile's rows: position p0, the first head of this KV head
+      const long long row0 = (long long)(it.first + p0) * p.H + it.kvh * p.G;
+      const int off = g_pos * (p.H - p.G) + row;  // this thread's from there
+      if (row < n_live && p.lse)
+        p.lse[row0 + off] = l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
+      const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty[x]);  // O may be overwritten
-#pragma unroll
-      for (int i = 0; i < kPromptHd; ++i) o[i] *= inv;
-      if (bad && live) {
-#pragma unroll 1
-        for (int key = it.clean * kPT; key < limit; ++key) {
-          const bf16* const v = p.v + (long long)(it.first + key) * p.vs + it.kvh * kPromptHd;
-#pragma unroll
-          for (int i = 0; i < kPromptHd; ++i) {
-            const float f = ld_f(v + i);
-            if (!(fabsf(f) < INFINITY)) o[i] += f;
-          }
-        }
-      }
       // Through shared memory, 64 dims at a time (16 bytes at chunk c ^ row): a row a lane would
       // touch 32 lines an instruction, so 32 turns of the memory pipe instead of 4.
-      const int slot = past.loads + 2 * max(it.steps_a, it.steps_b);
-      if (!(ok = wait(&sh.kv_full[slot % kPStages], slot / kPStages))) break;
-      uint8_t* const stage = sm + kPOffKV + slot % kPStages * kPStage + warp * kPOutBytes;
+      uint8_t* const mine_out = sm + kPOffOut + warp * kPOutBytes + lane * 128;
+      bf16* const out = p.out + row0 * kPromptHd + (lane & 7) * 8;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              f_to_bf16x8(o + 64 * half + 8 * c);
-        __syncwarp();
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), c = lane & 7;
-          const int rr = (warp & 3) * 32 + r, g = rr * p.g_inv >> 16;
-          if (g < p.pos && p0 + g < it.n) {
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-            *reinterpret_cast<uint4*>(
-                p.out + ((long long)(it.first + p0 + g) * p.H + it.kvh * p.G + rr - g * p.G) * kPromptHd +
-                64 * half + 8 * c) = v;
+          for (int e = 0; e < 4; ++e) {
+            const int d = 64 * half + 8 * c + 2 * e;
+            const float2 y = mul2(make_float2(o[d], o[d + 1]), inv);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *reinterpret_cast<uint4*>(mine_out + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (bad && row < n_live) {
+          // what this row sees of the elements that were replaced by zeros
+#pragma unroll 1
+          for (int key = it.clean * kPT; key < limit; ++key) {
+            const bf16* const v = p.v + (long long)(it.first + key) * p.vs + it.kvh * kPromptHd + 64 * half;
+#pragma unroll 1
+            for (int d = 0; d < 64; ++d) {
+              const float f = ld_f(v + d);
+              bf16* const y = reinterpret_cast<bf16*>(mine_out + (((d >> 3) ^ (lane & 7)) << 4)) + (d & 7);
+              if (!(fabsf(f) < INFINITY)) st_f(y, ld_f(y) + f);
+            }
           }
         }
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), rr = (warp & 3) * 32 + r;
+          if (rr < n_live)
+            *reinterpret_cast<uint4*>(out + (long long)out_row[i] * kPromptHd + 64 * half) =
+                *reinterpret_cast<const uint4*>(sm + kPOffOut + warp * kPOutBytes + r * 128 +
+                                                (((lane & 7) ^ (r & 7)) << 4));
+        }
+        __syncwarp();
       }
-      fence_proxy_async_smem();  // (a load may overwrite it)
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-      if (row == 0) mbar_arrive(&sh.kv_empty[slot % kPStages]);
       ++mine;
       done += n_mine;
     }
@@ -677,7 +680,7 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
                                       int64_t k_row_stride, const void* v, int64_t v_row_stride,
                                       void* out, float* lse, int32_t* status,
                                       dflash_stream_t stream) {
-  if (batch < 1 || batch >= (1 << 26) || n_rows < 1 || n_rows >= (1 << 30) || n_heads < 1 ||
+  if (batch < 1 || batch >= (1 << 26) || n_rows < 1 || n_rows >= (1 << 26) || n_heads < 1 ||
       n_heads > 65535 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 64 ||
       (causal != 0 && causal != 1) || !offsets || !q || !k || !v || !out || !status ||
       !prompt_stride_ok(q_row_stride, n_heads) || !prompt_stride_ok(k_row_stride, n_kv_heads) ||
@@ -725,7 +728,8 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.tiles = packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads < kvq_sms() ? 1 : 2;
   const int64_t units = packed_units(n_rows, batch, p.tiles * p.pos, 1);
   if (units * n_kv_heads >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
-  p.units = (int)units;
+  p.n_units = (int)units;
+  p.units = packed_units_of(p.tiles * p.pos, 1);
   PromptMaps maps;
   if (!prompt_map(&maps.q, q, n_heads, n_rows, q_row_stride, p.G, p.pos) ||
       !prompt_map(&maps.k, k, n_kv_heads, n_rows, k_row_stride, 1, kPT) ||
