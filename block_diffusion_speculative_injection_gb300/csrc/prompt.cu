@@ -23,12 +23,13 @@ struct PromptK {
   int batch, n_rows, H, Hkv, G, causal;
   int pos, g_inv;  // positions of a tile's 128 rows; row / G = row * g_inv >> 16 (row < 128)
   int tiles;       // query tiles of a CTA: 1 or 2
+  int box_out;     // 32 rows are whole positions: maps.out has boxes of them
   int n_units;     // of tiles * pos positions, over all sequences
   PackedUnits units;
 };
 
 struct PromptMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
 };
 
 // ---------------------------------------------------------------------------
@@ -478,14 +479,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int g_pos = row * p.g_inv >> 16;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = lanes + kPTmemS + x * kPT, t_o = lanes + kPTmemO + x * kPromptHd;
-    // rows that this thread writes, from the tile's first: the heads of other KV heads lie between
-    // positions
-    int out_row[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int rr = (warp & 3) * 32 + 4 * i + (lane >> 3);
-      out_row[i] = (rr * p.g_inv >> 16) * (p.H - p.G) + rr;
-    }
     bool ok = true;
     PromptPast past = {0, 0, 0};
     int mine = 0, done = 0;  // items with rows in this tile, and their steps
@@ -597,24 +590,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.o_empty[x]);  // O may be overwritten
-      // Through shared memory, 64 dims at a time (16 bytes at chunk c ^ row): a row a lane would
-      // touch 32 lines an instruction, so 32 turns of the memory pipe instead of 4.
-      uint8_t* const mine_out = sm + kPOffOut + warp * kPOutBytes + lane * 128;
-      bf16* const out = p.out + row0 * kPromptHd + (lane & 7) * 8;
+      // Out through shared memory, 64 dims at a time (16 bytes at chunk c ^ row): a row a lane would
+      // touch 32 lines an instruction, so 32 turns of the memory pipe instead of 4.  A warp whose 32
+      // rows are all the prompt's, and whole positions, leaves them to one bulk copy.
+      uint8_t* const out_rows = sm + kPOffOut + warp * kPOutBytes;
+      uint8_t* const out_row_mine = out_rows + lane * 128;
+      const int rr0 = (warp & 3) * 32;
+      const bool bulk = p.box_out && rr0 + 32 <= n_live;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 64 * half + 8 * c + 2 * e;
-            const float2 y = mul2(make_float2(o[d], o[d + 1]), inv);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          *reinterpret_cast<uint4*>(mine_out + ((c ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 32; ++i) {
+          const float2 y = mul2(make_float2(o[64 * half + 2 * i], o[64 * half + 2 * i + 1]), inv);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        if (lane == 0) bulk_wait_read();  // what was here before has left
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(out_row_mine + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         if (bad && row < n_live) {
           // what this row sees of the elements that were replaced by zeros
 #pragma unroll 1
@@ -623,25 +620,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
             for (int d = 0; d < 64; ++d) {
               const float f = ld_f(v + d);
-              bf16* const y = reinterpret_cast<bf16*>(mine_out + (((d >> 3) ^ (lane & 7)) << 4)) + (d & 7);
+              bf16* const y = reinterpret_cast<bf16*>(out_row_mine + (((d >> 3) ^ (lane & 7)) << 4)) + (d & 7);
               if (!(fabsf(f) < INFINITY)) st_f(y, ld_f(y) + f);
             }
           }
         }
-        __syncwarp();
+        if (bulk) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&maps.out, out_rows, 64 * half, it.kvh * p.G,
+                         it.first + p0 + (rr0 * p.g_inv >> 16));
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), rr = (warp & 3) * 32 + r;
-          if (rr < n_live)
-            *reinterpret_cast<uint4*>(out + (long long)out_row[i] * kPromptHd + 64 * half) =
-                *reinterpret_cast<const uint4*>(sm + kPOffOut + warp * kPOutBytes + r * 128 +
-                                                (((lane & 7) ^ (r & 7)) << 4));
+          for (int i = lane; i < 32 * 8; i += 32) {
+            const int r = i >> 3, c = i & 7, g = (rr0 + r) * p.g_inv >> 16;
+            if (rr0 + r < n_live)
+              *reinterpret_cast<uint4*>(p.out + (row0 + g * (p.H - p.G) + rr0 + r) * kPromptHd + 64 * half +
+                                        8 * c) =
+                  *reinterpret_cast<const uint4*>(out_rows + r * 128 + ((c ^ (r & 7)) << 4));
+          }
         }
         __syncwarp();
       }
       ++mine;
       done += n_mine;
     }
+    if (lane == 0) bulk_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -724,6 +732,7 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.causal = causal;
   p.pos = kPT / p.G;
   p.g_inv = 65536 / p.G + 1;
+  p.box_out = 32 % p.G == 0;
   // two query tiles a CTA, but one where the CTAs would be fewer than the SMs
   p.tiles = packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads < kvq_sms() ? 1 : 2;
   const int64_t units = packed_units(n_rows, batch, p.tiles * p.pos, 1);
@@ -731,9 +740,11 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.n_units = (int)units;
   p.units = packed_units_of(p.tiles * p.pos, 1);
   PromptMaps maps;
+  memset(&maps, 0, sizeof(maps));
   if (!prompt_map(&maps.q, q, n_heads, n_rows, q_row_stride, p.G, p.pos) ||
       !prompt_map(&maps.k, k, n_kv_heads, n_rows, k_row_stride, 1, kPT) ||
-      !prompt_map(&maps.v, v, n_kv_heads, n_rows, v_row_stride, 1, kPT))
+      !prompt_map(&maps.v, v, n_kv_heads, n_rows, v_row_stride, 1, kPT) ||
+      (p.box_out && !prompt_map(&maps.out, out, n_heads, n_rows, (int64_t)n_heads * kPromptHd, p.G, 32 / p.G)))
     return DFLASH_E_CUDA;
   static std::atomic<bool> smem_done[kMaxDevices];
   if (ensure_smem_attr(smem_done, prompt_attn_kernel, kPromptSmem) != cudaSuccess)
