@@ -502,8 +502,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if ((j + 1) * kPT > mask_from) {
           const int end = limit - j * kPT;
 #pragma unroll
-          for (int i = 0; i < kPT; ++i)
-            if (i >= end) s[i] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < kPT; c += 32) {
+            // (bits to predicates eight at a time: half the instructions of a comparison each)
+            const int n = end - c;
+            const uint32_t seen = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) s[c + i] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[4];
 #pragma unroll
