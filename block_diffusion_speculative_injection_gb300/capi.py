@@ -693,9 +693,13 @@ def dflash_status_check(status, stream=None) -> None:
 def _packed_rows(t, name: str, n_rows: int, heads: int) -> int:
     """Elements between the rows of a bf16 [n_rows][heads][128] tensor whose rows
     may be slices of wider ones."""
-    if t.dim() != 3:
+    if (t.dtype not in (_KVQ_DTYPES or _kvq_dtypes())["bf16"]
+            or t.shape != (n_rows, heads, 128)):
         _kvq_refuse(f"{name}: need bfloat16 of shape {(n_rows, heads, 128)}")
-    return _kvq_rows(t[None], name, 1, n_rows, heads)
+    sr, sh, sd = t.stride()
+    if sd != 1 or (sh != 128 and heads > 1):
+        _kvq_refuse(f"{name}: rows of {heads} * 128 elements are needed")
+    return sr if n_rows > 1 else heads * 128
 
 
 def dflash_kvq_append_packed(cache: KvqCache, batch, seq_ids, start, offsets, k, v,
@@ -717,12 +721,13 @@ def dflash_prompt_attention(batch, causal, offsets, q, k, v, out, lse=None, stat
     q's shape, lse [n_rows][n_heads], status [1] int32 (zero at the start)."""
     if q.dim() != 3 or k.dim() != 3:
         _kvq_refuse("q, k: need [n_rows][heads][128]")
-    n_rows, heads, kv_heads = q.shape[0], q.shape[1], k.shape[1]
+    n_rows, heads, _ = rows = q.shape
+    kv_heads = k.shape[1]
     _kvq_check(load().dflash_prompt_attention(
-        batch, n_rows, heads, kv_heads, int(causal), _kvq_dense(offsets, "offsets", "i32", (batch + 1,)),
+        batch, n_rows, heads, kv_heads, causal, _kvq_dense(offsets, "offsets", "i32", (batch + 1,)),
         q.data_ptr(), _packed_rows(q, "q", n_rows, heads), k.data_ptr(),
         _packed_rows(k, "k", n_rows, kv_heads), v.data_ptr(),
-        _packed_rows(v, "v", n_rows, kv_heads), _kvq_dense(out, "out", "bf16", (n_rows, heads, 128)),
+        _packed_rows(v, "v", n_rows, kv_heads), _kvq_dense(out, "out", "bf16", rows),
         _kvq_dense(lse, "lse", "f32", (n_rows, heads)), _kvq_dense(status, "status", "i32", (1,)),
         _kvq_stream(stream)), "dflash_prompt_attention")
 

@@ -11,10 +11,14 @@
 
 namespace dflash {
 
-// One CTA walks the batch (up to kMapBatch entries, kMapPer consecutive ones a thread).
-constexpr int kMapThreads = 1024, kMapBatch = 4096, kMapPer = kMapBatch / kMapThreads;
-constexpr int kRowThreads = 256;
-constexpr int kFusedRows = 4096;  // up to here the same CTA writes the rows' maps
+// Both calls are bound by latency: a launch, and then a chain of dependent reads (ids, the
+// sequences' counts, page ids).  A CTA walks the whole batch, kPer consecutive entries a thread.  For
+// the maps of many rows a cluster of CTAs does so, each for all entries, and shares the rows out; what
+// the call reads and changes is changed after all of them have read it.
+// 256 sequences with a block of 16 rows each, given back and mapped: _US_BLOCK_ us for both calls; 32 prompts
+// of 512 to 4096 rows (_ROWS_ rows, _BYTES_ MB of maps): _US_PROMPTS_ us.
+constexpr int kMapThreads = 1024, kMapBatch = 4096;
+constexpr int kMapCluster = 8, kMapRows = 2048;  // most CTAs; rows a CTA takes before there is another
 
 struct PagesK {
   int32_t *table, *mapped, *free, *n_free, *status;
@@ -26,7 +30,6 @@ struct MapK {
   int32_t *offsets, *kv_lens, *row_seq, *row_pos, *row_slot;
   int batch, n_rows;
   int hash;  // places of the table of ids, a power of two >= 2 * batch
-  int fused;
 };
 
 // Shared memory: per entry its id, the pages taken up to and with it, and where in the
@@ -83,27 +86,48 @@ __device__ __forceinline__ int id_place(const MapK& k, const MapSmem& s, int id,
   return -1;
 }
 
-// Entry b: false when its id is no sequence's, or an earlier entry names the same.
-__device__ __forceinline__ bool map_entry(const MapK& k, const MapSmem& s, int b) {
-  const int id = s.id[b];
-  return id >= 0 && id < k.p.n_seqs && id_place(k, s, id, b, false) == b;
-}
+// This thread's entries, read ahead of everything else: id (-1: none or out of range), the
+// first and second number of the call, the pages that the sequence has.
+template <int kPer>
+struct MapEntries {
+  int id[kPer], a[kPer], c[kPer], have[kPer];
+  bool mine[kPer], good[kPer];  // there is such an entry; its id is a sequence's, and named first here
+};
 
-__device__ __forceinline__ MapSmem map_begin(const MapK& k, int32_t* sm) {
+template <int kPer>
+__device__ __forceinline__ MapSmem map_begin(const MapK& k, int32_t* sm, MapEntries<kPer>& e) {
   MapSmem s;
-  const int n = k.batch + 1;
+  const int n = k.batch + 1, b0 = threadIdx.x * kPer;
   s.id = sm;
   s.end = sm + n;
   s.base = sm + 2 * n;
   s.off = sm + 3 * n;
   s.start = sm + 4 * n;
   s.seen = sm + 5 * n;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = b0 + i;
+    e.mine[i] = b < k.batch;
+    e.id[i] = !e.mine[i] ? -1 : k.seq_ids ? k.seq_ids[b] : b;
+    e.a[i] = e.mine[i] && k.start ? k.start[b] : 0;
+    e.c[i] = e.mine[i] && k.counts ? k.counts[b] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    e.good[i] = e.id[i] >= 0 && e.id[i] < k.p.n_seqs;
+    e.have[i] = e.good[i] ? k.p.mapped[e.id[i]] : 0;
+    if (e.mine[i]) s.id[b0 + i] = e.id[i];
+  }
   for (int i = threadIdx.x; i < k.hash; i += kMapThreads) s.seen[i] = -1;
-  for (int b = threadIdx.x; b < k.batch; b += kMapThreads) s.id[b] = k.seq_ids ? k.seq_ids[b] : b;
   __syncthreads();
-  for (int b = threadIdx.x; b < k.batch; b += kMapThreads)
-    if (s.id[b] >= 0 && s.id[b] < k.p.n_seqs) id_place(k, s, s.id[b], b, true);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (e.good[i]) id_place(k, s, e.id[i], b0 + i, true);
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    e.good[i] = e.good[i] && id_place(k, s, e.id[i], b0 + i, false) == b0 + i && e.have[i] >= 0 &&
+                e.have[i] <= k.p.pps;
   return s;
 }
 
@@ -120,59 +144,36 @@ __device__ __forceinline__ int entry_above(const int32_t* end, int batch, int i)
   return lo;
 }
 
-// the three numbers of packed row r of entry b (its rows from `first` on behind `start`
-// slots; start < 0: none)
-__device__ __forceinline__ void write_row(const MapK& k, int r, int seq, int start, int first) {
-  int pos = -1, slot = -1;
-  if (start < 0) {
-    seq = -1;
-  } else {
-    pos = start + (r - first);
-    const int page = k.p.table[(int64_t)seq * k.p.pps + pos / kPageSlots];
-    slot = page >= 0 && page < k.p.n_pages ? page * kPageSlots + pos % kPageSlots : -1;
-  }
-  if (k.row_seq) k.row_seq[r] = seq;
-  if (k.row_pos) k.row_pos[r] = pos;
-  if (k.row_slot) k.row_slot[r] = slot;
-}
-
-__global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k) {
+template <int kPer>
+__global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, const int C) {
+  pdl_trigger();
   pdl_wait();
   extern __shared__ int32_t map_smem[];
-  const MapSmem s = map_begin(k, map_smem);
-  const int tid = threadIdx.x, b0 = tid * kMapPer;
+  const int tid = threadIdx.x, b0 = tid * kPer, rank = blockIdx.x;
   int n_free = *k.p.n_free;
+  MapEntries<kPer> e;
+  const MapSmem s = map_begin(k, map_smem, e);
+  bool bad = false, full = false;
   if (n_free < 0 || n_free > k.p.n_pages) {
-    set_dev_status(k.p.status, kDevCheck);
+    bad = true;
     n_free = 0;
   }
   // what each entry needs: rows and pages
-  int rows[kMapPer], need[kMapPer], have[kMapPer], st[kMapPer];
-  bool good[kMapPer];
+  int rows[kPer], need[kPer];
   long long sum_rows = 0, sum_need = 0;
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i) {
-    const int b = b0 + i;
-    rows[i] = need[i] = have[i] = st[i] = 0;
-    good[i] = false;
-    if (b >= k.batch) continue;
-    st[i] = k.start ? k.start[b] : 0;
-    rows[i] = max(k.counts[b], 0);
-    good[i] = map_entry(k, s, b) && st[i] >= 0 && k.counts[b] >= 0;
-    if (good[i]) {
-      have[i] = k.p.mapped[s.id[b]];
-      good[i] = have[i] >= 0 && have[i] <= k.p.pps;
-    }
-    if (!good[i]) {
-      set_dev_status(k.p.status, kDevCheck);
-    } else {
-      const long long end = (long long)st[i] + rows[i];
-      if (end > (long long)k.p.pps * kPageSlots) {
-        set_dev_status(k.p.status, kDevCapacity);
-        good[i] = false;
-      } else {
-        need[i] = max(0, (int)((end + kPageSlots - 1) / kPageSlots) - have[i]);
-      }
+  for (int i = 0; i < kPer; ++i) {
+    rows[i] = max(e.c[i], 0);
+    need[i] = 0;
+    e.good[i] = e.good[i] && e.a[i] >= 0 && e.c[i] >= 0;
+    bad = bad || (e.mine[i] && !e.good[i]);
+    if (e.good[i]) {
+      const long long end = (long long)e.a[i] + rows[i];
+      e.good[i] = end <= (long long)k.p.pps * kPageSlots;
+      if (e.good[i])
+        need[i] = max(0, (int)((end + kPageSlots - 1) / kPageSlots) - e.have[i]);
+      else
+        full = true;
     }
     sum_rows += rows[i];
     sum_need += need[i];
@@ -180,103 +181,125 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k) {
   long long end_rows = sum_rows, end_need = sum_need;
   block_scan2(end_rows, end_need);
   long long row = end_rows - sum_rows, page = end_need - sum_need;
+  bool odd = false;  // an entry that needs pages does not get them
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
-    if (b >= k.batch) break;
+    if (!e.mine[i]) break;
     const int first = (int)min(row, (long long)k.n_rows);
-    if (good[i] && ((need[i] > 0 && page + need[i] > n_free) || row + rows[i] > k.n_rows)) {
-      set_dev_status(k.p.status, kDevCapacity);
-      good[i] = false;
-    }
-    k.offsets[b] = first;
-    k.kv_lens[b] = good[i] ? st[i] + rows[i] : max(st[i], 0);
-    s.off[b] = first;
-    s.start[b] = good[i] ? st[i] : -1;
-    s.base[b] = good[i] ? need[i] : 0;
+    const bool no_rows = row + rows[i] > k.n_rows;
     row += rows[i];
     page += need[i];
+    if (e.good[i] && ((need[i] > 0 && page > n_free) || no_rows)) {
+      full = true;
+      odd = odd || need[i] > 0;
+      e.good[i] = false;
+    }
+    if (!e.good[i]) need[i] = 0;
+    if (rank == 0) {
+      k.offsets[b] = first;
+      k.kv_lens[b] = e.good[i] ? e.a[i] + rows[i] : max(e.a[i], 0);
+    }
+    s.off[b] = first;
+    s.start[b] = e.good[i] ? e.a[i] : -1;
+    if (b == k.batch - 1) {
+      const int all = (int)min(row, (long long)k.n_rows);
+      if (rank == 0) k.offsets[k.batch] = all;
+      s.off[k.batch] = all;
+      full = full || row > k.n_rows;
+    }
   }
-  // The pages of the entries that get them, counted anew: an entry refused for its rows leaves
-  // its pages to nobody.
-  long long got = 0, none = 0;
+  if (bad) set_dev_status(k.p.status, kDevCheck);
+  if (full) set_dev_status(k.p.status, kDevCapacity);
+  // Pages are counted over the entries that get them: anew where some do not.
+  long long at = end_need - sum_need;
+  if (__syncthreads_or(odd)) {
+    long long got = 0, none = 0;
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i)
-    if (b0 + i < k.batch) got += s.base[b0 + i];
-  long long end_got = got;
-  block_scan2(end_got, none);
-  int at = (int)(end_got - got);
+    for (int i = 0; i < kPer; ++i) got += need[i];
+    long long end_got = got;
+    block_scan2(end_got, none);
+    at = end_got - got;
+  }
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
-    if (b >= k.batch) break;
-    const int take = s.base[b];
-    s.base[b] = have[i] - at;
-    at += take;
-    s.end[b] = at;
-    if (take > 0) k.p.mapped[s.id[b]] = have[i] + take;
-  }
-  if (b0 < k.batch && b0 + kMapPer >= k.batch) {  // the last entry's thread
-    const int all = (int)min(row, (long long)k.n_rows);
-    k.offsets[k.batch] = all;
-    s.off[k.batch] = all;
-    if (row > k.n_rows) set_dev_status(k.p.status, kDevCapacity);
+    if (!e.mine[i]) break;
+    s.base[b] = e.have[i] - (int)at;
+    at += need[i];
+    s.end[b] = (int)at;
   }
   __syncthreads();
+  // The three numbers of each packed row.  A page is the table's, or, not there yet, the free list's.
+  if (k.row_seq || k.row_pos || k.row_slot) {
+    const int stride = C * kMapThreads, n_packed = s.off[k.batch];
+    constexpr int kAtOnce = 4;
+    for (int r0 = rank * kMapThreads + tid; r0 < k.n_rows; r0 += kAtOnce * stride) {
+      int seq[kAtOnce], pos[kAtOnce], pg[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int r = r0 + i * stride;
+        seq[i] = pos[i] = pg[i] = -1;
+        if (r >= n_packed) continue;
+        const int b = entry_above(s.off + 1, k.batch, r);
+        if (s.start[b] < 0) continue;
+        seq[i] = s.id[b];
+        pos[i] = s.start[b] + (r - s.off[b]);
+        const int in_seq = pos[i] / kPageSlots, in_list = in_seq - s.base[b];
+        pg[i] = in_list >= (b > 0 ? s.end[b - 1] : 0)
+                    ? k.p.free[n_free - 1 - in_list]
+                    : k.p.table[(int64_t)seq[i] * k.p.pps + in_seq];
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int r = r0 + i * stride;
+        if (r >= k.n_rows) break;
+        if (k.row_seq) k.row_seq[r] = seq[i];
+        if (k.row_pos) k.row_pos[r] = pos[i];
+        if (k.row_slot)
+          k.row_slot[r] = pg[i] >= 0 && pg[i] < k.p.n_pages ? pg[i] * kPageSlots + pos[i] % kPageSlots : -1;
+      }
+    }
+  }
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // from here on the state changes
+  if (rank == 0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (need[i] > 0) k.p.mapped[e.id[i]] = e.have[i] + need[i];
+  }
   const int total = s.end[k.batch - 1];
-  for (int i = tid; i < total; i += kMapThreads) {
+  for (int i = rank * kMapThreads + tid; i < total; i += C * kMapThreads) {
     const int b = entry_above(s.end, k.batch, i);
     k.p.table[(int64_t)s.id[b] * k.p.pps + s.base[b] + i] = k.p.free[n_free - 1 - i];
     k.p.free[n_free - 1 - i] = -1;
   }
-  if (tid == 0 && total > 0) *k.p.n_free = n_free - total;
-  if (!k.fused) return;
-  __syncthreads();
-  for (int r = tid; r < k.n_rows; r += kMapThreads) {
-    const bool none_left = r >= s.off[k.batch];
-    const int b = none_left ? 0 : entry_above(s.off + 1, k.batch, r);
-    write_row(k, r, s.id[b], none_left ? -1 : s.start[b], s.off[b]);
-  }
+  if (rank == 0 && tid == 0 && total > 0) *k.p.n_free = n_free - total;
 }
 
-// The rows' maps of long batches.
-__global__ void __launch_bounds__(kRowThreads) pages_rows_kernel(const MapK k) {
-  pdl_wait();
-  const int r = blockIdx.x * kRowThreads + threadIdx.x;
-  if (r >= k.n_rows) return;
-  const bool none_left = r >= k.offsets[k.batch];
-  const int b = none_left ? 0 : entry_above(k.offsets + 1, k.batch, r);
-  const int first = k.offsets[b];
-  int start = -1;
-  if (!none_left) {  // an entry that was refused kept its length
-    start = k.start ? k.start[b] : 0;
-    if (k.kv_lens[b] - start != k.counts[b]) start = -1;
-  }
-  write_row(k, r, k.seq_ids ? k.seq_ids[b] : b, start, first);
-}
-
+template <int kPer>
 __global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k) {
+  pdl_trigger();
   pdl_wait();
   extern __shared__ int32_t map_smem[];
-  const MapSmem s = map_begin(k, map_smem);
-  const int tid = threadIdx.x, b0 = tid * kMapPer;
+  const int tid = threadIdx.x, b0 = tid * kPer;
   const int n_free = *k.p.n_free;
-  int give[kMapPer], keep[kMapPer];
+  MapEntries<kPer> e;
+  const MapSmem s = map_begin(k, map_smem, e);
+  int give[kPer], keep[kPer];
   long long sum = 0, none = 0;
+  bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i) {
-    const int b = b0 + i;
+  for (int i = 0; i < kPer; ++i) {
     give[i] = keep[i] = 0;
-    if (b >= k.batch) continue;
-    const int slots = k.start ? k.start[b] : 0;
-    bool good = map_entry(k, s, b) && slots >= 0;
-    if (good) {
-      const int have = k.p.mapped[s.id[b]];
-      good = have >= 0 && have <= k.p.pps;
-      keep[i] = (int)(((long long)slots + kPageSlots - 1) / kPageSlots);
-      if (good) give[i] = max(0, have - keep[i]);
-    }
-    if (!good) set_dev_status(k.p.status, kDevCheck);
+    e.good[i] = e.good[i] && e.a[i] >= 0;
+    bad = bad || (e.mine[i] && !e.good[i]);
+    if (!e.good[i]) continue;
+    keep[i] = (int)(((long long)e.a[i] + kPageSlots - 1) / kPageSlots);
+    give[i] = max(0, e.have[i] - keep[i]);
     sum += give[i];
   }
   long long end = sum;
@@ -291,21 +314,22 @@ __global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k
     if (tid == 0) set_dev_status(k.p.status, kDevCheck);
     return;
   }
+  if (bad) set_dev_status(k.p.status, kDevCheck);
 #pragma unroll
-  for (int i = 0; i < kMapPer; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
-    if (b >= k.batch) break;
+    if (!e.mine[i]) break;
     s.base[b] = keep[i] - (int)at;
     at += give[i];
     s.end[b] = (int)at;
-    if (give[i] > 0) k.p.mapped[s.id[b]] = keep[i];
+    if (give[i] > 0) k.p.mapped[e.id[i]] = keep[i];
   }
   __syncthreads();
   for (int i = tid; i < (int)total; i += kMapThreads) {
     const int b = entry_above(s.end, k.batch, i);
-    int32_t* const e = k.p.table + (int64_t)s.id[b] * k.p.pps + s.base[b] + i;
-    k.p.free[n_free + total - 1 - i] = *e;
-    *e = -1;
+    int32_t* const entry = k.p.table + (int64_t)s.id[b] * k.p.pps + s.base[b] + i;
+    k.p.free[n_free + total - 1 - i] = *entry;
+    *entry = -1;
   }
   if (tid == 0 && total > 0) *k.p.n_free = n_free + (int)total;
 }
@@ -395,19 +419,17 @@ dflash_status dflash_pages_map(const dflash_pages* pages, int32_t batch, int32_t
   k.row_pos = row_pos;
   k.row_slot = row_slot;
   k.n_rows = n_rows;
-  const bool rows = row_seq || row_pos || row_slot;
-  k.fused = rows && n_rows <= kFusedRows;
-  static std::atomic<bool> smem_done[kMaxDevices];
-  if (ensure_smem_attr(smem_done, pages_map_kernel, (int)(map_smem_ints(kMapBatch, 2 * kMapBatch) * 4)) !=
+  int C = 1;
+  if (row_seq || row_pos || row_slot)
+    while (C < kMapCluster && C * kMapRows < n_rows) C *= 2;
+  static std::atomic<bool> smem_done[2][kMaxDevices];
+  const int big = batch > kMapThreads;
+  const auto kernel = big ? pages_map_kernel<kMapBatch / kMapThreads> : pages_map_kernel<1>;
+  if (ensure_smem_attr(smem_done[big], kernel, (int)(map_smem_ints(kMapBatch, 2 * kMapBatch) * 4)) !=
       cudaSuccess)
     return DFLASH_E_CUDA;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (launch_k(true, pages_map_kernel, dim3(1), dim3(kMapThreads), map_smem_ints(batch, k.hash) * 4, st,
-               k) != cudaSuccess)
-    return DFLASH_E_CUDA;
-  if (rows && n_rows > kFusedRows &&
-      launch_k(true, pages_rows_kernel, dim3((n_rows + kRowThreads - 1) / kRowThreads),
-               dim3(kRowThreads), 0, st, k) != cudaSuccess)
+  if (launch_k_cluster(true, dim3(C, 1, 1), kernel, dim3(C), dim3(kMapThreads),
+                       map_smem_ints(batch, k.hash) * 4, (cudaStream_t)stream, k, C) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
@@ -426,12 +448,14 @@ dflash_status dflash_pages_release(const dflash_pages* pages, int32_t batch, con
   const void* const ptrs[] = {out[0].p, out[1].p, out[2].p, out[3].p, out[4].p, seq_ids, keep};
   DF_TRY(kvq_ptrs_ok(ptrs, 7));
   MapK k = map_args(pages, batch, seq_ids, keep);
-  static std::atomic<bool> smem_done[kMaxDevices];
-  if (ensure_smem_attr(smem_done, pages_release_kernel,
-                       (int)(map_smem_ints(kMapBatch, 2 * kMapBatch) * 4)) != cudaSuccess)
+  static std::atomic<bool> smem_done[2][kMaxDevices];
+  const int big = batch > kMapThreads;
+  const auto kernel = big ? pages_release_kernel<kMapBatch / kMapThreads> : pages_release_kernel<1>;
+  if (ensure_smem_attr(smem_done[big], kernel, (int)(map_smem_ints(kMapBatch, 2 * kMapBatch) * 4)) !=
+      cudaSuccess)
     return DFLASH_E_CUDA;
-  if (launch_k(true, pages_release_kernel, dim3(1), dim3(kMapThreads),
-               map_smem_ints(batch, k.hash) * 4, (cudaStream_t)stream, k) != cudaSuccess)
+  if (launch_k(true, kernel, dim3(1), dim3(kMapThreads), map_smem_ints(batch, k.hash) * 4,
+               (cudaStream_t)stream, k) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
