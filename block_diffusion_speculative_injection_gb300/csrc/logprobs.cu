@@ -18,7 +18,6 @@ constexpr int kLpStep = kLpThreads * 16;          // ids of an iteration of a CT
 constexpr int kLpTop = 32;                        // most alternatives
 constexpr int kLpKeys = 768;                      // candidates a CTA holds
 constexpr int kLpCluster = 8;                     // most CTAs a row
-static_assert(kLpKeys / kLpThreads < 4, "a thread's count in two bits");
 constexpr float kLpLog2e = 1.4426950408889634f;
 // d_i are cut off here, where e^d_i is zero in fp32, so that a logit of -inf adds 0 and not
 // 0 * inf to T
@@ -115,42 +114,56 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 
 struct LpShared {
   uint64_t keys[kLpKeys];
+  uint64_t shorter[kLpKeys];
+  uint64_t group_key[kLpThreads / 8];
   uint64_t best[kLpTop];     // the part's alternatives in order, 0 behind the last
   uint64_t all[kLpCluster * kLpTop];
   uint64_t warp_best[2][kLpWarps];
   RowSum part[kLpWarps];
   RowSum sum;                // the part's sums
+  RowSum sums[kLpCluster];   // all parts', in the first CTA
   float group[kLpThreads / 8];
-  int count;
+  int count, n_short;
 };
 
-// The n best of c keys (all different but for zeros), in order, to out[0 .. n), zeros behind the last;
-// whole CTA.  Up to a few hundred each is ranked by counting; of more, first the n-th best is
-// found by its bits.
-__device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out) {
-  const int tid = threadIdx.x;
+// The n best of c keys (all different but for zeros), in order, to out[0 .. n), zeros behind the
+// last; whole CTA.  Up to 256 each is ranked by counting.  Of more, the maxima of 32 groups are 32
+// different keys, and the n-th largest of them leaves a short list (of 768 random keys 31 for n = 20).
+__device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out, LpShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31;
   uint64_t least = 1;
-  if (c > kLpThreads) {
-    uint64_t t = 0;
-#pragma unroll 1
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t next = t | (1ull << bit);
-      int mine = 0;
-      for (int i = tid; i < c; i += kLpThreads) mine += keys[i] >= next;
-      const int sum = __syncthreads_count(mine & 1) + 2 * __syncthreads_count(mine >> 1);
-      if (sum >= n) t = next;
-    }
-    least = max(t, (uint64_t)1);
-  }
   if (tid < n) out[tid] = 0;
+  if (tid == 0) sh.n_short = 0;
+  if (c > kLpThreads) {
+    uint64_t g = 0;
+    for (int i = tid; i < c; i += kLpThreads) g = max(g, keys[i]);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if ((lane & 7) == 0) sh.group_key[tid >> 3] = g;
+    __syncthreads();
+    g = sh.group_key[lane];
+    int above = 0;
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      const uint64_t o = __shfl_sync(0xffffffffu, g, j);
+      above += o > g || (o == g && j < lane);
+    }
+    const int nth = __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1;
+    least = max(__shfl_sync(0xffffffffu, g, nth), least);
+    for (int i = tid; i < c; i += kLpThreads)
+      if (keys[i] >= least) sh.shorter[atomicAdd(&sh.n_short, 1)] = keys[i];
+  }
   __syncthreads();
+  if (c > kLpThreads) {
+    keys = sh.shorter;
+    c = sh.n_short;
+  }
   for (int i = tid; i < c; i += kLpThreads) {
     const uint64_t k = keys[i];
-    if (k < least) continue;
     int rank = 0;
 #pragma unroll 8
     for (int j = 0; j < c; ++j) rank += keys[j] > k;
-    if (rank < n) out[rank] = k;
+    if (k != 0 && rank < n) out[rank] = k;
   }
   __syncthreads();
 }
@@ -167,14 +180,45 @@ __device__ __forceinline__ uint64_t lp_block_max(uint64_t b, uint64_t* buffer) {
   return b;
 }
 
+// The n best of ids f0 .. f1 - 1 in order, one after the other, to out; whole CTA.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_kernel(const LogpK p, const int C) {
+__device__ __noinline__ void lp_rounds(const T* x, int f0, int f1, int n, uint64_t* out, LpShared& sh) {
+  uint64_t last = ~0ull;
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    uint64_t b = 0;
+#pragma unroll 4
+    for (int i = f0 + (int)threadIdx.x; i < f1; i += kLpThreads) {
+      const float v = ld_f(x + i);
+      const uint64_t key = v > -INFINITY ? lp_key(v, i) : 0;
+      if (key < last && key > b) b = key;
+    }
+    last = lp_block_max(b, sh.warp_best[k & 1]);
+    if (threadIdx.x == 0) out[k] = last;
+  }
+}
+
+// the next fp32 below x (not NaN; -inf stays)
+__device__ __forceinline__ float just_below(float x) {
+  const int b = __float_as_int(x);
+  if (x == -INFINITY) return x;
+  return x == 0.f ? __int_as_float((int)0x80000001u) : __int_as_float(b > 0 ? b - 1 : b + 1);
+}
+
+// A row's part of a CTA: the cluster of C CTAs shares the row out.  Bound by memory: each thread has
+// the next iteration's loads under way while it works on this one's.  (What it takes: fp32 15 and
+// bf16 9 instructions a logit with the shares of everything else.)
+template <typename T, bool kTopIds>
+__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
+    token_logprobs_kernel(const LogpK p, const int C) {
+  pdl_trigger();
   pdl_wait();
   constexpr int E = LpVec<T>::kN, U = LpVec<T>::kAtOnce;
   extern __shared__ __align__(16) uint8_t lp_smem[];
   LpShared& sh = *reinterpret_cast<LpShared*>(lp_smem);
   const int row = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
+  const int n_top = kTopIds ? p.top : 0;
   const int tok = p.tokens ? p.tokens[row] : 0;
   if (tok < 0) return;  // (the whole cluster) a row that is not in use
   const T* const x = static_cast<const T*>(p.logits) + (long long)row * p.stride;
@@ -182,68 +226,68 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
   const int head = min(p.vocab, (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
   const int vecs = (p.vocab - head) / E, tail0 = head + vecs * E;
   const int v0 = (int)((long long)vecs * rank / C), v1 = (int)((long long)vecs * (rank + 1) / C);
-  const uint4* const vec = reinterpret_cast<const uint4*>(x + head);
+  const uint4* const vec = reinterpret_cast<const uint4*>(x + head) + tid;
   float x_tok = 0.f;
   if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
   if (tid == 0) sh.count = 0;
-  RowSum a = {-INFINITY, 0.f, 0.f};
+  uint4 next[U];
+  auto fetch = [&](int i0) {
+    if (i0 + kLpThreads * U <= v1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = ld_stream(vec + i0 + u * kLpThreads);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        next[u] = i0 + u * kLpThreads + tid < v1
+                      ? ld_stream(vec + i0 + u * kLpThreads)
+                      : make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
+    }
+  };
+  fetch(v0);
+  float m = -INFINITY;  // this thread's maximum, and its sums in two parts each
+  float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
+  auto raise_to = [&](float top) {
+    const float d = fmaxf(m - top, kLpFloor), f = lp_exp(d);
+    t2 = mul2(fma2(s2, make_float2(d, d), t2), f);
+    s2 = mul2(s2, f);
+    m = top;
+  };
   auto add = [&](float v) {
     if (v == -INFINITY) return;
-    const float m = max_nan(a.m, v);
-    if (!(m == a.m)) raise(a, m);
-    const float d = fmaxf(v - a.m, kLpFloor), e = lp_exp(d);
-    a.s += e;
-    a.t += e * d;
+    const float top = max_nan(m, v);
+    if (!(top == m)) raise_to(top);
+    const float d = fmaxf(v - m, kLpFloor), e = lp_exp(d);
+    s2.x += e;
+    t2.x += e * d;
   };
   auto keep = [&](float v, int id) {
     const int at = atomicAdd(&sh.count, 1);
     if (at < kLpKeys) sh.keys[at] = lp_key(v, id);
   };
-  __syncthreads();
+  if (kTopIds) __syncthreads();
   // the ids before the vectors: candidates with the first ones
   if (rank == 0 && tid < head) {
     const float v = ld_f(x + tid);
     add(v);
-    if (p.top && v > -INFINITY) keep(v, tid);
+    if (kTopIds && v > -INFINITY) keep(v, tid);
   }
-  bool open = p.top > 0;  // fewer than `top` candidates so far
-  bool lost = false;      // more candidates than there was room for
-  float floor = INFINITY;
-  int next_cut = 0;
+  bool open = true;         // not known yet to have `top` candidates
+  bool lost = false;        // more candidates than there was room for
+  float floor = -INFINITY;  // values up to here are no candidates any more
+  int next_cut = 3;
   int it = 0;
-  uint4 next[U];
-  auto fetch = [&](int i0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kLpThreads + tid;
-      next[u] = i < v1 ? ld_stream(vec + i)
-                       : make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
-    }
-  };
-  fetch(v0);
 #pragma unroll 1
   for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
     uint4 now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = next[u];
     if (i0 + kLpThreads * U < v1) fetch(i0 + kLpThreads * U);
-    // calls f(value, id) for each of this thread's values
-    auto each = [&](auto f) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float v[E];
-        LpVec<T>::get(now[u], v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f(v[e], head + (i0 + u * kLpThreads + tid) * E + e);
-      }
-    };
     float mx = LpVec<T>::top(now[0]);
 #pragma unroll
     for (int u = 1; u < U; ++u) mx = max_nan(mx, LpVec<T>::top(now[u]));
-    const float m = max_nan(a.m, mx);
-    if (!(m == a.m)) raise(a, m);
+    const float top = max_nan(m, mx);
+    if (!(top == m)) raise_to(top);
     if (m != -INFINITY) {
-      float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
       const float2 minus_m = make_float2(-m, -m);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -261,68 +305,77 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
           t2 = fma2(w, d, t2);
         }
       }
-      a.s += s2.x + s2.y;
-      a.t += t2.x + t2.y;
     }
-    // (the values are unpacked anew for what follows, not held in registers)
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      asm volatile("" : "+r"(now[u].x), "+r"(now[u].y), "+r"(now[u].z), "+r"(now[u].w));
-    if (open) {
-      // While there are fewer than `top` candidates: the maxima of 32 groups are 32 different
-      // values, so the top-th largest of them is no more than the top-th best of this iteration.
+    if (!kTopIds) continue;
+    const bool opened = open;
+    int before = 0;
+    float low = 0.f;
+    if (opened) {
+      // The maxima of 32 groups are 32 different values, so the top-th largest of them is no more
+      // than the top-th best of this iteration.
       float g = mx != mx ? INFINITY : mx;  // (a row with a NaN has no alternatives' values anyway)
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
       if ((lane & 7) == 0) sh.group[tid >> 3] = g;
       __syncthreads();
-      const int before = sh.count;
+      before = sh.count;
       g = sh.group[lane];
       int above = 0;  // groups before this one
-#pragma unroll
+#pragma unroll 8
       for (int j = 0; j < 32; ++j) {
         const float o = __shfl_sync(0xffffffffu, g, j);
         above += o > g || (o == g && j < lane);
       }
-      float low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == p.top - 1)) - 1);
+      low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == n_top - 1)) - 1);
       if (low == INFINITY) low = -INFINITY;
+      floor = just_below(low);
+      open = low == -INFINITY;
       __syncthreads();
-      if (mx >= low)
-        each([&](float v, int id) {
-          if (v > -INFINITY && v >= low) keep(v, id);
-        });
-      __syncthreads();
-      if (sh.count > kLpKeys) {  // (many equal ones): `top` times the best below the last
-        uint64_t last = ~0ull;
-#pragma unroll 1
-        for (int k = 0; k < p.top; ++k) {
-          uint64_t b = 0;
-          each([&](float v, int id) {
-            const uint64_t key = v > -INFINITY ? lp_key(v, id) : 0;
-            if (key < last) b = max(b, key);
-          });
-          last = lp_block_max(b, sh.warp_best[k & 1]);
-          if (tid == 0) sh.keys[before + k] = last;
-        }
-        if (tid == 0) sh.count = before + p.top;  // (zeros among them are no candidates)
-      }
-    } else if (mx > floor) {
-      // ids rise with the iterations: what only equals the floor comes behind those that made it
-      each([&](float v, int id) {
-        if (v > floor) keep(v, id);
-      });
     }
-    if (p.top && it >= next_cut) {  // after the iterations 0, 3, 15, ..
-      next_cut = open ? it + 1 : 4 * it + 3;
+    if (mx > floor) {
+      float v[U * E];  // (unpacked anew, not held in registers)
+      uint32_t some = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        asm volatile("" : "+r"(now[u].x), "+r"(now[u].y), "+r"(now[u].z), "+r"(now[u].w));
+        LpVec<T>::get(now[u], v + u * E);
+      }
+#pragma unroll
+      for (int i = 0; i < U * E; ++i) some |= v[i] > floor ? 1u << i : 0u;
+#pragma unroll 1
+      for (; some; some &= some - 1) {
+        const int k = __ffs(some) - 1;
+        float y = v[0];
+#pragma unroll
+        for (int i = 1; i < U * E; ++i) y = k == i ? v[i] : y;
+        keep(y, head + (i0 + k / E * kLpThreads + tid) * E + k % E);
+      }
+    }
+    if (opened) {
+      // ids rise with the iterations: what only equals the floor comes behind those that made it
+      floor = low;
+      __syncthreads();
+      if (sh.count > kLpKeys) {  // (many equal ones): the best `top` of this iteration's ids
+        __syncthreads();
+        lp_rounds(x, head + i0 * E, head + min(v1, i0 + kLpThreads * U) * E, n_top, sh.keys + before, sh);
+        if (tid == 0) sh.count = before + n_top;  // (zeros among them are no candidates)
+        __syncthreads();
+      }
+    }
+    // The floor rises with what has been seen, after the iterations 3, 15, 63, .. of longer parts.
+    if (it >= next_cut && i0 + 3 * kLpThreads * U < v1) {
+      next_cut = 4 * it + 3;
       __syncthreads();
       const int c = sh.count;
       lost = lost || c > kLpKeys;
       if (!lost) {
-        lp_select(sh.keys, c, p.top, sh.best);
-        if (tid < p.top) sh.keys[tid] = sh.best[tid];
-        if (tid == 0) sh.count = p.top;
-        open = sh.best[p.top - 1] == 0;
-        if (!open) floor = lp_key_value(sh.best[p.top - 1]);
+        lp_select(sh.keys, c, n_top, sh.best, sh);
+        if (tid < n_top) sh.keys[tid] = sh.best[tid];
+        if (tid == 0) sh.count = n_top;
+        if (sh.best[n_top - 1] != 0) {
+          open = false;
+          floor = lp_key_value(sh.best[n_top - 1]);
+        }
       }
       __syncthreads();
     }
@@ -331,8 +384,9 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
   if (rank == C - 1 && tail0 + tid < p.vocab) {
     const float v = ld_f(x + tail0 + tid);
     add(v);
-    if (p.top && v > -INFINITY && (open || v > floor)) keep(v, tail0 + tid);
+    if (kTopIds && v > floor) keep(v, tail0 + tid);
   }
+  RowSum a = {m, s2.x + s2.y, t2.x + t2.y};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     RowSum b;
@@ -343,25 +397,15 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
   }
   if (lane == 0) sh.part[warp] = a;
   __syncthreads();
-  if (p.top) {
+  if (kTopIds) {
     lost = lost || sh.count > kLpKeys;
     if (!lost) {
-      lp_select(sh.keys, sh.count, p.top, sh.best);
+      lp_select(sh.keys, sh.count, n_top, sh.best, sh);
     } else {
-      // More candidates than there is room for (logits that rise with the id): `top` times the
-      // best one below the last, over the whole part.
-      const int f0 = rank == 0 ? 0 : head + v0 * E, f1 = rank == C - 1 ? p.vocab : head + v1 * E;
-      uint64_t last = ~0ull;
-      for (int k = 0; k < p.top; ++k) {
-        uint64_t b = 0;
-        for (int i = f0 + tid; i < f1; i += kLpThreads) {
-          const float v = ld_f(x + i);
-          const uint64_t key = v > -INFINITY ? lp_key(v, i) : 0;
-          if (key < last && key > b) b = key;
-        }
-        last = lp_block_max(b, sh.warp_best[k & 1]);
-        if (tid == 0) sh.best[k] = last;
-      }
+      // More candidates than there was room for (logits that rise with the id): the same over the
+      // whole part.
+      lp_rounds(x, rank == 0 ? 0 : head + v0 * E, rank == C - 1 ? p.vocab : head + v1 * E, n_top, sh.best,
+                sh);
       __syncthreads();
     }
   }
@@ -373,34 +417,23 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
   RowSum r;
   const uint64_t* best = sh.best;
   if (C > 1) {
-    cluster_sync();
-    if (rank == 0) {
-      for (int i = tid; i < C * p.top; i += kLpThreads) {
-        const uint32_t at = map_peer(smem_u32(&sh.best[i % p.top]), i / p.top);
-        uint64_t k;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(at) : "memory");
-        sh.all[i] = k;
-      }
-      if (tid == 0) {
-        r = sh.sum;
-        for (int c = 1; c < C; ++c) {
-          const uint32_t at = map_peer(smem_u32(&sh.sum), c);
-          RowSum b;
-          b.m = ld_peer_f32(at);
-          b.s = ld_peer_f32(at + 4);
-          b.t = ld_peer_f32(at + 8);
-          r = join(r, b);
-        }
-        sh.part[0] = r;
-      }
+    // every part goes to the first CTA's shared memory
+    if (kTopIds && tid < n_top)
+      st_peer_u64(map_peer(smem_u32(&sh.all[rank * n_top + tid]), 0), sh.best[tid]);
+    if (tid == 0) {
+      const uint32_t at = map_peer(smem_u32(&sh.sums[rank]), 0);
+      st_peer_f32(at, sh.sum.m);
+      st_peer_f32(at + 4, sh.sum.s);
+      st_peer_f32(at + 8, sh.sum.t);
     }
-    cluster_sync();  // the others' shared memory has been read
+    cluster_sync();
     if (rank != 0) return;
-    r = sh.part[0];
-    if (p.top) {
-      lp_select(sh.all, C * p.top, p.top, sh.keys);
+    if (kTopIds) {
+      lp_select(sh.all, C * n_top, n_top, sh.keys, sh);
       best = sh.keys;
     }
+    r = sh.sums[0];
+    for (int c = 1; c < C; ++c) r = join(r, sh.sums[c]);
   } else {
     __syncthreads();
     r = sh.sum;
@@ -412,9 +445,9 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas) token_logprobs_ke
       p.logp[row] = tok >= p.vocab || !mass ? -INFINITY : (x_tok - r.m) - log_s;
     if (p.entropy) p.entropy[row] = mass ? log_s - r.t / r.s : 0.f;
   }
-  if (tid < p.top) {
+  if (tid < n_top) {
     const uint64_t k = best[tid];
-    const long long at = (long long)row * p.top + tid;
+    const long long at = (long long)row * n_top + tid;
     p.top_ids[at] = k ? (int)~(uint32_t)k : -1;
     p.top_logp[at] = k ? (lp_key_value(k) - r.m) - log_s : -INFINITY;
   }
@@ -451,7 +484,9 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
   p.top = top;
   int C = 1;
   while (C < kLpCluster && (int64_t)rows * C * 2 <= 2 * kvq_sms() && vocab > C * kLpStep) C *= 2;
-  const auto kernel = dtype == DFLASH_F32 ? token_logprobs_kernel<float> : token_logprobs_kernel<bf16>;
+  const auto kernel = dtype == DFLASH_F32
+                          ? (top ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>)
+                          : (top ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
   if (launch_k_cluster(true, dim3(C, 1, 1), kernel, dim3((unsigned)(rows * C)), dim3(kLpThreads),
                        sizeof(LpShared), (cudaStream_t)stream, p, C) != cudaSuccess)
     return DFLASH_E_CUDA;

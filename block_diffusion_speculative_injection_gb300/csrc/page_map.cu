@@ -18,7 +18,7 @@ namespace dflash {
 // 256 sequences with a block of 16 rows each, given back and mapped: _US_BLOCK_ us for both calls; 32 prompts
 // of 512 to 4096 rows (_ROWS_ rows, _BYTES_ MB of maps): _US_PROMPTS_ us.
 constexpr int kMapThreads = 1024, kMapBatch = 4096;
-constexpr int kMapCluster = 8, kMapRows = 2048;  // most CTAs; rows a CTA takes before there is another
+constexpr int kMapCluster = 8, kMapRows = 4096;  // most CTAs; rows a CTA takes before there is another
 
 struct PagesK {
   int32_t *table, *mapped, *free, *n_free, *status;
@@ -42,31 +42,43 @@ __host__ __device__ inline size_t map_smem_ints(int batch, int hash) {
   return 5 * (size_t)(batch + 1) + hash;
 }
 
-// Inclusive prefix sums of two values over the CTA's threads.
-__device__ __forceinline__ void block_scan2(long long& a, long long& b) {
-  __shared__ long long part[2][kMapThreads / 32];
+// Sums stay at kMapMany, which is above every count of rows and pages that a call can serve
+// (so 32 bits do, and saturating addition is still associative).
+constexpr int kMapMany = (1 << 30) - 1;
+__device__ __forceinline__ int add_sat(int a, int b) { return min(a + b, kMapMany); }
+
+// Prefix sums of two values (0..kMapMany) over the CTA's threads: what lies before this one; and all.
+__device__ __forceinline__ void block_scan2(int& a, int& b, int& all_a, int& all_b) {
+  __shared__ int2 part[kMapThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
     if (lane >= o) {
-      a += x;
-      b += y;
+      a = add_sat(a, x);
+      b = add_sat(b, y);
     }
   }
-  if (lane == 31) {
-    part[0][warp] = a;
-    part[1][warp] = b;
-  }
+  if (lane == 31) part[warp] = make_int2(a, b);
   __syncthreads();
-  long long pa = lane < warp ? part[0][lane] : 0, pb = lane < warp ? part[1][lane] : 0;
+  int2 p = part[lane];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    pa += __shfl_xor_sync(0xffffffffu, pa, o);
-    pb += __shfl_xor_sync(0xffffffffu, pb, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, p.x, o), y = __shfl_up_sync(0xffffffffu, p.y, o);
+    if (lane >= o) {
+      p.x = add_sat(p.x, x);
+      p.y = add_sat(p.y, y);
+    }
   }
-  a += pa;
-  b += pb;
+  static_assert(kMapThreads / 32 == 32, "a lane for each warp");
+  all_a = __shfl_sync(0xffffffffu, p.x, 31);
+  all_b = __shfl_sync(0xffffffffu, p.y, 31);
+  const int wa = __shfl_sync(0xffffffffu, p.x, max(warp - 1, 0));
+  const int wb = __shfl_sync(0xffffffffu, p.y, max(warp - 1, 0));
+  a = __shfl_up_sync(0xffffffffu, a, 1);
+  b = __shfl_up_sync(0xffffffffu, b, 1);
+  a = add_sat(lane > 0 ? a : 0, warp > 0 ? wa : 0);
+  b = add_sat(lane > 0 ? b : 0, warp > 0 ? wb : 0);
   __syncthreads();
 }
 
@@ -160,36 +172,36 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
   }
   // what each entry needs: rows and pages
   int rows[kPer], need[kPer];
-  long long sum_rows = 0, sum_need = 0;
+  int row = 0, page = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    rows[i] = max(e.c[i], 0);
+    rows[i] = min(max(e.c[i], 0), kMapMany);
     need[i] = 0;
     e.good[i] = e.good[i] && e.a[i] >= 0 && e.c[i] >= 0;
     bad = bad || (e.mine[i] && !e.good[i]);
     if (e.good[i]) {
-      const long long end = (long long)e.a[i] + rows[i];
+      const long long end = (long long)e.a[i] + e.c[i];
       e.good[i] = end <= (long long)k.p.pps * kPageSlots;
       if (e.good[i])
         need[i] = max(0, (int)((end + kPageSlots - 1) / kPageSlots) - e.have[i]);
       else
         full = true;
     }
-    sum_rows += rows[i];
-    sum_need += need[i];
+    row = add_sat(row, rows[i]);
+    page = add_sat(page, need[i]);
   }
-  long long end_rows = sum_rows, end_need = sum_need;
-  block_scan2(end_rows, end_need);
-  long long row = end_rows - sum_rows, page = end_need - sum_need;
+  int all_rows, all_need;
+  block_scan2(row, page, all_rows, all_need);
+  int at = page;
   bool odd = false;  // an entry that needs pages does not get them
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
     if (!e.mine[i]) break;
-    const int first = (int)min(row, (long long)k.n_rows);
-    const bool no_rows = row + rows[i] > k.n_rows;
-    row += rows[i];
-    page += need[i];
+    const int first = min(row, k.n_rows);
+    row = add_sat(row, rows[i]);
+    page = add_sat(page, need[i]);
+    const bool no_rows = row > k.n_rows;
     if (e.good[i] && ((need[i] > 0 && page > n_free) || no_rows)) {
       full = true;
       odd = odd || need[i] > 0;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
     s.off[b] = first;
     s.start[b] = e.good[i] ? e.a[i] : -1;
     if (b == k.batch - 1) {
-      const int all = (int)min(row, (long long)k.n_rows);
+      const int all = min(row, k.n_rows);
       if (rank == 0) k.offsets[k.batch] = all;
       s.off[k.batch] = all;
       full = full || row > k.n_rows;
@@ -212,22 +224,20 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
   if (bad) set_dev_status(k.p.status, kDevCheck);
   if (full) set_dev_status(k.p.status, kDevCapacity);
   // Pages are counted over the entries that get them: anew where some do not.
-  long long at = end_need - sum_need;
   if (__syncthreads_or(odd)) {
-    long long got = 0, none = 0;
+    int none = 0;
+    at = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) got += need[i];
-    long long end_got = got;
-    block_scan2(end_got, none);
-    at = end_got - got;
+    for (int i = 0; i < kPer; ++i) at += need[i];
+    block_scan2(at, none, all_need, all_rows);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
     if (!e.mine[i]) break;
-    s.base[b] = e.have[i] - (int)at;
+    s.base[b] = e.have[i] - at;
     at += need[i];
-    s.end[b] = (int)at;
+    s.end[b] = at;
   }
   __syncthreads();
   // The three numbers of each packed row.  A page is the table's, or, not there yet, the free list's.
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k
   MapEntries<kPer> e;
   const MapSmem s = map_begin(k, map_smem, e);
   int give[kPer], keep[kPer];
-  long long sum = 0, none = 0;
+  int at = 0, none = 0, total, no_total;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -300,17 +310,11 @@ __global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k
     if (!e.good[i]) continue;
     keep[i] = (int)(((long long)e.a[i] + kPageSlots - 1) / kPageSlots);
     give[i] = max(0, e.have[i] - keep[i]);
-    sum += give[i];
+    at = add_sat(at, give[i]);
   }
-  long long end = sum;
-  block_scan2(end, none);
-  long long at = end - sum;
-  __shared__ long long s_total;
-  if (tid == kMapThreads - 1) s_total = end;
-  __syncthreads();
+  block_scan2(at, none, total, no_total);
   // more pages than there are: the counts are not this pool's
-  const long long total = s_total;
-  if (n_free < 0 || total + n_free > k.p.n_pages) {
+  if (n_free < 0 || n_free > k.p.n_pages || total > k.p.n_pages - n_free) {
     if (tid == 0) set_dev_status(k.p.status, kDevCheck);
     return;
   }
@@ -319,19 +323,19 @@ __global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k
   for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
     if (!e.mine[i]) break;
-    s.base[b] = keep[i] - (int)at;
+    s.base[b] = keep[i] - at;
     at += give[i];
-    s.end[b] = (int)at;
+    s.end[b] = at;
     if (give[i] > 0) k.p.mapped[e.id[i]] = keep[i];
   }
   __syncthreads();
-  for (int i = tid; i < (int)total; i += kMapThreads) {
+  for (int i = tid; i < total; i += kMapThreads) {
     const int b = entry_above(s.end, k.batch, i);
     int32_t* const entry = k.p.table + (int64_t)s.id[b] * k.p.pps + s.base[b] + i;
     k.p.free[n_free + total - 1 - i] = *entry;
     *entry = -1;
   }
-  if (tid == 0 && total > 0) *k.p.n_free = n_free + (int)total;
+  if (tid == 0 && total > 0) *k.p.n_free = n_free + total;
 }
 
 static bool pages_ok(const dflash_pages* p) {
@@ -392,7 +396,7 @@ dflash_status dflash_pages_map(const dflash_pages* pages, int32_t batch, int32_t
                                const int32_t* seq_ids, const int32_t* start, const int32_t* counts,
                                int32_t* offsets, int32_t* kv_lens, int32_t* row_seq,
                                int32_t* row_pos, int32_t* row_slot, dflash_stream_t stream) {
-  if (!pages_ok(pages) || batch < 1 || batch > kMapBatch || n_rows < 0 || n_rows >= (1 << 30) ||
+  if (!pages_ok(pages) || batch < 1 || batch > kMapBatch || n_rows < 0 || n_rows >= (1 << 29) ||
       !counts || !offsets || !kv_lens ||
       !kvq_ints_aligned({seq_ids, start, counts, offsets, kv_lens, row_seq, row_pos, row_slot}))
     return DFLASH_E_INVALID_ARG;

@@ -75,7 +75,7 @@ class Pages:
                 self.mapped[q] += 1
         rows = []
         for b, (q, s, c) in enumerate(zip(seqs, start, counts)):
-            for j in range(max(c, 0)):
+            for j in range(min(max(c, 0), n_rows - len(rows))):
                 pos = s + j
                 rows.append((q, pos, self.table[q][pos // PAGE] * PAGE + pos % PAGE) if ok[b]
                             else (-1, -1, -1))
