@@ -158,11 +158,15 @@ __device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out, LpS
     keys = sh.shorter;
     c = sh.n_short;
   }
-  for (int i = tid; i < c; i += kLpThreads) {
-    const uint64_t k = keys[i];
+  // as many lanes a key as there are
+  const int shift = c > 128 ? 0 : c > 64 ? 1 : c > 32 ? 2 : 3, lanes = 1 << shift;
+  for (int i0 = 0; i0 < c; i0 += kLpThreads >> shift) {
+    const int i = i0 + (tid >> shift);
+    const uint64_t k = i < c ? keys[i] : 0;
     int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < c; ++j) rank += keys[j] > k;
+#pragma unroll 4
+    for (int j = tid & (lanes - 1); j < c; j += lanes) rank += keys[j] > k;
+    for (int o = lanes >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (k != 0 && rank < n) out[rank] = k;
   }
   __syncthreads();
@@ -220,16 +224,12 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   const int lane = tid & 31, warp = tid >> 5;
   const int n_top = kTopIds ? p.top : 0;
   const int tok = p.tokens ? p.tokens[row] : 0;
-  if (tok < 0) return;  // (the whole cluster) a row that is not in use
   const T* const x = static_cast<const T*>(p.logits) + (long long)row * p.stride;
   // the row: up to E - 1 ids before the first 16-byte boundary, whole vectors, up to E - 1 behind
   const int head = min(p.vocab, (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
   const int vecs = (p.vocab - head) / E, tail0 = head + vecs * E;
   const int v0 = (int)((long long)vecs * rank / C), v1 = (int)((long long)vecs * (rank + 1) / C);
   const uint4* const vec = reinterpret_cast<const uint4*>(x + head) + tid;
-  float x_tok = 0.f;
-  if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
-  if (tid == 0) sh.count = 0;
   uint4 next[U];
   auto fetch = [&](int i0) {
     if (i0 + kLpThreads * U <= v1) {
@@ -243,7 +243,11 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
                       : make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
     }
   };
-  fetch(v0);
+  fetch(v0);             // (before the token is there)
+  if (tok < 0) return;  // (the whole cluster) a row that is not in use
+  float x_tok = 0.f;
+  if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
+  if (tid == 0) sh.count = 0;
   float m = -INFINITY;  // this thread's maximum, and its sums in two parts each
   float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
   auto raise_to = [&](float top) {
@@ -308,7 +312,6 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
     }
     if (!kTopIds) continue;
     const bool opened = open;
-    int before = 0;
     float low = 0.f;
     if (opened) {
       // The maxima of 32 groups are 32 different values, so the top-th largest of them is no more
@@ -318,7 +321,6 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
       if ((lane & 7) == 0) sh.group[tid >> 3] = g;
       __syncthreads();
-      before = sh.count;
       g = sh.group[lane];
       int above = 0;  // groups before this one
 #pragma unroll 8
@@ -330,7 +332,6 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       if (low == INFINITY) low = -INFINITY;
       floor = just_below(low);
       open = low == -INFINITY;
-      __syncthreads();
     }
     if (mx > floor) {
       float v[U * E];  // (unpacked anew, not held in registers)
@@ -355,10 +356,12 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       // ids rise with the iterations: what only equals the floor comes behind those that made it
       floor = low;
       __syncthreads();
-      if (sh.count > kLpKeys) {  // (many equal ones): the best `top` of this iteration's ids
-        __syncthreads();
-        lp_rounds(x, head + i0 * E, head + min(v1, i0 + kLpThreads * U) * E, n_top, sh.keys + before, sh);
-        if (tid == 0) sh.count = before + n_top;  // (zeros among them are no candidates)
+      const bool many = sh.count > kLpKeys;
+      __syncthreads();
+      if (many) {  // (equal ones): the best `top` of the ids so far
+        lp_rounds(x, rank == 0 ? 0 : head + v0 * E, head + min(v1, i0 + kLpThreads * U) * E, n_top, sh.keys,
+                  sh);
+        if (tid == 0) sh.count = n_top;  // (zeros among them are no candidates)
         __syncthreads();
       }
     }
