@@ -76,7 +76,7 @@ template <typename T>
 struct LpVec;
 template <>
 struct LpVec<float> {
-  static constexpr int kN = 4, kAtOnce = 4, kCtas = 4;  // values; vectors a thread reads at once
+  static constexpr int kN = 4, kAtOnce = 4, kStages = 3, kCtas = 3;  // values; vectors a thread reads at once
   static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void get(uint4 r, float* x) {
     x[0] = __uint_as_float(r.x);
@@ -91,7 +91,7 @@ struct LpVec<float> {
 };
 template <>
 struct LpVec<bf16> {
-  static constexpr int kN = 8, kAtOnce = 2, kCtas = 5;
+  static constexpr int kN = 8, kAtOnce = 2, kStages = 4, kCtas = 5;
   static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ __forceinline__ void get(uint4 r, float* x) { bf16x8_to_f(r, x); }
   static __device__ __forceinline__ __nv_bfloat162 pair(const uint32_t& w) {
@@ -104,15 +104,7 @@ struct LpVec<bf16> {
   }
 };
 
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-struct LpShared {
+struct alignas(16) LpShared {
   uint64_t keys[kLpKeys];
   uint64_t shorter[kLpKeys];
   uint64_t group_key[kLpThreads / 8];
@@ -230,21 +222,31 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   const int vecs = (p.vocab - head) / E, tail0 = head + vecs * E;
   const int v0 = (int)((long long)vecs * rank / C), v1 = (int)((long long)vecs * (rank + 1) / C);
   const uint4* const vec = reinterpret_cast<const uint4*>(x + head) + tid;
-  uint4 next[U];
+  // A thread's vectors of the next iterations are on their way into its own places of shared
+  // memory (nobody else touches them, so there is nothing to synchronise).
+  constexpr int kStages = LpVec<T>::kStages;
+  uint4* const ring = reinterpret_cast<uint4*>(lp_smem + sizeof(LpShared)) + tid;
+  int fetched = 0;
   auto fetch = [&](int i0) {
+    const uint32_t dst = smem_u32(ring + fetched * (U * kLpThreads));
+    fetched = fetched + 1 == kStages ? 0 : fetched + 1;
     if (i0 + kLpThreads * U <= v1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) next[u] = ld_stream(vec + i0 + u * kLpThreads);
+      for (int u = 0; u < U; ++u) cp_async16(dst + u * kLpThreads * 16, vec + i0 + u * kLpThreads, 16);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        next[u] = i0 + u * kLpThreads + tid < v1
-                      ? ld_stream(vec + i0 + u * kLpThreads)
-                      : make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
+        if (i0 + u * kLpThreads + tid < v1)
+          cp_async16(dst + u * kLpThreads * 16, vec + i0 + u * kLpThreads, 16);
     }
+    cp_async_commit();
   };
-  fetch(v0);             // (before the token is there)
-  if (tok < 0) return;  // (the whole cluster) a row that is not in use
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) fetch(v0 + k * kLpThreads * U);  // (before the token is there)
+  if (tok < 0) {  // (the whole cluster) a row that is not in use
+    cp_async_wait<0>();
+    return;
+  }
   float x_tok = 0.f;
   if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
   if (tid == 0) sh.count = 0;
@@ -279,13 +281,21 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   bool lost = false;        // more candidates than there was room for
   float floor = -INFINITY;  // values up to here are no candidates any more
   int next_cut = 3;
-  int it = 0;
+  int it = 0, at = 0;
 #pragma unroll 1
   for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
     uint4 now[U];
+    cp_async_wait<kStages - 2>();
 #pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = next[u];
-    if (i0 + kLpThreads * U < v1) fetch(i0 + kLpThreads * U);
+    for (int u = 0; u < U; ++u) now[u] = ring[(at * U + u) * kLpThreads];
+    at = at + 1 == kStages ? 0 : at + 1;
+    if (i0 + kLpThreads * U > v1) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * kLpThreads + tid >= v1)
+          now[u] = make_uint4(LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone, LpVec<T>::kNone);
+    }
+    fetch(i0 + (kStages - 1) * kLpThreads * U);
     float mx = LpVec<T>::top(now[0]);
 #pragma unroll
     for (int u = 1; u < U; ++u) mx = max_nan(mx, LpVec<T>::top(now[u]));
@@ -383,6 +393,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       __syncthreads();
     }
   }
+  cp_async_wait<0>();
   // the ids behind the vectors
   if (rank == C - 1 && tail0 + tid < p.vocab) {
     const float v = ld_f(x + tail0 + tid);
@@ -456,6 +467,12 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   }
 }
 
+template <typename T>
+constexpr int lp_smem_size() {
+  return (int)sizeof(LpShared) + LpVec<T>::kStages * LpVec<T>::kAtOnce * kLpThreads * 16;
+}
+static_assert(DFLASH_F32 == 0 && DFLASH_BF16 == 1, "an index of smem_done");
+
 }  // namespace dflash
 
 using namespace dflash;
@@ -490,8 +507,12 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
   const auto kernel = dtype == DFLASH_F32
                           ? (top ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>)
                           : (top ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
+  static std::atomic<bool> smem_done[4][kMaxDevices];
+  const int lp_smem_bytes = dtype == DFLASH_F32 ? lp_smem_size<float>() : lp_smem_size<bf16>();
+  if (ensure_smem_attr(smem_done[2 * dtype + (top > 0)], kernel, lp_smem_bytes) != cudaSuccess)
+    return DFLASH_E_CUDA;
   if (launch_k_cluster(true, dim3(C, 1, 1), kernel, dim3((unsigned)(rows * C)), dim3(kLpThreads),
-                       sizeof(LpShared), (cudaStream_t)stream, p, C) != cudaSuccess)
+                       lp_smem_bytes, (cudaStream_t)stream, p, C) != cudaSuccess)
     return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
