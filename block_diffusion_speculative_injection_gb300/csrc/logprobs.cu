@@ -76,7 +76,7 @@ template <typename T>
 struct LpVec;
 template <>
 struct LpVec<float> {
-  static constexpr int kN = 4, kAtOnce = 4, kStages = 3, kCtas = 3;  // values; vectors a thread reads at once
+  static constexpr int kN = 4, kAtOnce = 4, kStages = 3, kCtas = 4;  // values; vectors a thread reads at once
   static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ void get(uint4 r, float* x) {
     x[0] = __uint_as_float(r.x);
@@ -104,64 +104,88 @@ struct LpVec<bf16> {
   }
 };
 
-struct alignas(16) LpShared {
+// (The ring behind these starts at a 128-byte line: without that a loop of loads takes 10 % longer.)
+struct alignas(128) LpSums {
+  RowSum part[kLpWarps];
+  RowSum sums[kLpCluster];   // of all parts, in the first CTA
+};
+struct alignas(128) LpLists {
   uint64_t keys[kLpKeys];
   uint64_t shorter[kLpKeys];
   uint64_t group_key[kLpThreads / 8];
   uint64_t best[kLpTop];     // the part's alternatives in order, 0 behind the last
   uint64_t all[kLpCluster * kLpTop];
   uint64_t warp_best[2][kLpWarps];
-  RowSum part[kLpWarps];
-  RowSum sum;                // the part's sums
-  RowSum sums[kLpCluster];   // all parts', in the first CTA
   float group[kLpThreads / 8];
   int count, n_short;
 };
 
-// The n best of c keys (all different but for zeros), in order, to out[0 .. n), zeros behind the
-// last; whole CTA.  Up to 256 each is ranked by counting.  Of more, the maxima of 32 groups are 32
-// different keys, and the n-th largest of them leaves a short list (of 768 random keys 31 for n = 20).
-__device__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out, LpShared& sh) {
+__host__ __device__ constexpr int lp_lists_size(bool top) {
+  return (int)(sizeof(LpSums) + (top ? sizeof(LpLists) : 0));
+}
+
+// Fewer keys than c with the n best among them, to sh.shorter; whole CTA.  The maxima of 32 groups
+// are 32 different keys (or zeros), and the n-th largest of them leaves a short list: of 768
+// random keys 31 for n = 20.
+__device__ __forceinline__ int lp_shorten(const uint64_t* keys, int c, int n, LpLists& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
-  uint64_t least = 1;
-  if (tid < n) out[tid] = 0;
-  if (tid == 0) sh.n_short = 0;
-  if (c > kLpThreads) {
-    uint64_t g = 0;
-    for (int i = tid; i < c; i += kLpThreads) g = max(g, keys[i]);
+  uint64_t g = 0;
+  for (int i = tid; i < c; i += kLpThreads) g = max(g, keys[i]);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if ((lane & 7) == 0) sh.group_key[tid >> 3] = g;
-    __syncthreads();
-    g = sh.group_key[lane];
-    int above = 0;
-#pragma unroll 1
-    for (int j = 0; j < 32; ++j) {
-      const uint64_t o = __shfl_sync(0xffffffffu, g, j);
-      above += o > g || (o == g && j < lane);
-    }
-    const int nth = __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1;
-    least = max(__shfl_sync(0xffffffffu, g, nth), least);
-    for (int i = tid; i < c; i += kLpThreads)
-      if (keys[i] >= least) sh.shorter[atomicAdd(&sh.n_short, 1)] = keys[i];
-  }
+  for (int o = 4; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if ((lane & 7) == 0) sh.group_key[tid >> 3] = g;
+  if (tid == 0) sh.n_short = 0;
   __syncthreads();
-  if (c > kLpThreads) {
-    keys = sh.shorter;
-    c = sh.n_short;
+  g = sh.group_key[lane];
+  int above = 0;
+#pragma unroll 1
+  for (int j = 0; j < 32; ++j) {
+    const uint64_t o = __shfl_sync(0xffffffffu, g, j);
+    above += o > g || (o == g && j < lane);
   }
-  // as many lanes a key as there are
-  const int shift = c > 128 ? 0 : c > 64 ? 1 : c > 32 ? 2 : 3, lanes = 1 << shift;
-  for (int i0 = 0; i0 < c; i0 += kLpThreads >> shift) {
-    const int i = i0 + (tid >> shift);
-    const uint64_t k = i < c ? keys[i] : 0;
+  const int nth = __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1;
+  const uint64_t least = max(__shfl_sync(0xffffffffu, g, nth), (uint64_t)1);
+  for (int i = tid; i < c; i += kLpThreads)
+    if (keys[i] >= least) sh.shorter[atomicAdd(&sh.n_short, 1)] = keys[i];
+  __syncthreads();
+  return sh.n_short;
+}
+
+// The n best of c keys (all different but for zeros), in order, to out[0 .. n), zeros behind the
+// last; whole CTA.  Each is ranked by counting.
+__device__ __forceinline__ void lp_select(const uint64_t* keys, int c, int n, uint64_t* out,
+                                          LpLists& sh) {
+  const int tid = threadIdx.x;
+  if (tid < n) out[tid] = 0;
+  if (c > kLpThreads) {
+    c = lp_shorten(keys, c, n, sh);
+    keys = sh.shorter;
+  } else {
+    __syncthreads();
+  }
+  for (int i = tid; i < c; i += kLpThreads) {
+    const uint64_t k = keys[i];
     int rank = 0;
-#pragma unroll 4
-    for (int j = tid & (lanes - 1); j < c; j += lanes) rank += keys[j] > k;
-    for (int o = lanes >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+#pragma unroll 8
+    for (int j = 0; j < c; ++j) rank += keys[j] > k;
     if (k != 0 && rank < n) out[rank] = k;
   }
   __syncthreads();
+}
+
+// join of the first n (a power of two, up to 32) sums, by a whole warp; in every lane
+__device__ __forceinline__ RowSum lp_join(const RowSum* sums, int n) {
+  RowSum a = sums[threadIdx.x & (n - 1)];
+#pragma unroll 1
+  for (int o = n >> 1; o > 0; o >>= 1) {
+    RowSum b;
+    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+    // (in the order of the lanes, so that all have the same)
+    a = (threadIdx.x & o) ? join(b, a) : join(a, b);
+  }
+  return a;
 }
 
 // largest of the threads' keys, in every thread; two calls in a row use different buffers
@@ -178,7 +202,7 @@ __device__ __forceinline__ uint64_t lp_block_max(uint64_t b, uint64_t* buffer) {
 
 // The n best of ids f0 .. f1 - 1 in order, one after the other, to out; whole CTA.
 template <typename T>
-__device__ __noinline__ void lp_rounds(const T* x, int f0, int f1, int n, uint64_t* out, LpShared& sh) {
+__device__ __noinline__ void lp_rounds(const T* x, int f0, int f1, int n, uint64_t* out, LpLists& sh) {
   uint64_t last = ~0ull;
 #pragma unroll 1
   for (int k = 0; k < n; ++k) {
@@ -205,13 +229,14 @@ __device__ __forceinline__ float just_below(float x) {
 // the next iteration's loads under way while it works on this one's.  (What it takes: fp32 15 and
 // bf16 9 instructions a logit with the shares of everything else.)
 template <typename T, bool kTopIds>
-__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
+__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && sizeof(T) == 4 ? 1 : 0))
     token_logprobs_kernel(const LogpK p, const int C) {
   pdl_trigger();
   pdl_wait();
   constexpr int E = LpVec<T>::kN, U = LpVec<T>::kAtOnce;
   extern __shared__ __align__(16) uint8_t lp_smem[];
-  LpShared& sh = *reinterpret_cast<LpShared*>(lp_smem);
+  LpSums& sums = *reinterpret_cast<LpSums*>(lp_smem);
+  LpLists& sh = *reinterpret_cast<LpLists*>(lp_smem + sizeof(LpSums));  // (with alternatives only)
   const int row = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int n_top = kTopIds ? p.top : 0;
@@ -225,7 +250,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   // A thread's vectors of the next iterations are on their way into its own places of shared
   // memory (nobody else touches them, so there is nothing to synchronise).
   constexpr int kStages = LpVec<T>::kStages;
-  uint4* const ring = reinterpret_cast<uint4*>(lp_smem + sizeof(LpShared)) + tid;
+  uint4* const ring = reinterpret_cast<uint4*>(lp_smem + lp_lists_size(kTopIds)) + tid;
   int fetched = 0;
   auto fetch = [&](int i0) {
     const uint32_t dst = smem_u32(ring + fetched * (U * kLpThreads));
@@ -249,7 +274,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
   }
   float x_tok = 0.f;
   if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
-  if (tid == 0) sh.count = 0;
+  if (kTopIds && tid == 0) sh.count = 0;
   float m = -INFINITY;  // this thread's maximum, and its sums in two parts each
   float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
   auto raise_to = [&](float top) {
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
     b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
     a = join(a, b);
   }
-  if (lane == 0) sh.part[warp] = a;
+  if (lane == 0) sums.part[warp] = a;
   __syncthreads();
   if (kTopIds) {
     lost = lost || sh.count > kLpKeys;
@@ -423,22 +448,18 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       __syncthreads();
     }
   }
-  if (tid == 0) {
-    RowSum r = sh.part[0];
-    for (int w = 1; w < kLpWarps; ++w) r = join(r, sh.part[w]);
-    sh.sum = r;
-  }
-  RowSum r;
   const uint64_t* best = sh.best;
+  RowSum r;
+  if (warp == 0) r = lp_join(sums.part, kLpWarps);
   if (C > 1) {
     // every part goes to the first CTA's shared memory
     if (kTopIds && tid < n_top)
       st_peer_u64(map_peer(smem_u32(&sh.all[rank * n_top + tid]), 0), sh.best[tid]);
     if (tid == 0) {
-      const uint32_t at = map_peer(smem_u32(&sh.sums[rank]), 0);
-      st_peer_f32(at, sh.sum.m);
-      st_peer_f32(at + 4, sh.sum.s);
-      st_peer_f32(at + 8, sh.sum.t);
+      const uint32_t to = map_peer(smem_u32(&sums.sums[rank]), 0);
+      st_peer_f32(to, r.m);
+      st_peer_f32(to + 4, r.s);
+      st_peer_f32(to + 8, r.t);
     }
     cluster_sync();
     if (rank != 0) return;
@@ -446,12 +467,9 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
       lp_select(sh.all, C * n_top, n_top, sh.keys, sh);
       best = sh.keys;
     }
-    r = sh.sums[0];
-    for (int c = 1; c < C; ++c) r = join(r, sh.sums[c]);
-  } else {
-    __syncthreads();
-    r = sh.sum;
+    if (warp == 0) r = lp_join(sums.sums, C);
   }
+  if (warp != 0) return;  // (up to 32 alternatives)
   const bool mass = r.m != -INFINITY;
   const float log_s = logf(r.s);
   if (tid == 0) {
@@ -468,8 +486,8 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas)
 }
 
 template <typename T>
-constexpr int lp_smem_size() {
-  return (int)sizeof(LpShared) + LpVec<T>::kStages * LpVec<T>::kAtOnce * kLpThreads * 16;
+constexpr int lp_smem_size(bool top) {
+  return lp_lists_size(top) + LpVec<T>::kStages * LpVec<T>::kAtOnce * kLpThreads * 16;
 }
 static_assert(DFLASH_F32 == 0 && DFLASH_BF16 == 1, "an index of smem_done");
 
@@ -508,7 +526,7 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
                           ? (top ? token_logprobs_kernel<float, true> : token_logprobs_kernel<float, false>)
                           : (top ? token_logprobs_kernel<bf16, true> : token_logprobs_kernel<bf16, false>);
   static std::atomic<bool> smem_done[4][kMaxDevices];
-  const int lp_smem_bytes = dtype == DFLASH_F32 ? lp_smem_size<float>() : lp_smem_size<bf16>();
+  const int lp_smem_bytes = dtype == DFLASH_F32 ? lp_smem_size<float>(top > 0) : lp_smem_size<bf16>(top > 0);
   if (ensure_smem_attr(smem_done[2 * dtype + (top > 0)], kernel, lp_smem_bytes) != cudaSuccess)
     return DFLASH_E_CUDA;
   if (launch_k_cluster(true, dim3(C, 1, 1), kernel, dim3((unsigned)(rows * C)), dim3(kLpThreads),
