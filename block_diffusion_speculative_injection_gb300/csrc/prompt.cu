@@ -541,8 +541,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
           if (far) {
+            const float2 minus_m = make_float2(-m_next, -m_next);
 #pragma unroll
-            for (int i = 0; i < kPT; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - m_next);
+            for (int i = 0; i < kPT; i += 2) {
+              const float2 y =
+                  add2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), minus_m);
+              s[i] = __float_as_uint(y.x);
+              s[i + 1] = __float_as_uint(y.y);
+            }
             base = 0.f;
           }
         }
@@ -577,47 +583,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
       }
-      // ---- the rows' results
-      if (ok) ok = wait(&sh.o_full[x], mine);
-      if (!ok) break;
-      tc_fence_after();
-      float o[kPromptHd];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_o + 32 * c, reinterpret_cast<uint32_t*>(o) + 32 * c);
+      // ---- the rows' results.  (Rolled, and as little as can be behind the wait: this code runs once
+      // an item, and the instruction cache has forgotten it by then.)
       const float inv = l == 0.f ? 0.f : rcp(l);
       const int n_live = min(p.pos, it.n - p0) * p.G;  // rows of the prompt
       // first of the tile's rows: position p0, the first head of this KV head
       const long long row0 = (long long)(it.first + p0) * p.H + it.kvh * p.G;
-      const int off = g_pos * (p.H - p.G) + row;  // this thread's from there
       if (row < n_live && p.lse)
-        p.lse[row0 + off] = l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
-      const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.o_empty[x]);  // O may be overwritten
+        p.lse[row0 + g_pos * (p.H - p.G) + row] =
+            l == 0.f ? -INFINITY : (m * kPScaleLog2 + log2f(l)) * kPLn2;
       // Out through shared memory, 64 dims at a time (16 bytes at chunk c ^ row): a row a lane would
       // touch 32 lines an instruction, so 32 turns of the memory pipe instead of 4.  A warp whose 32
       // rows are all the prompt's, and whole positions, leaves them to one bulk copy.
       uint8_t* const out_rows = sm + kPOffOut + warp * kPOutBytes;
-      uint8_t* const out_row_mine = out_rows + lane * 128;
       const int rr0 = (warp & 3) * 32;
       const bool bulk = p.box_out && rr0 + 32 <= n_live;
-#pragma unroll
+      if (ok) ok = wait(&sh.o_full[x], mine);
+      if (!ok) break;
+      tc_fence_after();
+      const bool bad = *const_cast<volatile int*>(&sh.bad[past.items % kPSlots]) != 0;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 y = mul2(make_float2(o[64 * half + 2 * i], o[64 * half + 2 * i + 1]), inv);
-          const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
         if (lane == 0) bulk_wait_read();  // what was here before has left
         __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld32_nowait(t_o + 64 * half + 32 * c, o);
+          tmem_wait_ld();
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(out_row_mine + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(out_rows + lane * 128 + (((4 * c + i) ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        if (half == 1) {  // O may be overwritten
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_empty[x]);
+        }
         if (bad && row < n_live) {
           // what this row sees of the elements that were replaced by zeros
 #pragma unroll 1
@@ -626,7 +636,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
             for (int d = 0; d < 64; ++d) {
               const float f = ld_f(v + d);
-              bf16* const y = reinterpret_cast<bf16*>(out_row_mine + (((d >> 3) ^ (lane & 7)) << 4)) + (d & 7);
+              bf16* const y = reinterpret_cast<bf16*>(out_rows + lane * 128 + (((d >> 3) ^ (lane & 7)) << 4)) +
+                              (d & 7);
               if (!(fabsf(f) < INFINITY)) st_f(y, ld_f(y) + f);
             }
           }
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         } else {
           __syncwarp();
-#pragma unroll
+#pragma unroll 2
           for (int i = lane; i < 32 * 8; i += 32) {
             const int r = i >> 3, c = i & 7, g = (rr0 + r) * p.g_inv >> 16;
             if (rr0 + r < n_live)
@@ -740,7 +751,7 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.g_inv = 65536 / p.G + 1;
   p.box_out = 32 % p.G == 0;
   // two query tiles a CTA, but one where the CTAs would be fewer than the SMs
-  p.tiles = packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads < kvq_sms() ? 1 : 2;
+  p.tiles = 2 * packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads <= kvq_sms() ? 1 : 2;
   const int64_t units = packed_units(n_rows, batch, p.tiles * p.pos, 1);
   if (units * n_kv_heads >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;
   p.n_units = (int)units;
