@@ -40,7 +40,8 @@ __device__ __forceinline__ int packed_find(const int32_t* offsets, int batch, co
     const int n = __popc(__ballot_sync(0xffffffffu, below));
     if (n == 0) return -1;
     lo += (n - 1) * step;
-    if (step == 1) return lo;
+    // (in a list that is not in order, the last of n probes need not be one of those below)
+    if (step == 1) return packed_base(offsets, lo, u) <= at ? lo : -1;
     end = min(end, lo + step);
   }
 }

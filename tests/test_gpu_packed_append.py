@@ -92,6 +92,24 @@ def test_bad_entries_set_the_status(kw, status):
     assert e.value.status == status
 
 
+def test_many_bad_offsets_write_nothing_elsewhere():
+    """Sequence 3 is nobody's: its pages stay as they are."""
+    rng = np.random.default_rng(0)
+    c = filled(2, 4, 2, [1, 1, 1, 100], 5)
+    before = [t.clone() for t in pool(c)]
+    x = torch.ones(40, 4, HD, dtype=torch.bfloat16, device="cuda")
+    for _ in range(30):
+        off = rng.integers(-30, 70, 4)
+        off[1] = off[2] + 1  # never in order
+        capi().dflash_kvq_append_packed(c.h, 3, None, i32([0, 200, 17]), i32(off), x[:, :2], x[:, 2:])
+        with pytest.raises(capi().DFlashError):
+            capi().dflash_kvq_check(c.h)
+    mine = torch.from_numpy(c.table[3]).long().cuda()
+    spare = sorted(set(range(before[0].shape[0])) - set(c.table.reshape(-1).tolist()))
+    keep = torch.cat([mine, torch.tensor(spare, device="cuda")])
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(before, pool(c)))
+
+
 def test_packed_prompts_from_lengths_to_log_probabilities():
     """As a server would, captured once and replayed with other lengths: pages from the lengths,
     K and V into the 8-bit cache, attention of the prompts, log probabilities of their tokens; then

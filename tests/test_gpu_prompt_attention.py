@@ -203,14 +203,38 @@ def test_runs_are_equal():
         assert all(torch.equal(a, b) for a, b in zip(first, c.run(True)))
 
 
-@pytest.mark.parametrize("off", [[0, 50, 40, 90], [0, 50, 60, 91], [-1, 50, 60, 90], [60, 50, 40, 0]])
+BAD = [[0, 50, 40, 90], [0, 50, 60, 91], [-1, 50, 60, 90], [60, 50, 40, 0], [0, -5, 20, 90], [0, 1 << 25, 3, 90],
+       [0, 90, 10, 50], [-2 ** 31, 2 ** 31 - 1, -7, 90], [90, 90, 0, 90]]
+
+
+@pytest.mark.parametrize("off", BAD)
 def test_bad_offsets_set_the_status(off):
+    """And nothing outside the arrays is written."""
     c = Case([50, 10, 30], 1, 4, seed=1)
-    c.run(True, offsets=i32(off))
+    q, k, v = c.qkv
+    wide = torch.full((c.T + 400, c.H, HD), 3.0, dtype=torch.bfloat16, device="cuda")
+    wide_lse = torch.full((c.T + 400, c.H), 3.0, device="cuda")
+    status = i32([0])
+    capi().dflash_prompt_attention(3, True, i32(off), q, k, v, wide[200:200 + c.T], wide_lse[200:200 + c.T], status)
     with pytest.raises(capi().DFlashError) as e:
-        capi().dflash_status_check(c.status)
+        capi().dflash_status_check(status)
     assert e.value.status == 5
-    capi().dflash_status_check(c.status)  # and clears
+    capi().dflash_status_check(status)  # and clears
+    for w in (wide, wide_lse):
+        assert (w[:200] == 3.0).all() and (w[200 + c.T:] == 3.0).all()
+
+
+def test_many_bad_offsets():
+    rng = np.random.default_rng(0)
+    c = Case([300], 2, 4, seed=1)
+    q, k, v = c.qkv
+    wide = torch.full((c.T + 400, c.H, HD), 3.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(20):
+        off = rng.integers(-40, 360, 101)
+        status = i32([0])
+        capi().dflash_prompt_attention(100, True, i32(off), q, k, v, wide[200:200 + c.T], None, status)
+        assert int(status) == 3
+    assert (wide[:200] == 3.0).all() and (wide[200 + c.T:] == 3.0).all()
 
 
 def test_captured_with_other_lengths_and_streams():
