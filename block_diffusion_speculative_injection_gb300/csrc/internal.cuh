@@ -459,6 +459,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// In two steps: that every CTA of the cluster has started, so that its shared memory may be
+// written, is arrived at early and waited for late.
+__device__ __forceinline__ void cluster_started_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // address of the same shared-memory offset in cluster CTA `rank`
 __device__ __forceinline__ uint32_t map_peer(uint32_t smem_addr, uint32_t rank) {
   uint32_t r;

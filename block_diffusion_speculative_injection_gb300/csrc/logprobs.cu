@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
     cp_async_wait<0>();
     return;
   }
+  if (C > 1) cluster_started_arrive();
   float x_tok = 0.f;
   if (rank == 0 && tid == 0 && p.tokens && tok < p.vocab) x_tok = ld_f(x + tok);
   if (kTopIds && tid == 0) sh.count = 0;
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
   if (warp == 0) r = lp_join(sums.part, kLpWarps);
   if (C > 1) {
     // every part goes to the first CTA's shared memory
+    cluster_started_wait();
     if (kTopIds && tid < n_top)
       st_peer_u64(map_peer(smem_u32(&sh.all[rank * n_top + tid]), 0), sh.best[tid]);
     if (tid == 0) {
