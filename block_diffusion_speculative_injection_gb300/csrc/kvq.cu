@@ -45,7 +45,8 @@ __device__ __forceinline__ uint2 code_row(const float* x, float s) {
 // 8 heads (92 MB) take 21 us, 4.3 TB/s.
 //
 // Packed rows: `rows` in all, and n_blk units of 16 of them; the r rows of a sequence touch up
-// to floor(r / 16) + 2 blocks.
+// to floor(r / 16) + 2 blocks.  79,838 rows of 8 heads in 32 sequences (491 MB) take 80 us,
+// 6.1 TB/s (91 % of a plain copy's rate).
 // ---------------------------------------------------------------------------
 struct AppendK {
   KvqK c;
@@ -661,6 +662,21 @@ int kvq_sms() {
     sms[dev].store(n, std::memory_order_relaxed);
   }
   return n;
+}
+
+static bool ranges_overlap(const MemRange& a, const MemRange& b) {
+  if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes;
+}
+bool ranges_apart(const MemRange* out, int n_out, const MemRange* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(out[i], out[j])) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (ranges_overlap(out[i], in[j])) return false;
+  }
+  return true;
 }
 
 KvqK kvq_device_view(const dflash_kvq_cache* c) {

@@ -119,4 +119,12 @@ inline bool kvq_ints_aligned(std::initializer_list<const int32_t*> ptrs) {
   return true;
 }
 
+// `bytes` bytes from p on (p NULL: none)
+struct MemRange {
+  const void* p;
+  int64_t bytes;
+};
+// whether nothing of out[0 .. n_out) overlaps another of them or an input
+bool ranges_apart(const MemRange* out, int n_out, const MemRange* in, int n_in);
+
 }  // namespace dflash

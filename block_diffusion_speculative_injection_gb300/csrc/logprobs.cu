@@ -6,6 +6,12 @@
 //   log p_t = d_t - log S,  entropy = -sum p_i log p_i = log S - T / S.
 // S and T of parts of a row with maxima m1 <= m join as
 //   S += f S1,  T += f (T1 + (m1 - m) S1),  f = e^(m1 - m).
+//
+// Bound by memory where rows fill the GPU: 2048 rows of 128,256 in bf16 take 84 us, 6.3 TB/s (92 % of
+// a plain copy's rate).  With 20 alternatives 512 rows of 151,936 in fp32, 384 of them in use, take
+// 43.4 us, 5.4 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
+// time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 20
+// alternatives take 10 us, where their bytes take 1.4.
 #include <cmath>
 
 #include "attn_util.cuh"
@@ -71,7 +77,11 @@ __device__ __forceinline__ float lp_key_value(uint64_t k) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// 16 bytes of logits: the values, the largest (NaN passes), and a word of -inf
+// 16 bytes of logits: the values, the largest (NaN passes), and a word of -inf.
+// kAtOnce vectors a thread and iteration, kStages iterations' places in shared memory, kCtas CTAs an
+// SM.  152 rows of 151,936 in fp32: 10.2 us with 4 x 3 at 4 CTAs, 11.6 with 2 x 4 at 5, 21.5 with
+// 4 x 2 at 5.  With alternatives fp32 needs the registers of 3 CTAs, and in bf16 the lists leave
+// room for 4 (lists short enough for 5: 512 rows 57 us instead of 49, 2000 rows 143 instead of 148).
 template <typename T>
 struct LpVec;
 template <>
@@ -225,9 +235,9 @@ __device__ __forceinline__ float just_below(float x) {
   return x == 0.f ? __int_as_float((int)0x80000001u) : __int_as_float(b > 0 ? b - 1 : b + 1);
 }
 
-// A row's part of a CTA: the cluster of C CTAs shares the row out.  Bound by memory: each thread has
-// the next iteration's loads under way while it works on this one's.  (What it takes: fp32 15 and
-// bf16 9 instructions a logit with the shares of everything else.)
+// A row's part of a CTA: the cluster of C CTAs shares the row out.  Each thread has the next
+// iterations' loads under way while it works on this one's.  (What it takes: fp32 15 and bf16 9
+// instructions a logit with the shares of everything else.)
 template <typename T, bool kTopIds>
 __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && sizeof(T) == 4 ? 1 : 0))
     token_logprobs_kernel(const LogpK p, const int C) {
@@ -306,7 +316,12 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
   bool open = true;         // not known yet to have `top` candidates
   bool lost = false;        // more candidates than there was room for
   float floor = -INFINITY;  // values up to here are no candidates any more
-  int next_cut = 3;
+  // The floor rises with what has been seen after iteration next_cut, then 4 times as many.  The
+  // n-th largest of 32 groups' maxima leaves 32 (H(32) - H(32 - n)) candidates an iteration on
+  // average (H: harmonic numbers): 22 for n = 16, but 130 for 32, whose four iterations would often
+  // overflow the list (512 rows, 32 alternatives: 1373 us; cut after the first iteration 70).  A
+  // cut too many costs 0.3 us of 10.
+  int next_cut = n_top > kLpTop / 2 ? 0 : 3;
   int it = 0, at = 0;
 #pragma unroll 1
   for (int i0 = v0; i0 < v1; i0 += kLpThreads * U, ++it) {
@@ -401,7 +416,6 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
         __syncthreads();
       }
     }
-    // The floor rises with what has been seen, after the iterations 3, 15, 63, .. of longer parts.
     if (it >= next_cut && i0 + 3 * kLpThreads * U < v1) {
       next_cut = 4 * it + 3;
       __syncthreads();
@@ -510,6 +524,14 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
       !kvq_aligned(logits, dtype == DFLASH_F32 ? 4 : 2) || !kvq_aligned(logp, 4) ||
       !kvq_aligned(entropy, 4) || !kvq_aligned(top_logp, 4) || !kvq_ints_aligned({tokens, top_ids}))
     return DFLASH_E_INVALID_ARG;
+  // (rows that would lie past any memory: their addresses would not fit 64 bits either)
+  if (rows - 1 >= ((int64_t)1 << 48) / row_stride) return DFLASH_E_INVALID_ARG;
+  // What is written must be nothing that other CTAs still read, nor another output.
+  const int64_t words = 4 * (int64_t)rows;
+  const MemRange out[] = {{logp, words}, {entropy, words}, {top_ids, words * top}, {top_logp, words * top}};
+  const MemRange in[] = {{logits, ((rows - 1) * row_stride + vocab) * (dtype == DFLASH_F32 ? 4 : 2)},
+                         {tokens, words}};
+  if (!ranges_apart(out, 4, in, 2)) return DFLASH_E_INVALID_ARG;
   const void* const ptrs[] = {logits, tokens, logp, entropy, top_ids, top_logp};
   DF_TRY(kvq_ptrs_ok(ptrs, 6));
   LogpK p;
@@ -522,6 +544,10 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
   p.top_logp = top_logp;
   p.vocab = vocab;
   p.top = top;
+  // A row to several CTAs while there are no more than two an SM, and each has more than an
+  // iteration: 16 rows of 151,936 with 5 alternatives take 9.7 us by 8 CTAs each and 19 by one; 100
+  // rows with 20 take 26 by two and 32 by one.  Beyond that it gains nothing (256 rows: 41.9 us by two,
+  // 41.6 by one) and soon costs, since every CTA makes a selection of its own (512 rows: 66.5, 64.1).
   int C = 1;
   while (C < kLpCluster && (int64_t)rows * C * 2 <= 2 * kvq_sms() && vocab > C * kLpStep) C *= 2;
   const auto kernel = dtype == DFLASH_F32

@@ -42,7 +42,7 @@ struct PromptMaps {
 //
 // m is the largest score when it was taken and is raised only when a tile's largest exceeds it
 // by more than 2^8 in the weights: then the row of O in tensor memory and the sum l are rescaled.  Any
-// consistent m gives the same O / l.  A weight is rounded to bf16 (half a step: 2^-9) because V is
+// consistent m gives the same O / l.  A weight is rounded to bf16 (by up to 2^-8 of it) because V is
 // bf16 and both operands of a product have one type; the sum l takes it unrounded.
 //
 // Keys behind a row's own position, or the prompt's end, have weight 0, which keeps finite values
@@ -50,11 +50,27 @@ struct PromptMaps {
 // whole, a warp replaces those by zeros in shared memory.  If there were any, the rows that do see
 // them add them to their results at the end.
 //
-// Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle): Q 2 x 32 KB, a ring of five
-// stages of 32 KB for K and V in the order K0 K1 V0 K2 V1 ..  Tensor memory: S and O of both tiles, all
-// 512 columns.
+// Shared memory (1024-aligned, rows of 128 B, 128-byte swizzle): Q 2 x 32 KB, a ring of four
+// stages of 32 KB for K and V in the order K0 K1 V0 K2 V1 .., 32 KB for results on their way out.
+// Tensor memory: S and O of both tiles, all 512 columns.
 // Warps 0-3, 4-7: softmax of tile 0 and 1.  Warp 8: TMA.  Warps 9, 10: the tiles' MMAs, O(j) and
 // then S(j + 1), so that S(j + 1) follows the last read of P(j), which it overwrites.  Warp 11: V.
+//
+// A CTA that is done with its two tiles takes on those of one that has not started, so that loads and
+// scores of the next item begin under the results of the last, and the items, longest first, end
+// together (32 ragged prompts: 1.68 -> 1.38 ms).
+//
+// What bounds it: a step of both tiles is 8.4 MFLOP x 4 = 33.6 MFLOP of products an SM, 1.35 us at
+// 1.89 PFLOP/s over 152 SMs.  Long prompts reach that (four of 8192, bidirectional, 32 heads); one of
+// 16,384 causal tokens takes 1.2 ms, 1.8 PFLOP/s.  Shorter prompts pay 2.6 us for each change of
+// items (the last step's chain, the results, the first scores) and some 0.25 us more for a step
+// with a mask: 32 prompts of 512 to 4096 take 1.23 ms, 1.53 PFLOP/s.  One of 2048 is 28 us, 16 steps
+// in a row and two more changes; three short ones 6.7 us, a launch and one step.
+//
+// Measured and left: three stages instead of four (with the room, five) and P in one or four parts
+// (slower); results by separate warps (slower: registers); items known three ahead, and the next
+// CTA asked for three steps early (2048 tokens: 34 us instead of 30); V cleaned by the softmax
+// warps in front of their stores (2 % slower).
 // ---------------------------------------------------------------------------
 constexpr int kPT = 128;                       // rows of a query tile, keys of a step
 constexpr uint32_t kPBox = kPT * 128;          // 128 rows of 64 dims
@@ -87,10 +103,10 @@ struct PromptItem {
   int clean;             // first key tile that not every row sees whole
   int kvh;
 };
-constexpr int kPParts = 2;   // of P: a part's products begin while the next is computed
-constexpr int kPSlots = 2;   // items known ahead
-constexpr int kPAskLate = 1; // steps
-constexpr int kPClean = 4;   // barriers of the cleaned tiles, used in turn
+constexpr int kPParts = 2;    // of P: a part's products begin while the next is computed
+constexpr int kPSlots = 2;    // items known ahead
+constexpr int kPAskLate = 1;  // steps
+constexpr int kPClean = 4;    // barriers of the cleaned tiles, used in turn
 struct PromptShared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kPParts], o_full[2], o_empty[2], issued[2], drained[2];
   uint64_t raw_full[kPClean], clean[kPClean];
@@ -677,13 +693,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 static bool prompt_stride_ok(int64_t stride, int heads) {
   return stride >= (int64_t)heads * kPromptHd && stride % 8 == 0 && stride < ((int64_t)1 << 31);
 }
-// bytes [p, p + n)
-static bool prompt_overlap(const void* p, int64_t n, const void* q, int64_t m) {
-  if (!p || !q) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
-  return x < y ? y - x < (uint64_t)n : x - y < (uint64_t)m;
-}
-
 // bf16 rows [n_rows] of `heads` heads, boxes of 64 dims, box_heads heads and box_rows rows
 static bool prompt_map(CUtensorMap* m, const void* ptr, int heads, int n_rows, int64_t row_stride,
                        int box_heads, int box_rows) {
@@ -714,24 +723,17 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
       !kvq_ints_aligned({offsets, status}))
     return DFLASH_E_INVALID_ARG;
   // What is written must be nothing that other CTAs still read, nor the other output.
-  struct Range {
-    const void* p;
-    int64_t n;
-  };
   auto bytes = [&](int64_t stride, int heads) {
     return ((n_rows - 1) * stride + (int64_t)heads * kPromptHd) * 2;
   };
-  const Range in[] = {{q, bytes(q_row_stride, n_heads)},
+  const MemRange in[] = {{q, bytes(q_row_stride, n_heads)},
                       {k, bytes(k_row_stride, n_kv_heads)},
                       {v, bytes(v_row_stride, n_kv_heads)},
                       {offsets, ((int64_t)batch + 1) * 4},
                       {status, 4}};
-  const Range o[] = {{out, (int64_t)n_rows * n_heads * kPromptHd * 2},
+  const MemRange o[] = {{out, (int64_t)n_rows * n_heads * kPromptHd * 2},
                      {lse, (int64_t)n_rows * n_heads * 4}};
-  for (const Range& w : o)
-    for (const Range& r : in)
-      if (prompt_overlap(w.p, w.n, r.p, r.n)) return DFLASH_E_INVALID_ARG;
-  if (prompt_overlap(o[0].p, o[0].n, o[1].p, o[1].n)) return DFLASH_E_INVALID_ARG;
+  if (!ranges_apart(o, 2, in, 5)) return DFLASH_E_INVALID_ARG;
   const void* const ptrs[] = {offsets, q, k, v, out, lse, status};
   DF_TRY(kvq_ptrs_ok(ptrs, 7));
   PromptK p;
@@ -750,7 +752,9 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.pos = kPT / p.G;
   p.g_inv = 65536 / p.G + 1;
   p.box_out = 32 % p.G == 0;
-  // two query tiles a CTA, but one where the CTAs would be fewer than the SMs
+  // Two query tiles a CTA, each beside the other's softmax; one while that leaves no SM two CTAs.  32
+  // and 8 heads, one prompt of 256: 7.4 us by one tile, 8.3 by two; 512: 10.7 and 11.1; 1024:
+  // 19.5 and 16.9, bidirectional 26.7 and 16.9.
   p.tiles = 2 * packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads <= kvq_sms() ? 1 : 2;
   const int64_t units = packed_units(n_rows, batch, p.tiles * p.pos, 1);
   if (units * n_kv_heads >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;

@@ -607,17 +607,17 @@ DFLASH_API dflash_status dflash_kvq_check(const dflash_kvq_cache *cache, dflash_
  * A server takes prompts of different lengths as one run of rows: sequence b's
  * rows are offsets[b] .. offsets[b + 1] - 1 of n_rows, offsets [batch + 1] int32 on
  * the device, ascending within [0, n_rows].  Rows before the first sequence and behind
- * the last are left as they were.  These calls carry such a batch from the requests' lengths to
- * pages (dflash_pages_map), into the 8-bit cache (dflash_kvq_append_packed),
- * through the attention of each layer (dflash_prompt_attention) and from the logits to
- * log probabilities (dflash_token_logprobs).  The pages have no counterpart; the calls are
- * the library's own.
+ * the last are left as they were.  These calls carry such a batch from the requests'
+ * lengths to pages (dflash_pages_map), into the 8-bit cache (dflash_kvq_append_packed),
+ * through the attention of each layer (dflash_prompt_attention) and from the logits to log
+ * probabilities (dflash_token_logprobs).  The pages have no counterpart; the calls are the
+ * library's own.
  * They follow the rules of the 8-bit cache's calls: all pointers are device memory of
- * the current device (else DFLASH_E_INVALID_ARG), calls only enqueue work on `stream` and
- * keep nothing between calls, and what a kernel finds wrong is left in a status word
+ * the current device (else DFLASH_E_INVALID_ARG), calls only enqueue work on `stream`
+ * and keep nothing between calls, and what a kernel finds wrong is left in a status word
  * (one int32, zero at the start; the first failure stays), read and cleared by
- * dflash_status_check or, where it is a cache's, dflash_kvq_check.  Offsets that are not in
- * order or leave [0, n_rows] set DFLASH_E_DEVICE_CHECK; what is written then is
+ * dflash_status_check or, where it is a cache's, dflash_kvq_check.  Offsets that are not
+ * in order or leave [0, n_rows] set DFLASH_E_DEVICE_CHECK; what is written then is
  * unspecified, but nothing outside the arrays. */
 
 /* Pages of a cache, mapped on the GPU: the counterpart of dflash_kv_pool_* for
@@ -637,20 +637,23 @@ typedef struct {
 } dflash_pages;
 
 /* Maps pages so that sequence seq_ids[b] (NULL: b) covers slots 0 .. start[b] +
- * counts[b] - 1 (start NULL: 0), and lays out the packed batch of those new rows.  Entries
- * are served in order: entry b's new pages are the next ones off the free list.  Where the
- * free pages do not suffice for entry b, it and every later entry that needs any get none
- * (status DFLASH_E_CAPACITY); so does an entry past pages_per_seq * 128 slots or past n_rows
- * packed rows.  A bad id, a negative start or count, or a sequence that an earlier entry names
- * sets DFLASH_E_DEVICE_CHECK.  Such an entry changes no page and keeps its length.
- *   offsets_dev  [batch + 1] out: sums of the counts (negative ones count as 0), at most n_rows
- *   kv_lens_dev  [batch] out: start + count; start (0 where that is negative) for a refused entry
+ * counts[b] - 1 (start NULL: 0), and lays out the packed batch of those new rows.
+ * Entries are served in order: entry b's new pages are the next ones off the free list.
+ * Where the free pages do not suffice for entry b, it and every later entry that needs
+ * any get none (status DFLASH_E_CAPACITY); so does an entry past pages_per_seq * 128
+ * slots or past n_rows packed rows.  A bad id, a negative start or count, or a sequence
+ * that an earlier entry names sets DFLASH_E_DEVICE_CHECK.  Such an entry changes no page
+ * and keeps its length.
+ *   offsets_dev  [batch + 1] out: sums of the counts (negative ones count as 0), at most
+ *                n_rows
+ *   kv_lens_dev  [batch] out: start + count; start (0 where that is negative) for a
+ *                refused entry
  *   row_seq_dev, row_pos_dev, row_slot_dev  [n_rows] out, each or NULL: sequence,
- *                position (start + j, the form dflash_inject_kv takes) and cache slot (page *
- *                128 + row within the page) of each packed row; -1 for the rows of
- *                refused entries and behind the last sequence
- * batch 1..4096; n_rows >= 0 bounds the sum of the counts.  No array written may overlap
- * another or an input. */
+ *                position (start + j, the form dflash_inject_kv takes) and cache slot
+ *                (page * 128 + row within the page) of each packed row; -1 for the rows
+ *                of refused entries and behind the last sequence
+ * batch 1..4096; n_rows 0 .. 2^29 - 1 bounds the sum of the counts.  No array written may
+ * overlap another or an input. */
 DFLASH_API dflash_status dflash_pages_map(const dflash_pages *pages, int32_t batch, int32_t n_rows,
                                           const int32_t *seq_ids_dev, const int32_t *start_dev,
                                           const int32_t *counts_dev, int32_t *offsets_dev,
@@ -659,10 +662,10 @@ DFLASH_API dflash_status dflash_pages_map(const dflash_pages *pages, int32_t bat
                                           dflash_stream_t stream);
 
 /* Gives back the pages of sequences seq_ids[b] (NULL: b) behind their first keep[b]
- * slots (NULL: 0, all of them).  Pages go to the end of the free list in such an order that
- * mapping the same entries again takes the same pages.  A bad id, a negative keep or a sequence that an
- * earlier entry names changes nothing (DFLASH_E_DEVICE_CHECK); so does the whole call where
- * the list would hold more than n_pages.  batch 1..4096. */
+ * slots (NULL: 0, all of them).  Pages go to the end of the free list in such an order
+ * that mapping the same entries again takes the same pages.  A bad id, a negative keep or
+ * a sequence that an earlier entry names changes nothing (DFLASH_E_DEVICE_CHECK); so does
+ * the whole call where the list would hold more than n_pages.  batch 1..4096. */
 DFLASH_API dflash_status dflash_pages_release(const dflash_pages *pages, int32_t batch,
                                               const int32_t *seq_ids_dev, const int32_t *keep_dev,
                                               dflash_stream_t stream);
@@ -671,12 +674,13 @@ DFLASH_API dflash_status dflash_pages_release(const dflash_pages *pages, int32_t
  * capture). */
 DFLASH_API dflash_status dflash_status_check(int32_t *status_dev, dflash_stream_t stream);
 
-/* dflash_kvq_append of a packed batch: rows offsets[b] .. of K and V go to slots start[b],
- * start[b] + 1, .. of sequence seq_ids[b] (NULL: b), with the same codes and exponents as
- * that call's.
+/* dflash_kvq_append of a packed batch: rows offsets[b] .. of K and V go to slots
+ * start[b], start[b] + 1, .. of sequence seq_ids[b] (NULL: b), with the same codes and
+ * exponents as that call's.
  *   k_dev, v_dev  [n_rows] rows of n_kv_heads * 128 bf16, row_stride elements apart (>=
  *                 n_kv_heads * 128, a multiple of 8), 16-byte aligned
- *   start_dev [batch], offsets_dev [batch + 1] */
+ *   start_dev [batch], offsets_dev [batch + 1]
+ * n_rows 1 .. 2^30 - 1, batch 1 .. 2^26 - 1, (n_rows / 16 + 2 batch) * n_kv_heads < 2^30. */
 DFLASH_API dflash_status dflash_kvq_append_packed(const dflash_kvq_cache *cache, int32_t batch,
                                                   int32_t n_rows, const int32_t *seq_ids_dev,
                                                   const int32_t *start_dev,
@@ -684,23 +688,25 @@ DFLASH_API dflash_status dflash_kvq_append_packed(const dflash_kvq_cache *cache,
                                                   const void *v_dev, int64_t k_row_stride,
                                                   int64_t v_row_stride, dflash_stream_t stream);
 
-/* Attention of every prompt of a packed batch over itself: row i of a prompt of n rows,
- * query head h (KV head h / (n_heads / n_kv_heads)) gets
+/* Attention of every prompt of a packed batch over itself: row i of a prompt of n
+ * rows, query head h (KV head h / (n_heads / n_kv_heads)) gets
  *   out = sum_k p_k v_k,  p = softmax over its keys of q_i . k_k / sqrt(128),
  * its keys being rows 0 .. i of the prompt (causal = 1) or all n (causal = 0).  bf16,
  * head_dim 128; n_heads / n_kv_heads 1..64.
- * Scores, weights' sums and the accumulated output are in fp32, a weight is rounded to bf16
- * where it meets V, the result is rounded to bf16.  Rows that a row does not see do not enter its
- * result, NaN included; an infinity or NaN in a V row it does see makes that element of its
- * result an infinity or NaN, whatever the weight.
- *   q_dev        [n_rows] rows of n_heads * 128, q_row_stride elements apart (>= n_heads * 128, a
- *                multiple of 8: a slice of a fused projection's output), 16-byte aligned
+ * Scores, sums of weights and the accumulated output are in fp32; a weight is rounded to
+ * bf16 where it meets V, and the result is.  Rows that a row does not see do not enter
+ * its result, NaN included; an infinity or NaN in a V row it does see makes that element
+ * of its result an infinity or NaN, whatever the weight.
+ *   q_dev        [n_rows] rows of n_heads * 128, q_row_stride elements apart (>= n_heads
+ *                * 128, a multiple of 8: a slice of a fused projection's output), 16-byte
+ *                aligned
  *   k_dev, v_dev [n_rows] rows of n_kv_heads * 128, likewise
  *   out_dev      [n_rows][n_heads][128], 16-byte aligned
- *   lse_dev      [n_rows][n_heads] float or NULL: natural log of the sum of exp(q . k / sqrt(128))
- *                (what dflash_kvq_score takes)
+ *   lse_dev      [n_rows][n_heads] float or NULL: natural log of the sum of exp(q . k /
+ *                sqrt(128)) (what dflash_kvq_score takes)
  *   status_dev   one int32
- * out and lse must not overlap the inputs. */
+ * batch 1 .. 2^26 - 1, n_rows 1 .. 2^26 - 1, n_heads up to 65535.  out and lse must not
+ * overlap the inputs or each other. */
 DFLASH_API dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_heads,
                                                  int32_t n_kv_heads, int32_t causal,
                                                  const int32_t *offsets_dev, const void *q_dev,
@@ -710,19 +716,22 @@ DFLASH_API dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, 
                                                  float *lse_dev, int32_t *status_dev,
                                                  dflash_stream_t stream);
 
-/* For each row of logits (temperature 1) the log probability of a given token, the entropy
- * (natural log) of the distribution and its `top` best ids with their log probabilities
- * (logit descending, ties lowest id), all from one read.
+/* For each row of logits (temperature 1) the log probability of a given token, the
+ * entropy (natural log) of the distribution and its `top` best ids with their log
+ * probabilities (logit descending, ties lowest id), all from one read.
  *   dtype        DFLASH_F32 or DFLASH_BF16; rows row_stride elements apart (>= vocab)
- *   tokens_dev   [rows] int32: < 0: the row is not in use, its logits are not read and its
- *                outputs are left as they were; >= vocab: logp -inf.  NULL (with logp NULL): all rows in use
+ *   tokens_dev   [rows] int32: < 0: the row is not in use, its logits have no
+ *                influence and its outputs are left as they were; >= vocab: logp -inf.
+ *                NULL (with logp NULL): all rows in use
  *   logp_dev     [rows] float or NULL
  *   entropy_dev  [rows] float or NULL
  *   top_ids_dev  [rows][top] int32, top_logp_dev [rows][top] float (NULL with top = 0)
- * Logits of -inf have no probability: they are no alternatives (id -1, log probability -inf
- * where fewer than `top` others are left), and a row of nothing else gives logp -inf and
- * entropy 0.  A row with a NaN or +inf gives NaN for each number, and any ids.  Sums are in fp32, in a
- * fixed order: equal inputs give equal outputs.  rows < 2^27, vocab < 2^30, top 0..32. */
+ * Logits of -inf have no probability: they are no alternatives (id -1, log probability
+ * -inf where fewer than `top` others are left), and a row of nothing else gives logp
+ * -inf and entropy 0.  A row with a NaN or +inf gives NaN for each number, and any
+ * ids.  Sums are in fp32, in a fixed order: equal inputs give equal outputs.  rows
+ * 1 .. 2^27 - 1, vocab 1 .. 2^30 - 1, top 0..32; no array written may overlap another
+ * or an input. */
 DFLASH_API dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype,
                                                const void *logits_dev, int64_t row_stride,
                                                const int32_t *tokens_dev, int32_t top,

@@ -109,10 +109,15 @@ def test_packed_append_refuses(lib, kw):
     {"rows": 0}, {"rows": 1 << 27}, {"vocab": 0}, {"vocab": 1 << 30, "stride": 1 << 30}, {"dtype": 2}, {"dtype": -1},
     {"x": None}, {"stride": 99}, {"stride": 1 << 40}, {"top": -1}, {"top": 33}, {"tokens": None},
     {"ids": None}, {"best": None}, {"lp": None, "en": None, "top": 0}, {"x": A + 2}, {"dtype": 1, "x": A + 1},
-    {"lp": A + 2}, {"en": A + 1}, {"best": A + 2}, {"tokens": A + 2}, {"ids": A + 3},
+    {"lp": 3 * A + 2}, {"en": 4 * A + 1}, {"best": 6 * A + 2}, {"tokens": 2 * A + 2}, {"ids": 5 * A + 3},
+    {"rows": 1 << 20, "stride": 1 << 39, "vocab": 100, "x": FAR},
+    # outputs over inputs, or over each other
+    {"lp": A}, {"lp": A + 1196}, {"en": A - 8}, {"ids": A + 400}, {"best": A - 44}, {"lp": 2 * A}, {"ids": 2 * A + 8},
+    {"lp": 4 * A + 8}, {"ids": 6 * A}, {"best": 3 * A - 40},
 ])
 def test_logprobs_refuse(lib, kw):
-    d = dict(rows=3, vocab=100, dtype=0, x=A, stride=100, tokens=A, top=4, lp=A, en=A, ids=A, best=A)
+    d = dict(rows=3, vocab=100, dtype=0, x=A, stride=100, tokens=2 * A, top=4, lp=3 * A, en=4 * A, ids=5 * A,
+             best=6 * A)
     d.update(kw)
     assert lib.dflash_token_logprobs(*d.values(), None) == 1
 
