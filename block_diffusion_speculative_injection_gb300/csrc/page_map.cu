@@ -30,7 +30,8 @@ struct MapK {
   const int32_t *seq_ids, *start, *counts;  // release: start holds the slots kept
   int32_t *offsets, *kv_lens, *row_seq, *row_pos, *row_slot;
   int batch, n_rows;
-  int hash;  // places of the table of ids, a power of two >= 2 * batch
+  int hash;        // places of the table of ids, a power of two >= 2 * batch
+  int hash_shift;  // 32 - log2(hash)
 };
 
 // Shared memory: per entry its id, the pages taken up to and with it, and where in the
@@ -83,10 +84,10 @@ __device__ __forceinline__ void block_scan2(int& a, int& b, int& all_a, int& all
   __syncthreads();
 }
 
-// Places in the table of ids: an id's place keeps the first entry that names it.
+// Places in the table of ids: an id's place keeps the first entry that names it.  (Multiples of 2^32
+// times the golden ratio fall apart, so neighbouring ids hardly ever meet.)
 __device__ __forceinline__ int id_place(const MapK& k, const MapSmem& s, int id, int b, bool insert) {
-  uint32_t h = (uint32_t)id * 2654435761u;
-  h ^= h >> 15;
+  uint32_t h = (uint32_t)id * 2654435769u >> k.hash_shift;
   for (int i = 0; i < k.hash; ++i, ++h) {  // (at most half of the places are taken)
     const int at = (int)(h & (uint32_t)(k.hash - 1));
     const int held = insert ? atomicCAS(&s.seen[at], -1, b) : s.seen[at];
@@ -131,16 +132,19 @@ __device__ __forceinline__ MapSmem map_begin(const MapK& k, int32_t* sm, MapEntr
     e.have[i] = e.good[i] ? k.p.mapped[e.id[i]] : 0;
     if (e.mine[i]) s.id[b0 + i] = e.id[i];
   }
-  for (int i = threadIdx.x; i < k.hash; i += kMapThreads) s.seen[i] = -1;
-  __syncthreads();
+  if (k.seq_ids) {
+    for (int i = threadIdx.x; i < k.hash; i += kMapThreads) s.seen[i] = -1;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (e.good[i]) id_place(k, s, e.id[i], b0 + i, true);
-  __syncthreads();
+    for (int i = 0; i < kPer; ++i)
+      if (e.good[i]) id_place(k, s, e.id[i], b0 + i, true);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    e.good[i] = e.good[i] && id_place(k, s, e.id[i], b0 + i, false) == b0 + i && e.have[i] >= 0 &&
-                e.have[i] <= k.p.pps;
+    for (int i = 0; i < kPer; ++i)
+      e.good[i] = e.good[i] && id_place(k, s, e.id[i], b0 + i, false) == b0 + i;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) e.good[i] = e.good[i] && e.have[i] >= 0 && e.have[i] <= k.p.pps;
   return s;
 }
 
@@ -365,7 +369,8 @@ static MapK map_args(const dflash_pages* p, int batch, const int32_t* seq_ids, c
   k.start = start;
   k.batch = batch;
   k.hash = 64;
-  while (k.hash < 2 * batch) k.hash *= 2;
+  k.hash_shift = 26;
+  for (; k.hash < 2 * batch; k.hash *= 2) --k.hash_shift;
   return k;
 }
 
