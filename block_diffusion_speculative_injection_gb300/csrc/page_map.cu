@@ -15,11 +15,12 @@ namespace dflash {
 // sequences' counts, page ids).  A CTA walks the whole batch, kPer consecutive entries a thread.  For
 // the maps of many rows a cluster of CTAs does so, each for all entries, and shares the rows out; what
 // the call reads and changes is changed after all of them have read it.
-// 256 sequences with a block of 16 rows each, given back and mapped: 12.8 us for both calls; 32 prompts
-// of 512 to 4096 rows (79,838 rows, 0.96 MB of maps): 17.8 us.  With one CTA these are 14.2 and
-// 57 us; with eight for 128 sequences with a block each 12.0 instead of 11.9, for one 5.6 instead of 5.2.
+// 256 sequences with a block of 16 rows each, given back and mapped: 7.9 us for both calls (9.3
+// by one CTA, 8.8 by two); 32 prompts of 512 to 4096 rows (79,838 rows, 0.96 MB of maps): 12.4 us, 8
+// SMs' instructions for the maps' rows.
 constexpr int kMapThreads = 1024, kMapBatch = 4096;
 constexpr int kMapCluster = 8, kMapRows = 1024;  // most CTAs; rows a CTA takes before there is another
+constexpr int kMapRuns = 4;                      // rows a thread has under way
 
 struct PagesK {
   int32_t *table, *mapped, *free, *n_free, *status;
@@ -32,6 +33,7 @@ struct MapK {
   int batch, n_rows;
   int hash;        // places of the table of ids, a power of two >= 2 * batch
   int hash_shift;  // 32 - log2(hash)
+  int runs;        // of 32 rows a warp takes at once, 1..kMapRuns
 };
 
 // Shared memory: per entry its id, the pages taken up to and with it, and where in the
@@ -148,9 +150,9 @@ __device__ __forceinline__ MapSmem map_begin(const MapK& k, int32_t* sm, MapEntr
   return s;
 }
 
-// first entry whose `end` is above i
-__device__ __forceinline__ int entry_above(const int32_t* end, int batch, int i) {
-  int lo = 0, hi = batch - 1;
+// first entry, from lo on, whose `end` is above i
+__device__ __forceinline__ int entry_above(const int32_t* end, int batch, int i, int lo = 0) {
+  int hi = batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (end[mid] > i)
@@ -246,17 +248,20 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
   }
   __syncthreads();
   // The three numbers of each packed row.  A page is the table's, or, not there yet, the free list's.
+  // (A warp takes up to kMapRuns runs of 32 rows: a thread's next row is mostly of the same entry.)
   if (k.row_seq || k.row_pos || k.row_slot) {
-    const int stride = C * kMapThreads, n_packed = s.off[k.batch];
-    constexpr int kAtOnce = 4;
-    for (int r0 = rank * kMapThreads + tid; r0 < k.n_rows; r0 += kAtOnce * stride) {
-      int seq[kAtOnce], pos[kAtOnce], pg[kAtOnce];
+    const int n_packed = s.off[k.batch];
+    const int runs = k.runs;
+    for (int r0 = (rank * kMapThreads + (tid & ~31)) * runs + (tid & 31); r0 < k.n_rows;
+         r0 += runs * C * kMapThreads) {
+      int seq[kMapRuns], pos[kMapRuns], pg[kMapRuns];
+      int b = 0;
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int r = r0 + i * stride;
+      for (int i = 0; i < kMapRuns; ++i) {
+        const int r = r0 + i * 32;
         seq[i] = pos[i] = pg[i] = -1;
-        if (r >= n_packed) continue;
-        const int b = entry_above(s.off + 1, k.batch, r);
+        if (i >= runs || r >= n_packed) continue;
+        if (i == 0 || s.off[b + 1] <= r) b = entry_above(s.off + 1, k.batch, r, b);
         if (s.start[b] < 0) continue;
         seq[i] = s.id[b];
         pos[i] = s.start[b] + (r - s.off[b]);
@@ -266,9 +271,9 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
                     : k.p.table[(int64_t)seq[i] * k.p.pps + in_seq];
       }
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int r = r0 + i * stride;
-        if (r >= k.n_rows) break;
+      for (int i = 0; i < kMapRuns; ++i) {
+        const int r = r0 + i * 32;
+        if (i >= runs || r >= k.n_rows) break;
         if (k.row_seq) k.row_seq[r] = seq[i];
         if (k.row_pos) k.row_pos[r] = pos[i];
         if (k.row_slot)
@@ -414,6 +419,7 @@ dflash_status dflash_pages_map(const dflash_pages* pages, int32_t batch, int32_t
   int C = 1;
   if (row_seq || row_pos || row_slot)
     while (C < kMapCluster && C * kMapRows < n_rows) C *= 2;
+  k.runs = std::max(1, std::min(kMapRuns, n_rows / (C * kMapThreads)));
   static std::atomic<bool> smem_done[2][kMaxDevices];
   const int big = batch > kMapThreads;
   const auto kernel = big ? pages_map_kernel<kMapBatch / kMapThreads> : pages_map_kernel<1>;
