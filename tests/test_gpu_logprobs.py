@@ -73,6 +73,22 @@ def test_against_oracle(rows, vocab, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("top", [16, 17, 31, 32])
+def test_long_rows_of_a_cta_each(top, dtype):
+    """The list of alternatives is cut several times: scattered logits, a few values many times,
+    and a list that overflows."""
+    R, vocab = 310, 70001
+    gen = torch.Generator(device="cuda").manual_seed(top)
+    x = (torch.randn(R, vocab, device="cuda", generator=gen) * 2).to(dtype)
+    x[1] = torch.randint(-5, 6, (vocab,), device="cuda", generator=gen).to(dtype)
+    x[2] = (torch.arange(vocab, device="cuda") * 2.0 ** -8).to(dtype)
+    tokens = torch.randint(0, vocab, (R,), device="cuda", generator=gen).to(torch.int32)
+    got = run(x, tokens, top)
+    check(x[:12], tokens[:12], top, [g[:12] for g in got])
+    check(x[-3:], tokens[-3:], top, [g[-3:] for g in got])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad", [1, 2, 3, 5])
 def test_strides_and_misaligned_rows(pad, dtype):
     gen = torch.Generator(device="cuda").manual_seed(pad)

@@ -148,6 +148,30 @@ def test_both_forms_of_the_rows_maps(n_rows):
     q.same()
 
 
+@pytest.mark.parametrize("n_rows", [1023, 1024, 1025, 2049, 8193, 16385, 33000])
+def test_rows_over_several_ctas(n_rows):
+    """Empty and refused entries among long and short ones, and rows behind the last."""
+    rng = np.random.default_rng(n_rows)
+    B = 50
+    counts = rng.integers(0, 2 * n_rows // B, B)
+    counts[rng.permutation(B)[:20]] = 0
+    counts[B // 2:B // 2 + 10] = rng.integers(0, 4, 10)
+    start = rng.integers(0, 300, B)
+    start[7] = -1
+    p = Pool(sum(-(-(int(c) + 300) // PAGE) for c in counts), B, 2 * n_rows // B // PAGE + 5)
+    p.map(rng.permutation(B).tolist(), start.tolist(), counts.tolist(), n_rows)
+
+
+def test_ids_that_meet_in_a_table():
+    """Ids whose multiples of the golden ratio lie together, some of them twice."""
+    ids = [i for i in range(6000) if i * 2654435769 % 2 ** 32 < 2 ** 26][:40]
+    assert len(ids) == 40
+    p = Pool(100, 6000, 2)
+    seqs = ids + [ids[3], ids[39]] + list(range(40, 60))
+    p.map(seqs, [0] * len(seqs), [1 + i for i in range(len(seqs))])
+    p.release(seqs[::-1], [0] * len(seqs))
+
+
 def test_captured_and_replayed():
     p = Pool(64, 4, 8)
     seqs, start, counts = i32([1, 3]), i32([0, 0]), i32([16, 16])
