@@ -9,9 +9,9 @@
 //
 // Bound by memory where rows fill the GPU: 2048 rows of 128,256 in bf16 take 84 us, 6.3 TB/s (92 % of
 // a plain copy's rate).  With 20 alternatives 512 rows of 151,936 in fp32, 384 of them in use, take
-// 43.4 us, 5.4 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
+// 42.4 us, 5.5 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
 // time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 20
-// alternatives take 10 us, where their bytes take 1.4.
+// alternatives take 9.7 us, where their bytes take 1.4.
 #include <cmath>
 
 #include "attn_util.cuh"
@@ -235,6 +235,70 @@ __device__ __forceinline__ float just_below(float x) {
   return x == 0.f ? __int_as_float((int)0x80000001u) : __int_as_float(b > 0 ? b - 1 : b + 1);
 }
 
+// The n-th largest of 32 groups' maxima of the threads' values (NaN counts as +inf), -inf for a +inf
+// (a row with a +inf or NaN has no alternatives' values anyway); whole CTA.  The maxima are 32
+// different values, so it is no more than the n-th best of all.
+__device__ __forceinline__ float lp_group_floor(float mx, int n, LpLists& sh) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  float g = mx != mx ? INFINITY : mx;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if ((lane & 7) == 0) sh.group[tid >> 3] = g;
+  __syncthreads();
+  g = sh.group[lane];
+  int above = 0;  // groups before this one
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const float o = __shfl_sync(0xffffffffu, g, j);
+    above += o > g || (o == g && j < lane);
+  }
+  const float low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1);
+  return low == INFINITY ? -INFINITY : low;
+}
+
+// The n best of what the list holds become the list, and sh.best; whole CTA.
+__device__ __forceinline__ void lp_cut(int n, LpLists& sh) {
+  lp_select(sh.keys, min(sh.count, kLpKeys), n, sh.best, sh);
+  if (threadIdx.x < n) sh.keys[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) sh.count = n;  // (zeros among them are no candidates)
+  __syncthreads();
+}
+
+// The list had no room for all candidates of ids f0 .. f1 - 1 (logits that rise with the id): these
+// ids anew, above the n-th best of the ids before them and above their own groups' floor; if that
+// is too many as well (many equal ones), one after the other.  Whole CTA; then as lp_cut.  (512 rows
+// of 151,936 in fp32, 20 alternatives: 63 us; with logits that are three standard deviations higher
+// from id 9000 on 90, with ascending ones 293.)
+template <typename T>
+__device__ __noinline__ void lp_overflow(const T* x, int f0, int f1, int n, LpLists& sh) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < min(sh.count, kLpKeys); i += kLpThreads)
+    if ((int)~(uint32_t)sh.keys[i] >= f0) sh.keys[i] = 0;
+  __syncthreads();
+  lp_cut(n, sh);
+  const float before = sh.best[n - 1] != 0 ? lp_key_value(sh.best[n - 1]) : -INFINITY;
+  float mx = -INFINITY;
+#pragma unroll 16
+  for (int i = f0 + tid; i < f1; i += kLpThreads) mx = max_nan(mx, ld_f(x + i));
+  const float least = fmaxf(before, just_below(lp_group_floor(mx, n, sh)));
+#pragma unroll 16
+  for (int i = f0 + tid; i < f1; i += kLpThreads) {
+    const float v = ld_f(x + i);
+    if (v > least) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kLpKeys) sh.keys[at] = lp_key(v, i);
+    }
+  }
+  __syncthreads();
+  if (sh.count > kLpKeys) {
+    lp_rounds(x, f0, f1, n, sh.keys + n, sh);
+    __syncthreads();
+    if (tid == 0) sh.count = 2 * n;
+    __syncthreads();
+  }
+  lp_cut(n, sh);
+}
+
 // A row's part of a CTA: the cluster of C CTAs shares the row out.  Each thread has the next
 // iterations' loads under way while it works on this one's.  (What it takes: fp32 15 and bf16 9
 // instructions a logit with the shares of everything else.)
@@ -306,6 +370,15 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
     const int at = atomicAdd(&sh.count, 1);
     if (at < kLpKeys) sh.keys[at] = lp_key(v, id);
   };
+  // the n best of the ids up to `end` become the list, those from `begun` on having been added to it
+  int begun = head + v0 * E;
+  auto cut = [&](int end) {
+    if (sh.count > kLpKeys)
+      lp_overflow(x, begun, end, n_top, sh);
+    else
+      lp_cut(n_top, sh);
+    begun = end;
+  };
   if (kTopIds) __syncthreads();
   // the ids before the vectors: candidates with the first ones
   if (rank == 0 && tid < head) {
@@ -314,13 +387,11 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
     if (kTopIds && v > -INFINITY) keep(v, tid);
   }
   bool open = true;         // not known yet to have `top` candidates
-  bool lost = false;        // more candidates than there was room for
   float floor = -INFINITY;  // values up to here are no candidates any more
   // The floor rises with what has been seen after iteration next_cut, then 4 times as many.  The
   // n-th largest of 32 groups' maxima leaves 32 (H(32) - H(32 - n)) candidates an iteration on
   // average (H: harmonic numbers): 22 for n = 16, but 130 for 32, whose four iterations would often
-  // overflow the list (512 rows, 32 alternatives: 1373 us; cut after the first iteration 70).  A
-  // cut too many costs 0.3 us of 10.
+  // overflow the list.  A cut too many costs 0.3 us of 10.
   int next_cut = n_top > kLpTop / 2 ? 0 : 3;
   int it = 0, at = 0;
 #pragma unroll 1
@@ -365,22 +436,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
     const bool opened = open;
     float low = 0.f;
     if (opened) {
-      // The maxima of 32 groups are 32 different values, so the top-th largest of them is no more
-      // than the top-th best of this iteration.
-      float g = mx != mx ? INFINITY : mx;  // (a row with a NaN has no alternatives' values anyway)
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-      if ((lane & 7) == 0) sh.group[tid >> 3] = g;
-      __syncthreads();
-      g = sh.group[lane];
-      int above = 0;  // groups before this one
-#pragma unroll 8
-      for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(0xffffffffu, g, j);
-        above += o > g || (o == g && j < lane);
-      }
-      low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == n_top - 1)) - 1);
-      if (low == INFINITY) low = -INFINITY;
+      low = lp_group_floor(mx, n_top, sh);
       floor = just_below(low);
       open = low == -INFINITY;
     }
@@ -403,34 +459,14 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
         keep(y, head + (i0 + k / E * kLpThreads + tid) * E + k % E);
       }
     }
-    if (opened) {
-      // ids rise with the iterations: what only equals the floor comes behind those that made it
-      floor = low;
-      __syncthreads();
-      const bool many = sh.count > kLpKeys;
-      __syncthreads();
-      if (many) {  // (equal ones): the best `top` of the ids so far
-        lp_rounds(x, rank == 0 ? 0 : head + v0 * E, head + min(v1, i0 + kLpThreads * U) * E, n_top, sh.keys,
-                  sh);
-        if (tid == 0) sh.count = n_top;  // (zeros among them are no candidates)
-        __syncthreads();
-      }
-    }
+    // ids rise with the iterations: what only equals the floor comes behind those that made it
+    if (opened) floor = low;
     if (it >= next_cut && i0 + 3 * kLpThreads * U < v1) {
       next_cut = 4 * it + 3;
       __syncthreads();
-      const int c = sh.count;
-      lost = lost || c > kLpKeys;
-      if (!lost) {
-        lp_select(sh.keys, c, n_top, sh.best, sh);
-        if (tid < n_top) sh.keys[tid] = sh.best[tid];
-        if (tid == 0) sh.count = n_top;
-        if (sh.best[n_top - 1] != 0) {
-          open = false;
-          floor = lp_key_value(sh.best[n_top - 1]);
-        }
-      }
-      __syncthreads();
+      cut(head + min(v1, i0 + kLpThreads * U) * E);
+      open = sh.best[n_top - 1] == 0;
+      if (!open) floor = lp_key_value(sh.best[n_top - 1]);
     }
   }
   cp_async_wait<0>();
@@ -451,18 +487,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
   }
   if (lane == 0) sums.part[warp] = a;
   __syncthreads();
-  if (kTopIds) {
-    lost = lost || sh.count > kLpKeys;
-    if (!lost) {
-      lp_select(sh.keys, sh.count, n_top, sh.best, sh);
-    } else {
-      // More candidates than there was room for (logits that rise with the id): the same over the
-      // whole part.
-      lp_rounds(x, rank == 0 ? 0 : head + v0 * E, rank == C - 1 ? p.vocab : head + v1 * E, n_top, sh.best,
-                sh);
-      __syncthreads();
-    }
-  }
+  if (kTopIds) cut(rank == C - 1 ? p.vocab : head + v1 * E);
   const uint64_t* best = sh.best;
   RowSum r;
   if (warp == 0) r = lp_join(sums.part, kLpWarps);

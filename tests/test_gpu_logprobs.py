@@ -82,6 +82,12 @@ def test_long_rows_of_a_cta_each(top, dtype):
     x = (torch.randn(R, vocab, device="cuda", generator=gen) * 2).to(dtype)
     x[1] = torch.randint(-5, 6, (vocab,), device="cuda", generator=gen).to(dtype)
     x[2] = (torch.arange(vocab, device="cuda") * 2.0 ** -8).to(dtype)
+    x[3] += (torch.arange(vocab, device="cuda") * 2.0 ** -12).to(dtype)
+    x[4, 5000:] += 9
+    x[5] = torch.arange(vocab, device="cuda") // 9000
+    x[6] = -float("inf")
+    x[6, 9000:] = torch.arange(vocab - 9000, device="cuda") % 1000 * 0.01
+    x[7] = 1
     tokens = torch.randint(0, vocab, (R,), device="cuda", generator=gen).to(torch.int32)
     got = run(x, tokens, top)
     check(x[:12], tokens[:12], top, [g[:12] for g in got])
