@@ -10,7 +10,7 @@
 // Bound by memory where rows fill the GPU: 2048 rows of 128,256 in bf16 take 84 us, 6.3 TB/s (92 % of
 // a plain copy's rate).  With 20 alternatives 512 rows of 151,936 in fp32, 384 of them in use, take
 // 42.4 us, 5.5 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
-// time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 20
+// time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 5
 // alternatives take 9.7 us, where their bytes take 1.4.
 #include <cmath>
 

@@ -193,3 +193,37 @@ def test_packed_prompts_from_lengths_to_log_probabilities():
     got = dec[0, 0].double().cpu().numpy()
     # K and V in e4m3 (2^-4 of an element): scores move by about 2^-4 of a standard deviation
     assert np.abs(got - ref[-1]).max() <= 0.25 * mag[-1].max()
+
+
+def test_host_memory_is_refused():
+    """By each call, for each of its arrays, before anything is launched."""
+    c, B, T, V = capi(), 2, 20, 50
+    cuda = dict(device="cuda")
+    ints = lambda *n: torch.zeros(*n, dtype=torch.int32, **cuda)
+    rows = lambda h: torch.zeros(T, h, HD, dtype=torch.bfloat16, **cuda)
+    status = ints(1)
+    pages = c.Pages.empty(4, B, 2, status=status)
+    codes = [torch.zeros(4, 2, PAGE, HD, dtype=torch.uint8, **cuda) for _ in "kv"]
+    exps = [torch.zeros(4, 2, PAGE // 16, dtype=torch.int8, **cuda) for _ in "kv"]
+    cache = c.KvqCache(*codes, *exps, pages.tensors[0], status)
+    calls = [
+        (lambda *a: c.dflash_pages_map(pages, B, T, *a), [ints(B), ints(B), ints(B), ints(B + 1), ints(B)]
+         + [ints(T) for _ in range(3)]),
+        (lambda *a: c.dflash_pages_release(pages, B, *a), [ints(B), ints(B)]),
+        (lambda *a: c.dflash_kvq_append_packed(cache, B, *a), [ints(B), ints(B), ints(B + 1), rows(2), rows(2)]),
+        (lambda *a: c.dflash_prompt_attention(B, True, *a),
+         [ints(B + 1), rows(4), rows(2), rows(2), rows(4), torch.zeros(T, 4, **cuda), ints(1)]),
+        (lambda x, t, *a: c.dflash_token_logprobs(x, t, 2, *a),
+         [torch.zeros(T, V, **cuda), ints(T), torch.zeros(T, **cuda), torch.zeros(T, **cuda), ints(T, 2),
+          torch.zeros(T, 2, **cuda)]),
+        (c.dflash_status_check, [ints(1)]),
+    ]
+    for call, args in calls:
+        for i in range(len(args)):
+            with pytest.raises(c.DFlashError) as e:
+                call(*[a.cpu() if j == i else a for j, a in enumerate(args)])
+            assert e.value.status == 1, (args[i].shape, i)
+    with pytest.raises(c.DFlashError):
+        c.dflash_pages_release(c.Pages.empty(4, B, 2, device="cpu"), B)
+    torch.cuda.synchronize()
+    assert int(status) == 0
