@@ -105,6 +105,17 @@ def test_strides_and_misaligned_rows(pad, dtype):
     check(x, tokens, 9, run(x, tokens, 9))
 
 
+def test_elements_past_32_bits():
+    wide = torch.empty(1100, 2 ** 21 + 3, dtype=torch.bfloat16, device="cuda")
+    assert wide.numel() > 2 ** 31
+    x = wide[:, -5001:]
+    x[1080:] = torch.randn(20, 5001, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0))
+    tokens = torch.full((1100,), -1, dtype=torch.int32, device="cuda")
+    tokens[1080:] = torch.arange(20, device="cuda") * 250
+    got = run(x, tokens, 6)
+    check(x[1070:], tokens[1070:], 6, [g[1070:] for g in got])
+
+
 def patterns(vocab):
     i = torch.arange(vocab, device="cuda").float()
     yield torch.zeros(vocab, device="cuda")                       # all equal

@@ -59,6 +59,19 @@ def test_equals_the_batched_call(heads, lens, old, lead, pad, seqs):
     assert all(torch.equal(s, t) for s, t in zip(pool(a), pool(b)))
 
 
+def test_elements_past_32_bits():
+    x = torch.empty(1100, 2 ** 14, HD, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    x[1000:].normal_(generator=torch.Generator(device="cuda").manual_seed(0))
+    a, b = (filled(2, 2, 2, [3, 70], 1) for _ in range(2))
+    off = i32([1023, 1030, 1100])
+    capi().dflash_kvq_append_packed(a.h, 2, None, i32([3, 70]), off, x[:, 5:7], x[:, -2:])
+    k, v = x[1023:, 5:7].contiguous(), x[1023:, -2:].contiguous()
+    capi().dflash_kvq_append_packed(b.h, 2, None, i32([3, 70]), off - 1023, k, v)
+    capi().dflash_kvq_check(a.h)
+    assert all(torch.equal(s, t) for s, t in zip(pool(a), pool(b)))
+
+
 def test_many_ragged_sequences():
     rng = np.random.default_rng(11)
     B = 70

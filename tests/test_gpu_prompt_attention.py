@@ -116,6 +116,27 @@ def test_long_prompt():
             assert torch.allclose(c.lse[a:e, h].double(), torch.logsumexp(s, -1), rtol=0, atol=1e-4)
 
 
+def test_elements_past_32_bits():
+    hkv, g, off = 8192, 2, [1020, 1021, 1099]
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.empty(1100, hkv * (g + 2), HD, dtype=torch.bfloat16, device="cuda")
+    x[1000:].normal_(generator=gen)
+    q, k, v = x[:, :hkv * g], x[:, hkv * g:-hkv], x[:, -hkv:]
+    out = torch.full((1100, hkv * g, HD), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse, status = torch.full((1100, hkv * g), 7.0, device="cuda"), i32([0])
+    assert out.numel() > 2 ** 31
+    capi().dflash_prompt_attention(2, True, i32(off), q, k, v, out, lse, status)
+    capi().dflash_status_check(status)
+    assert (out[1019] == 7).all() and (out[1099] == 7).all() and (lse[1019] == 7).all()
+    for a, e in zip(off, off[1:]):
+        for h in (0, 9001, hkv * g - 1):
+            f = [t[a:e, i:i + 1].double().cpu().numpy() for t, i in ((q, h), (k, h // g), (v, h // g))]
+            ref, ref_lse, mag = op.attend(*f, True)
+            err = np.abs(out[a:e, h:h + 1].double().cpu().numpy() - ref)
+            assert (err <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * mag).all()
+            np.testing.assert_allclose(lse[a:e, h:h + 1].cpu().numpy(), ref_lse, rtol=0, atol=1e-4)
+
+
 def test_without_lse_and_wide_rows():
     c = Case([77, 140], 2, 4, seed=9, wide=3)
     c.run(True, lse=False)
