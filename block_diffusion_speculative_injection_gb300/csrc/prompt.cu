@@ -516,10 +516,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32_nowait(t_s + 32 * c, s + 32 * c);
         tmem_wait_ld();
         if ((j + 1) * kPT > mask_from) {
-          const int end = limit - j * kPT;
+          const int end = limit - j * kPT, all = __shfl_sync(0xffffffffu, end, 0);  // (rows see more and more)
 #pragma unroll
           for (int c = 0; c < kPT; c += 32) {
             // (bits to predicates eight at a time: half the instructions of a comparison each)
+            if (all >= c + 32) continue;
             const int n = end - c;
             const uint32_t seen = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
@@ -541,7 +542,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float m_next = grown ? top : m;
         float base = m_next == -INFINITY ? 0.f : -m_next * kPScaleLog2;
         const bool far = fabsf(m_next) > kPFar && m_next != -INFINITY;
-        if (__any_sync(0xffffffffu, grown || far)) {
+        // (at the first step there is nothing to rescale, nor this code to be fetched)
+        if (__any_sync(0xffffffffu, (grown && j > 0) || far)) {
           if (j > 0 && __any_sync(0xffffffffu, grown)) {
             // O holds the steps before: S(j) is complete, so they are
             const float alpha = grown ? ex2((m - top) * kPScaleLog2) : 1.f;
