@@ -68,9 +68,12 @@ struct PromptMaps {
 // in a row and two more changes; three short ones 6.7 us, a launch and one step.
 //
 // Measured and left: three stages instead of four (with the room, five) and P in one or four parts
-// (slower); results by separate warps (slower: registers); items known three ahead, and the next
-// CTA asked for three steps early (2048 tokens: 34 us instead of 30); V cleaned by the softmax
-// warps in front of their stores (2 % slower).
+// (slower); results by separate warps (slower: registers), in four parts of 32 dims through two
+// buffers in turn (no gain), their second half behind the next item's first weights (2 % slower);
+// items known three ahead, and the next CTA asked for three steps early (2048 tokens: 34 us instead
+// of 30); V cleaned by the softmax warps in front of their stores (2 % slower); half a step's
+// products and weights left out where the last step has no more than 64 keys (0.4 us less for
+// short prompts, 2 to 5 % more for long ones: the loop's code is scheduled less well).
 // ---------------------------------------------------------------------------
 constexpr int kPT = 128;                       // rows of a query tile, keys of a step
 constexpr uint32_t kPBox = kPT * 128;          // 128 rows of 64 dims
