@@ -60,13 +60,13 @@ struct PromptMaps {
 // scores of the next item begin under the results of the last, and the items, longest first, end
 // together (32 ragged prompts: 1.68 -> 1.38 ms).
 //
-// What bounds it: a step of both tiles is 8.4 MFLOP x 4 = 33.6 MFLOP of products an SM, 1.35 us at
-// 1.89 PFLOP/s over 152 SMs.  Long prompts reach that (four of 8192, bidirectional, 32 heads); one of
-// 16,384 causal tokens takes 1.2 ms, 1.8 PFLOP/s (1.34 ms under the power cap, 96 % of
-// the rate that a large library matrix product sustains there).  Shorter prompts pay 2.6 us for each change of
-// items (the last step's chain, the results, the first scores) and some 0.25 us more for a step
-// with a mask: 32 prompts of 512 to 4096 take 1.22 ms, 1.54 PFLOP/s.  One of 2048 is 28 us, 16 steps
-// in a row and two more changes; three short ones 6.7 us, a launch and one step.
+// What bounds it: a step of both tiles is four products of 4.2 MFLOP, 1.35 us at 1.89 PFLOP/s over
+// 152 SMs.  Long prompts reach that (four of 8192, bidirectional, 32 heads); one of 16,384 causal
+// tokens takes 1.2 ms, 1.8 PFLOP/s (1.34 ms under the power cap, 96 % of the rate that a large
+// library matrix product sustains there).  Shorter prompts pay 2.6 us for each change of items (the
+// last step's chain, the results, the first scores) and some 0.25 us more for a step with a mask: 32
+// prompts of 512 to 4096 take 1.22 ms, 1.54 PFLOP/s.  One of 2048 is 28 us, 16 steps in a row and
+// two more changes; three short ones 6.7 us, a launch and one step.
 //
 // Measured and left: three stages instead of four (with the room, five) and P in one or four parts
 // (slower); results by separate warps (slower: registers), in four parts of 32 dims through two
