@@ -9,9 +9,9 @@
 //
 // Bound by memory where rows fill the GPU: 2048 rows of 128,256 in bf16 take 84 us, 6.3 TB/s (92 % of
 // a plain copy's rate).  With 20 alternatives 512 rows of 151,936 in fp32, 384 of them in use, take
-// 42.4 us, 5.5 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
+// 40.9 us, 5.7 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
 // time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 5
-// alternatives take 9.7 us, where their bytes take 1.4.
+// alternatives take 8.8 us, where their bytes take 1.4.
 #include <cmath>
 
 #include "attn_util.cuh"
@@ -81,7 +81,7 @@ __device__ __forceinline__ float lp_key_value(uint64_t k) {
 // kAtOnce vectors a thread and iteration, kStages iterations' places in shared memory, kCtas CTAs an
 // SM.  152 rows of 151,936 in fp32: 10.2 us with 4 x 3 at 4 CTAs, 11.6 with 2 x 4 at 5, 21.5 with
 // 4 x 2 at 5.  With alternatives fp32 needs the registers of 3 CTAs, and in bf16 the lists leave
-// room for 4 (lists short enough for 5: 512 rows 57 us instead of 49, 2000 rows 143 instead of 148).
+// room for 4, and 63 registers (lists short enough for 5: 512 rows 16 % more, 2000 rows 4 % less).
 template <typename T>
 struct LpVec;
 template <>
@@ -128,6 +128,7 @@ struct alignas(128) LpLists {
   uint64_t warp_best[2][kLpWarps];
   float group[kLpThreads / 8];
   int count, n_short;
+  float floor;
 };
 
 __host__ __device__ constexpr int lp_lists_size(bool top) {
@@ -236,8 +237,8 @@ __device__ __forceinline__ float just_below(float x) {
 }
 
 // The n-th largest of 32 groups' maxima of the threads' values (NaN counts as +inf), -inf for a +inf
-// (a row with a +inf or NaN has no alternatives' values anyway); whole CTA.  The maxima are 32
-// different values, so it is no more than the n-th best of all.
+// (a row with a +inf or NaN has no alternatives' values anyway); whole CTA, one warp ranks.  The
+// maxima are 32 different values, so it is no more than the n-th best of all.
 __device__ __forceinline__ float lp_group_floor(float mx, int n, LpLists& sh) {
   const int tid = threadIdx.x, lane = tid & 31;
   float g = mx != mx ? INFINITY : mx;
@@ -245,15 +246,18 @@ __device__ __forceinline__ float lp_group_floor(float mx, int n, LpLists& sh) {
   for (int o = 4; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
   if ((lane & 7) == 0) sh.group[tid >> 3] = g;
   __syncthreads();
-  g = sh.group[lane];
-  int above = 0;  // groups before this one
+  if (tid < 32) {
+    g = sh.group[lane];
+    int above = 0;  // groups before this one
 #pragma unroll 8
-  for (int j = 0; j < 32; ++j) {
-    const float o = __shfl_sync(0xffffffffu, g, j);
-    above += o > g || (o == g && j < lane);
+    for (int j = 0; j < 32; ++j) {
+      const float o = __shfl_sync(0xffffffffu, g, j);
+      above += o > g || (o == g && j < lane);
+    }
+    if (above == n - 1) sh.floor = g == INFINITY ? -INFINITY : g;
   }
-  const float low = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == n - 1)) - 1);
-  return low == INFINITY ? -INFINITY : low;
+  __syncthreads();
+  return sh.floor;
 }
 
 // The n best of what the list holds become the list, and sh.best; whole CTA.
@@ -267,8 +271,8 @@ __device__ __forceinline__ void lp_cut(int n, LpLists& sh) {
 // The list had no room for all candidates of ids f0 .. f1 - 1 (logits that rise with the id): these
 // ids anew, above the n-th best of the ids before them and above their own groups' floor; if that
 // is too many as well (many equal ones), one after the other.  Whole CTA; then as lp_cut.  (512 rows
-// of 151,936 in fp32, 20 alternatives: 63 us; with logits that are three standard deviations higher
-// from id 9000 on 90, with ascending ones 293.)
+// of 151,936 in fp32, 20 alternatives: 62 us; with logits that are three standard deviations higher
+// from id 9000 on 87, with ascending ones 308.)
 template <typename T>
 __device__ __noinline__ void lp_overflow(const T* x, int f0, int f1, int n, LpLists& sh) {
   const int tid = threadIdx.x;
@@ -303,7 +307,7 @@ __device__ __noinline__ void lp_overflow(const T* x, int f0, int f1, int n, LpLi
 // iterations' loads under way while it works on this one's.  (What it takes: fp32 15 and bf16 9
 // instructions a logit with the shares of everything else.)
 template <typename T, bool kTopIds>
-__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && sizeof(T) == 4 ? 1 : 0))
+__global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds ? 1 : 0))
     token_logprobs_kernel(const LogpK p, const int C) {
   pdl_trigger();
   pdl_wait();
@@ -400,6 +404,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
     cp_async_wait<kStages - 2>();
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = ring[(at * U + u) * kLpThreads];
+    const T* const here = reinterpret_cast<const T*>(ring + at * (U * kLpThreads));
     at = at + 1 == kStages ? 0 : at + 1;
     if (i0 + kLpThreads * U > v1) {
 #pragma unroll
@@ -453,10 +458,7 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds && size
 #pragma unroll 1
       for (; some; some &= some - 1) {
         const int k = __ffs(some) - 1;
-        float y = v[0];
-#pragma unroll
-        for (int i = 1; i < U * E; ++i) y = k == i ? v[i] : y;
-        keep(y, head + (i0 + k / E * kLpThreads + tid) * E + k % E);
+        keep(ld_f(here + k / E * (kLpThreads * E) + k % E), head + (i0 + k / E * kLpThreads + tid) * E + k % E);
       }
     }
     // ids rise with the iterations: what only equals the floor comes behind those that made it
