@@ -572,9 +572,10 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
   p.vocab = vocab;
   p.top = top;
   // A row to several CTAs while there are no more than two an SM, and each has more than an
-  // iteration: 16 rows of 151,936 with 5 alternatives take 9.7 us by 8 CTAs each and 19 by one; 100
-  // rows with 20 take 26 by two and 32 by one.  Beyond that it gains nothing (256 rows: 41.9 us by two,
-  // 41.6 by one) and soon costs, since every CTA makes a selection of its own (512 rows: 66.5, 64.1).
+  // iteration: 16 rows of 151,936 with 5 alternatives take 8.6 us by 8 CTAs each and 17 by one; 100
+  // rows with 20 take 24 by two and 30 by one.  Beyond that it gains little (256 rows: 39 us by two,
+  // 37 by one, without alternatives 27 and 30) and soon costs, since every CTA makes a selection of
+  // its own (512 rows: 62 by one or two, 77 by four).
   int C = 1;
   while (C < kLpCluster && (int64_t)rows * C * 2 <= 2 * kvq_sms() && vocab > C * kLpStep) C *= 2;
   const auto kernel = dtype == DFLASH_F32
