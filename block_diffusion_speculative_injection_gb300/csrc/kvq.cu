@@ -65,9 +65,8 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
   const int lane = threadIdx.x & 31;
   long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int kv = (int)(w & 1);
-  int b, blk, cnt;
-  long long row0;  // the sequence's first row
-  int head;
+  int b, blk, cnt, head;
+  int first = 0;  // the sequence's first row, packed
   if (kPacked) {
     packed_check(p.offsets, p.batch, p.rows, (long long)blockIdx.x * 128 + threadIdx.x,
                  (long long)gridDim.x * 128, p.c.status);
@@ -76,10 +75,8 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
     w /= p.c.Hkv;
     if (w >= p.n_blk) return;
     b = packed_find(p.offsets, p.batch, p.units, w);
-    int first = 0;
     if (b < 0 || !packed_rows(p.offsets, b, p.rows, first, cnt)) return;
     blk = (int)(w - packed_base(p.offsets, b, p.units));
-    row0 = first;
   } else {
     w >>= 1;
     head = (int)(w % p.c.Hkv);
@@ -89,7 +86,6 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
     if (w >= p.batch) return;
     b = (int)w;
     cnt = p.counts ? p.counts[b] : p.rows;
-    row0 = (long long)b * p.rows;
   }
   const int seq = kvq_seq(p.c, p.seq_ids, b);
   const int s0 = p.start[b];
@@ -126,7 +122,7 @@ __global__ void __launch_bounds__(128, 7) kvq_append_kernel(const AppendK p) {
       raw[i].x = c.x;
       raw[i].y = c.y;
     } else if (r < n_live) {
-      const long long row = row0 + (slot0 + r - s0);
+      const long long row = (kPacked ? first : (long long)b * p.rows) + (slot0 + r - s0);
       raw[i] = *reinterpret_cast<const uint4*>(in + row * stride + head * kKvqHd + col);
     }
   }

@@ -15,8 +15,8 @@ namespace dflash {
 // sequences' counts, page ids).  A CTA walks the whole batch, kPer consecutive entries a thread.  For
 // the maps of many rows a cluster of CTAs does so, each for all entries, and shares the rows out; what
 // the call reads and changes is changed after all of them have read it.
-// 256 sequences with a block of 16 rows each, given back and mapped: 7.9 us for both calls (9.3
-// by one CTA, 8.8 by two); 32 prompts of 512 to 4096 rows (79,838 rows, 0.96 MB of maps): 12.4 us, 8
+// 256 sequences with a block of 16 rows each, given back and mapped: 7.8 us for both calls (9.3
+// by one CTA, 8.8 by two); 32 prompts of 512 to 4096 rows (79,838 rows, 0.96 MB of maps): 11.9 us, 8
 // SMs' instructions for the maps' rows.
 constexpr int kMapThreads = 1024, kMapBatch = 4096;
 constexpr int kMapCluster = 8, kMapRows = 1024;  // most CTAs; rows a CTA takes before there is another
@@ -164,7 +164,7 @@ __device__ __forceinline__ int entry_above(const int32_t* end, int batch, int i,
 }
 
 template <int kPer>
-__global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, const int C) {
+__global__ void __launch_bounds__(kMapThreads, 1) pages_map_kernel(const MapK k, const int C) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ int32_t map_smem[];
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kMapThreads) pages_map_kernel(const MapK k, co
 }
 
 template <int kPer>
-__global__ void __launch_bounds__(kMapThreads) pages_release_kernel(const MapK k) {
+__global__ void __launch_bounds__(kMapThreads, 1) pages_release_kernel(const MapK k) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ int32_t map_smem[];
