@@ -188,7 +188,6 @@ struct PromptPast {
 
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptMaps maps, const PromptK p) {
-  pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -220,7 +219,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     mbar_init(&sh.next_full, 1);
     mbar_fence_init();
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
+  // (before there is tensor memory: the kernel before may not hold all of its own yet)
+  pdl_wait();
   if (warp == 8) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -250,11 +254,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const bool leader = elect_one();
     if (warp == 8) {
       // ---- producer: finds the items and loads them
-      if (leader) {
-        tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
-      }
       int issued = 0, cleaned = 0, items = 0, q_loads[2] = {0, 0};
       bool ok = true;
       auto load = [&](const PromptItem& it, bool is_v, int j) -> bool {
