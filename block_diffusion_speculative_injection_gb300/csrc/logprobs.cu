@@ -515,16 +515,18 @@ __global__ void __launch_bounds__(kLpThreads, LpVec<T>::kCtas - (kTopIds ? 1 : 0
   if (warp != 0) return;  // (up to 32 alternatives)
   const bool mass = r.m != -INFINITY;
   const float log_s = logf(r.s);
+  // what has no probability; a NaN (never a candidate) or +inf leaves the row without any numbers
+  const float none = r.m < INFINITY ? -INFINITY : NAN;
   if (tid == 0) {
     if (p.logp && p.tokens)
-      p.logp[row] = tok >= p.vocab || !mass ? -INFINITY : (x_tok - r.m) - log_s;
+      p.logp[row] = tok >= p.vocab || !mass ? none : (x_tok - r.m) - log_s;
     if (p.entropy) p.entropy[row] = mass ? log_s - r.t / r.s : 0.f;
   }
   if (tid < n_top) {
     const uint64_t k = best[tid];
     const long long at = (long long)row * n_top + tid;
     p.top_ids[at] = k ? (int)~(uint32_t)k : -1;
-    p.top_logp[at] = k ? (lp_key_value(k) - r.m) - log_s : -INFINITY;
+    p.top_logp[at] = k ? (lp_key_value(k) - r.m) - log_s : none;
   }
 }
 

@@ -728,8 +728,9 @@ DFLASH_API dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, 
  *   top_ids_dev  [rows][top] int32, top_logp_dev [rows][top] float (NULL with top = 0)
  * Logits of -inf have no probability: they are no alternatives (id -1, log probability
  * -inf where fewer than `top` others are left), and a row of nothing else gives logp
- * -inf and entropy 0.  A row with a NaN or +inf gives NaN for each number, and any
- * ids.  Sums are in fp32, in a fixed order: equal inputs give equal outputs.  rows
+ * -inf and entropy 0.  A row with a NaN or +inf gives NaN for each number, whatever its
+ * token (>= vocab included) and however few alternatives it has, and any ids (-1 or below
+ * vocab).  Sums are in fp32, in a fixed order: equal inputs give equal outputs.  rows
  * 1 .. 2^27 - 1, vocab 1 .. 2^30 - 1, top 0..32; no array written may overlap another
  * or an input. */
 DFLASH_API dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype,

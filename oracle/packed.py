@@ -101,8 +101,11 @@ class Pages:
 
 
 def logprobs(x, token, top):
-    """(log probability, entropy, ids, their log probabilities) of one row."""
+    """(log probability, entropy, ids, their log probabilities) of one row.  A NaN or +inf makes
+    every number NaN (the ids may be any then)."""
     x = np.asarray(x, dtype=np.float64)
+    if not (x < np.inf).all():
+        return np.nan, np.nan, [-1] * top, [np.nan] * top
     alive = np.flatnonzero(x > -np.inf)
     if alive.size == 0:
         return -np.inf, 0.0, [-1] * top, [-np.inf] * top
