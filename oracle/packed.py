@@ -85,10 +85,11 @@ class Pages:
     def release(self, seqs, keep):
         wrong, seen, given = set(), set(), []
         for q, k in zip(seqs, keep):
-            if not 0 <= q < self.n_seqs or q in seen or k < 0:
+            good = 0 <= q < self.n_seqs and q not in seen and k >= 0
+            seen.add(q)
+            if not good:
                 wrong.add("check")
                 continue
-            seen.add(q)
             first = -(-k // PAGE)
             while self.mapped[q] > first:
                 self.mapped[q] -= 1
