@@ -718,7 +718,10 @@ def dflash_prompt_attention(batch, causal, offsets, q, k, v, out, lse=None, stat
                             stream=None) -> None:
     """Attention of a packed batch of prompts over themselves: q [n_rows][n_heads][128],
     k, v [n_rows][n_kv_heads][128] (rows may be slices of wider ones), out of
-    q's shape, lse [n_rows][n_heads], status [1] int32 (zero at the start)."""
+    q's shape, lse [n_rows][n_heads] or None, status [1] int32 (zero at the start; always
+    needed, its default only lets lse be left out)."""
+    if status is None:
+        _kvq_refuse("status: need int32 [1], where bad offsets are reported")
     if q.dim() != 3 or k.dim() != 3:
         _kvq_refuse("q, k: need [n_rows][heads][128]")
     n_rows, heads, _ = rows = q.shape
