@@ -111,6 +111,7 @@ constexpr int kPParts = 2;    // of P: a part's products begin while the next is
 constexpr int kPSlots = 2;    // items known ahead
 constexpr int kPAskLate = 1;  // steps
 constexpr int kPClean = 4;    // barriers of the cleaned tiles, used in turn
+constexpr int kPIdle = 1 << 16;  // empty items after which there is word of them (70 ms; a wait ends after 2 s)
 struct PromptShared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][kPParts], o_full[2], o_empty[2], issued[2], drained[2];
   uint64_t raw_full[kPClean], clean[kPClean];
@@ -318,7 +319,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         packed_check(p.offsets, p.batch, p.n_rows, 32ll * index + lane, 1ll << 40, status);
         PromptItem it;
-        const bool any = prompt_item(p, index, it) && publish(it);
+        bool any = prompt_item(p, index, it);
+        if (!any && asked % kPIdle == kPIdle - 1) {  // so that the others' waits do not run out
+          memset(&it, 0, sizeof(it));
+          it.n = 1;  // (an item without steps)
+          any = true;
+        }
+        any = any && publish(it);
         const int n = any ? max(it.steps_a, it.steps_b) : 0;
         // The next item is asked for while the last steps' loads are under way; with few steps
         // there is no time for that, and little to share out better.

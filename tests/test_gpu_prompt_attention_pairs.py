@@ -256,3 +256,21 @@ def test_captured_with_other_lengths_beside_another_stream():
         c.run(True)
         assert torch.equal(c.out[:c.off[-1]], outs[0][:c.off[-1]])
         c.check(True)
+
+
+def test_millions_of_empty_prompts():
+    """Two prompts with 2^26 - 3 empty ones between: 3.5 million empty items in a row for each CTA, for
+    longer than a wait within the kernel may take."""
+    B, hkv, lens = (1 << 26) - 1, 8, (100, 60)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(160, 3 * hkv, HD, device="cuda", generator=gen).to(torch.bfloat16)
+    q, k, v = x[:, :hkv], x[:, hkv:2 * hkv], x[:, 2 * hkv:]
+    off = torch.full((B + 1,), lens[0], dtype=torch.int32, device="cuda")
+    off[0], off[B] = 0, 160
+    out, few = (torch.zeros(160, hkv, HD, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    status = i32([0])
+    capi().dflash_prompt_attention(B, True, off, q, k, v, out, None, status)
+    capi().dflash_status_check(status)
+    capi().dflash_prompt_attention(2, True, i32([0, 100, 160]), q, k, v, few, None, status)
+    capi().dflash_status_check(status)
+    assert torch.equal(out, few)
