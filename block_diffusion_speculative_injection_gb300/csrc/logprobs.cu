@@ -9,9 +9,10 @@
 //
 // Bound by memory where rows fill the GPU: 2048 rows of 128,256 in bf16 take 84 us, 6.3 TB/s (92 % of
 // a plain copy's rate).  With 20 alternatives 512 rows of 151,936 in fp32, 384 of them in use, take
-// 40.9 us, 5.7 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
+// 40.6 us, 5.7 TB/s: the rest is the selection, whose barriers all CTAs reach at about the same
 // time, so that the memory idles meanwhile.  Few rows are bound by latency: 16 such rows with 5
-// alternatives take 8.8 us, where their bytes take 1.4.
+// alternatives take 9.1 us, where their bytes take 1.4.  (Times in this file are from memory: calls in
+// a graph whose inputs rotate through 1.2 GB.)
 #include <cmath>
 
 #include "attn_util.cuh"
@@ -79,9 +80,11 @@ __device__ __forceinline__ float lp_key_value(uint64_t k) {
 
 // 16 bytes of logits: the values, the largest (NaN passes), and a word of -inf.
 // kAtOnce vectors a thread and iteration, kStages iterations' places in shared memory, kCtas CTAs an
-// SM.  152 rows of 151,936 in fp32: 10.2 us with 4 x 3 at 4 CTAs, 11.6 with 2 x 4 at 5, 21.5 with
-// 4 x 2 at 5.  With alternatives fp32 needs the registers of 3 CTAs, and in bf16 the lists leave
-// room for 4, and 63 registers (lists short enough for 5: 512 rows 16 % more, 2000 rows 4 % less).
+// SM.  152 rows of 151,936 in fp32: 16.6 us with 4 x 3 at 4 CTAs, 22.4 with 2 x 4 at 5, 20.7 with 4 x 2 at 5
+// (what is in L2 already: 10.3, 12, 20.2; 512 rows: 48.8, 50.4, 48.7).  With alternatives fp32 needs the
+// registers of 3 CTAs (20 of them, 384 of 512 rows in use: 40.6 us, with 4 CTAs of 4 x 2 48.5; but all
+// 512 rows 62.3 and 52.7), and in bf16 the lists leave room for 4, and 63 registers (lists short enough
+// for 5: 512 rows of 128,256 42.8 -> 51.3 us, 2000 rows 131.2 -> 130.2).
 template <typename T>
 struct LpVec;
 template <>
@@ -574,10 +577,11 @@ dflash_status dflash_token_logprobs(int32_t rows, int32_t vocab, int32_t dtype, 
   p.vocab = vocab;
   p.top = top;
   // A row to several CTAs while there are no more than two an SM, and each has more than an
-  // iteration: 16 rows of 151,936 with 5 alternatives take 8.6 us by 8 CTAs each and 17 by one; 100
-  // rows with 20 take 24 by two and 30 by one.  Beyond that it gains little (256 rows: 39 us by two,
-  // 37 by one, without alternatives 27 and 30) and soon costs, since every CTA makes a selection of
-  // its own (512 rows: 62 by one or two, 77 by four).
+  // iteration: 16 rows of 151,936 with 5 alternatives take 9.1 us by 8 CTAs each, 10.9 by four and 19 by
+  // one; 100 rows with 20 take 24.5 by two and 30 by one (and 19 by four: the rule is not the best there;
+  // without alternatives two and four are equal, and 152 rows take 16.6 and 20.5).  Beyond that it gains
+  // little (256 rows: 39 us by two, 37 by one, without alternatives 27 and 30) and soon costs, since every
+  // CTA makes a selection of its own (512 rows: 62 by one or two, 77 by four).
   int C = 1;
   while (C < kLpCluster && (int64_t)rows * C * 2 <= 2 * kvq_sms() && vocab > C * kLpStep) C *= 2;
   const auto kernel = dtype == DFLASH_F32

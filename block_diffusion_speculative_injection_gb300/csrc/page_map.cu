@@ -17,7 +17,9 @@ namespace dflash {
 // the call reads and changes is changed after all of them have read it.
 // 256 sequences with a block of 16 rows each, given back and mapped: 7.8 us for both calls (9.3
 // by one CTA, 8.8 by two); 32 prompts of 512 to 4096 rows (79,838 rows, 0.96 MB of maps): 11.9 us, 8
-// SMs' instructions for the maps' rows.
+// SMs' instructions for the maps' rows.  No more CTAs than a cluster has, because what they read (counts,
+// table, free list) may change only after all have read it, and a cluster has that barrier without a second
+// launch: right for the steps of a server, dear for very many rows (4096 sequences of 200: 76 us, bytes 1.5).
 constexpr int kMapThreads = 1024, kMapBatch = 4096;
 constexpr int kMapCluster = 8, kMapRows = 1024;  // most CTAs; rows a CTA takes before there is another
 constexpr int kMapRuns = 4;                      // rows a thread has under way

@@ -57,16 +57,21 @@ struct PromptMaps {
 // then S(j + 1), so that S(j + 1) follows the last read of P(j), which it overwrites.  Warp 11: V.
 //
 // A CTA that is done with its two tiles takes on those of one that has not started, so that loads and
-// scores of the next item begin under the results of the last, and the items, longest first, end
-// together (32 ragged prompts: 1.68 -> 1.38 ms).
+// scores of the next item begin under the results of the last, and SMs that had short items take more
+// (32 ragged prompts: 1.68 -> 1.38 ms).  Items go from the last rows of the packed batch to the first: the
+// long ones of a causal prompt before its short ones, but the prompts just as the caller has them, the last
+// one first.  A batch of 8192 tokens and 64 times 256 takes 387 us with the longest prompt first or last,
+// bidirectional (equally long items) 668 with it first and 651 with it last; 4096 and 200 times 128 take
+// 183, and 260 and 236.
 //
 // What bounds it: a step of both tiles is four products of 4.2 MFLOP, 1.35 us at 1.89 PFLOP/s over
-// 152 SMs.  Long prompts reach that (four of 8192, bidirectional, 32 heads); one of 16,384 causal
-// tokens takes 1.2 ms, 1.8 PFLOP/s (1.34 ms under the power cap, 96 % of the rate that a large
+// 152 SMs.  Long prompts reach that (four of 8192, bidirectional, 32 heads: 2.33 ms); one of 16,384
+// causal tokens takes 1.2 ms, 1.8 PFLOP/s (1.34 ms under the power cap, 96 % of the rate that a large
 // library matrix product sustains there).  Shorter prompts pay 2.6 us for each change of items (the
 // last step's chain, the results, the first scores) and some 0.25 us more for a step with a mask: 32
-// prompts of 512 to 4096 take 1.22 ms, 1.54 PFLOP/s.  One of 2048 is 28 us, 16 steps in a row and
-// two more changes; three short ones 6.7 us, a launch and one step.
+// prompts of 512 to 4096 take 1.22 ms, 1.54 PFLOP/s.  One of 2048 is 28.5 us with its inputs in L2, as the
+// projection before leaves them, and 31.2 from memory: 16 steps in a row and two more changes; three
+// short ones 7.1 us, a launch and one step.
 //
 // Measured and left: three stages instead of four (with the room, five) and P in one or four parts
 // (slower); results by separate warps (slower: registers), in four parts of 32 dims through two
@@ -128,7 +133,7 @@ static_assert(sizeof(PromptShared) <= 768, "barriers fit");
 __device__ __forceinline__ bool prompt_item(const PromptK& p, int index, PromptItem& it) {
   const int from_end = (int)((uint32_t)index / (uint32_t)p.Hkv);
   it.kvh = index - from_end * p.Hkv;
-  // the last positions first: they take longest
+  // the last rows first: in a causal prompt they take longest
   const int u = p.n_units - 1 - from_end;
   const int b = packed_find(p.offsets, p.batch, p.units, u);
   if (b < 0 || !packed_rows(p.offsets, b, p.n_rows, it.first, it.n)) return false;
@@ -765,8 +770,8 @@ dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_h
   p.g_inv = 65536 / p.G + 1;
   p.box_out = 32 % p.G == 0;
   // Two query tiles a CTA, each beside the other's softmax; one while that leaves no SM two CTAs.  32
-  // and 8 heads, one prompt of 256: 7.4 us by one tile, 8.3 by two; 512: 10.7 and 11.1; 1024:
-  // 19.5 and 16.9, bidirectional 26.7 and 16.9.
+  // and 8 heads, inputs in L2, one prompt of 256: 7.4 us by one tile, 8.3 by two; 512: 10.7 and 11.1;
+  // 1024: 19.5 and 16.9, bidirectional 26.7 and 16.9.
   p.tiles = 2 * packed_units(n_rows, batch, 2 * p.pos, 1) * n_kv_heads <= kvq_sms() ? 1 : 2;
   const int64_t units = packed_units(n_rows, batch, p.tiles * p.pos, 1);
   if (units * n_kv_heads >= ((int64_t)1 << 31)) return DFLASH_E_INVALID_ARG;

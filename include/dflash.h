@@ -693,8 +693,10 @@ DFLASH_API dflash_status dflash_kvq_append_packed(const dflash_kvq_cache *cache,
  *   out = sum_k p_k v_k,  p = softmax over its keys of q_i . k_k / sqrt(128),
  * its keys being rows 0 .. i of the prompt (causal = 1) or all n (causal = 0).  bf16,
  * head_dim 128; n_heads / n_kv_heads 1..64.
+ * Keys are rows of the call: slots that a cache holds already are not among them.
  * Scores, sums of weights and the accumulated output are in fp32; a weight is rounded to
- * bf16 where it meets V, and the result is.  Rows that a row does not see do not enter
+ * bf16 where it meets V, and the result is, so that beside the scores' own rounding out is off
+ * by 2^-8 |out| + 2^-8 sum_k p_k |v_k| at most.  Rows that a row does not see do not enter
  * its result, NaN included; an infinity or NaN in a V row it does see makes that element
  * of its result an infinity or NaN, whatever the weight.
  *   q_dev        [n_rows] rows of n_heads * 128, q_row_stride elements apart (>= n_heads
@@ -706,7 +708,8 @@ DFLASH_API dflash_status dflash_kvq_append_packed(const dflash_kvq_cache *cache,
  *                sqrt(128)) (what dflash_kvq_score takes)
  *   status_dev   one int32
  * batch 1 .. 2^26 - 1, n_rows 1 .. 2^26 - 1, n_heads up to 65535.  out and lse must not
- * overlap the inputs or each other. */
+ * overlap the inputs or each other.  Without a mask, a prompt much longer than the others is
+ * served best as the last of the batch (3 to 9 % less time than as the first). */
 DFLASH_API dflash_status dflash_prompt_attention(int32_t batch, int32_t n_rows, int32_t n_heads,
                                                  int32_t n_kv_heads, int32_t causal,
                                                  const int32_t *offsets_dev, const void *q_dev,
